@@ -46,7 +46,7 @@ typedef enum {
   AWQ_ERR_WORKSPACE = 3,   /* workspace smaller than the matching *_workspace_size() */
   AWQ_ERR_NONFINITE = 4,   /* a candidate loss was NaN or infinite (device-side) */
   AWQ_ERR_CUDA = 5,        /* a CUDA runtime call or launch failed */
-  AWQ_ERR_DEVICE = 6,      /* a kernel gave up a bounded wait (device-side) */
+  AWQ_ERR_DEVICE = 6,      /* a kernel gave up a bounded wait or refused a device-side index (device-side) */
   AWQ_ERR_UNSUPPORTED = 7, /* no sm_100 device, or a configuration not built */
   AWQ_ERR_BOUNDS = 8       /* debug build: an index check failed (awq_bounds_error) */
 } awq_status;
@@ -296,6 +296,120 @@ size_t awq_w4a16_workspace_size(int64_t N, int64_t d_out, int64_t d_in, const aw
 awq_status awq_w4a16_gemm(const void* X, awq_dtype dtype, const uint32_t* qweight, const void* scales_f16,
                           const void* zeros_f16, int64_t N, int64_t d_out, int64_t d_in, const awq_qcfg* cfg,
                           void* Y, void* ws, size_t ws_bytes, awq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit integer linear layer: weights and activations in 8 bits, one step per
+ * output channel and one per token, beside the W4A16 product. The scales s of
+ * the search serve it as well: W S is quantised once, X S^-1 per call.
+ * ------------------------------------------------------------------------- */
+/* How awq_quantize_int8 applies s. */
+typedef enum awq_scale_mode { AWQ_SCALE_NONE = 0, AWQ_SCALE_MUL = 1, AWQ_SCALE_DIV = 2 } awq_scale_mode;
+
+/* Symmetric 8-bit quantiser, one step per row (a row is an output channel of
+ * W or a token of X):
+ *   v_i = x_i (NONE), x_i * s_i (MUL: weights, W S) or x_i * (1 / s_i) (DIV: activations, X S^-1)
+ *   top = max(max_i |v_i|, 1e-8),  step = top / 127,  q_i = rne(v_i * (127 / top))
+ * each operation one fp32 rounding, quotients correctly rounded: the codes
+ * depend on the inputs alone. A row that holds NaN or infinity (after the
+ * scaling) gets step NaN and codes 0.
+ * x: DEVICE bf16 or fp16 (dtype) [rows, d_in], rows ldx elements apart (ldx a
+ * multiple of 8, ldx >= d_in), 16-byte aligned; s: DEVICE float [d_in],
+ * 16-byte aligned (ignored for NONE); q: DEVICE int8 [rows, d_in], 16-byte
+ * aligned; step: DEVICE float [rows]. Errors: AWQ_ERR_INVALID_ARG
+ * (null/misaligned, bad dtype or mode), AWQ_ERR_SHAPE (rows < 1, d_in < 16,
+ * d_in % 16, d_in > 131072, ldx). Asynchronous. */
+awq_status awq_quantize_int8(const void* x, awq_dtype dtype, int64_t ldx, const float* s, awq_scale_mode mode,
+                             int64_t rows, int64_t d_in, int8_t* q, float* step, awq_stream_t stream);
+
+/* The product of two such operands:
+ *   Y[t, o] = (sum_i xq[t, i] wq[o, i]) * x_step[t] * w_step[o] (+ bias[o])
+ * The sum is exact in int32 (d_in <= 131072); it is converted to fp32,
+ * multiplied by x_step, by w_step, the bias is added, each with one fp32
+ * rounding, and Y is rounded once to its type (dtype). The result does not
+ * depend on how the sum is split.
+ * xq: DEVICE int8 [N, d_in], wq: DEVICE int8 [d_out, d_in], both 16-byte
+ * aligned; x_step: float [N]; w_step: float [d_out]; bias: float [d_out] or
+ * NULL; Y: DEVICE [N, d_out] bf16 or fp16, 16-byte aligned. d_in a multiple of
+ * 16, at most 131072 (AWQ_ERR_SHAPE). ws: awq_w8a8_workspace_size bytes (error
+ * word, and int32 partials where few tiles are split between CTAs).
+ * Asynchronous; device-side errors land in the workspace. */
+size_t awq_w8a8_workspace_size(int64_t N, int64_t d_out, int64_t d_in);
+awq_status awq_w8a8_gemm(const int8_t* xq, const float* x_step, const int8_t* wq, const float* w_step,
+                         const float* bias, awq_dtype dtype, int64_t N, int64_t d_out, int64_t d_in, void* Y, void* ws,
+                         size_t ws_bytes, awq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A key/value cache held in 4 bits, in pages, and the attention that reads it.
+ * ------------------------------------------------------------------------- */
+/* Shape of a cache. Quantisation groups are `group` consecutive channels of
+ * one (token, kv head). */
+typedef struct {
+  int32_t n_kv_heads; /* 1 .. 1024 */
+  int32_t head_dim;   /* 64, 96, 128 or 256 */
+  int32_t page_size;  /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int32_t group;      /* 32, 64 or 128, head_dim % group == 0 */
+} awq_kv4cfg;
+
+/* Bytes of one (page, kv head): page_size * (head_dim + 8 head_dim / group).
+ * A cache is DEVICE [n_pages, n_kv_heads, awq_kv4_page_bytes], 16-byte
+ * aligned, n_pages * page_size < 2^31. Each (page, head) is page_size / 16
+ * strips of 16 tokens; with D = head_dim, a strip holds, in bytes:
+ *   keys    [16 tokens][4 q][D/32 j][4 b]   channel 8 (4 j + q) + 2 b + n in nibble n of the byte
+ *   values  [D/32 p][8 r][4 q][2 h][4 b]    token 2 q + (b >> 1) + 8 (b & 1), channel 32 p + 16 n + 8 h + r in nibble n
+ *   key parameters, then value parameters   [D/group][16 tokens] of (fp16 step, fp16 zero)
+ * and a code stands for (code - zero) * step. 0 for an invalid cfg. */
+size_t awq_kv4_page_bytes(const awq_kv4cfg* cfg);
+
+/* Write T tokens' keys and values. Quantiser of a group (the asymmetric
+ * quantiser above with a range that always holds 0 and the stored step):
+ *   lo = min(0, min v), hi = max(0, max v), step = fp16((hi - lo) / 15) kept in [2^-24, 65504],
+ *   inv = 1 / step, zero = rne(-lo * inv), code = clamp(rne(v * inv) + zero, 0, 15)
+ * in fp32, one rounding an operation. A group that holds NaN or infinity gets
+ * step NaN. k, v: DEVICE bf16 or fp16, element (t, h, d) at t * tok_stride +
+ * h * head_stride + d (strides in elements, multiples of 8; k and v 16-byte
+ * aligned), so slices of a fused projection are read in place. slots: DEVICE
+ * int32 [T]: page * page_size + position; a slot outside the cache (for
+ * example -1) is skipped. No other token's bytes are touched. The slots of a
+ * call must differ (tokens that share one leave a mixture of themselves
+ * there). T = 0 is AWQ_OK. Asynchronous. */
+awq_status awq_kv4_append(const void* k, const void* v, awq_dtype dtype, int64_t T, int64_t k_tok_stride,
+                          int64_t k_head_stride, int64_t v_tok_stride, int64_t v_head_stride, const int32_t* slots,
+                          void* cache, int64_t n_pages, const awq_kv4cfg* cfg, awq_stream_t stream);
+
+/* Read T tokens back: (code - zero) * step, rounded once to bf16 or fp16.
+ * slots as above (they may repeat); a slot outside the cache gives zeros.
+ * k, v: DEVICE [T, n_kv_heads, head_dim], 16-byte aligned; either may be NULL.
+ * Asynchronous. */
+awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const int32_t* slots, int64_t T, const awq_kv4cfg* cfg,
+                          void* k, void* v, awq_dtype dtype, awq_stream_t stream);
+
+/* Attention of new tokens over the cache (which holds their own keys and
+ * values already):
+ *   out[t, e] = sum_i softmax_i(scale * q[t, e] . k_i) v_i,  kv head e / (n_q_heads / n_kv_heads)
+ * Sequence b has q's rows q_start[b] .. q_start[b + 1] - 1 (q_start: DEVICE
+ * int32 [batch + 1], not decreasing; NULL: one row a sequence) and a context
+ * of lens[b] tokens (DEVICE int32 [batch]), its token i in page
+ * table[b, i / page_size] (DEVICE int32 [batch, table_pages]). Its rows are
+ * the last tokens of the context: row j of n sees the first lens[b] - n + 1 + j
+ * tokens. A row that sees none gives zeros (lse -inf). Rows of q that belong
+ * to no sequence are neither read nor written.
+ * q: DEVICE bf16 or fp16 [T, n_q_heads, head_dim] with the given strides
+ * (elements, multiples of 8, 16-byte aligned base); out: [T, n_q_heads,
+ * head_dim] contiguous in q's type, 16-byte aligned; lse: DEVICE float
+ * [T, n_q_heads] or NULL: the natural logarithm of the sum of exponentials.
+ * max_q: at least every sequence's number of rows (host value; it chooses the
+ * kernel). Scores, softmax statistics and output sums are fp32; the weights
+ * (probability times value step) enter the tensor cores in fp16.
+ * Tokens in pages outside [0, n_pages) are left out, lengths are cut to
+ * table_pages * page_size, and rows to max_q and T; any of these makes
+ * awq_workspace_error report AWQ_ERR_DEVICE.
+ * ws: awq_kv4_attention_workspace_size bytes. Asynchronous. */
+size_t awq_kv4_attention_workspace_size(int64_t batch, int64_t n_q_heads, int64_t max_q, const awq_kv4cfg* cfg);
+awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t q_tok_stride, int64_t q_head_stride, int64_t T,
+                             int64_t n_q_heads, const int32_t* q_start, int64_t max_q, const void* cache,
+                             int64_t n_pages, const int32_t* table, int64_t table_pages, const int32_t* lens,
+                             int64_t batch, float scale, const awq_kv4cfg* cfg, void* out, float* lse, void* ws,
+                             size_t ws_bytes, awq_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * The search, one step at a time (awq_search_scales is exactly these calls

@@ -38,6 +38,8 @@ EXPORTED = (
     "awq_quantize_pack_group_clip", "awq_fold_inv_scales", "awq_w4a16_workspace_size", "awq_w4a16_gemm",
     "awq_pack_workspace_size", "awq_quantize_pack_ws", "awq_selftest_bounded_wait",
     "awq_bounds_checks_enabled", "awq_bounds_error", "awq_selftest_bounds",
+    "awq_quantize_int8", "awq_w8a8_workspace_size", "awq_w8a8_gemm", "awq_kv4_page_bytes", "awq_kv4_append",
+    "awq_kv4_gather", "awq_kv4_attention_workspace_size", "awq_kv4_attention",
 )
 
 
@@ -61,6 +63,18 @@ def make_cfg(bits=4, group=128, symmetric=False, n_alpha=20, form="auto", eps_a=
         cfg.alphas = ctypes.cast(arr, POINTER(c_float))
         cfg._keep = arr  # keep the host array alive with the struct
     return cfg
+
+
+class Kv4Cfg(ctypes.Structure):
+    """Shape of a 4-bit key/value cache (awq_kv4cfg)."""
+    _fields_ = [("n_kv_heads", c_int32), ("head_dim", c_int32), ("page_size", c_int32), ("group", c_int32)]
+
+
+def make_kv4(n_kv_heads, head_dim, page_size=64, group=None) -> Kv4Cfg:
+    """group=None: the widest one that divides head_dim."""
+    if group is None:
+        group = next((g for g in (128, 64, 32) if head_dim % g == 0), 0)
+    return Kv4Cfg(int(n_kv_heads), int(head_dim), int(page_size), int(group))
 
 
 _libs = {}
@@ -133,6 +147,23 @@ def lib() -> ctypes.CDLL:
                                           c_void_p, c_void_p, c_void_p]),
             "awq_debug_copy_dw": (c_int32, [c_void_p, c_int64, c_int64, c_int64, cfgp, c_int32, c_void_p,
                                             c_void_p]),
+        }
+        kvp = POINTER(Kv4Cfg)
+        sig |= {
+            "awq_quantize_int8": (c_int32, [c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int64, c_int64, c_void_p,
+                                            c_void_p, c_void_p]),
+            "awq_w8a8_workspace_size": (c_size_t, [c_int64, c_int64, c_int64]),
+            "awq_w8a8_gemm": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64,
+                                        c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
+            "awq_kv4_page_bytes": (c_size_t, [kvp]),
+            "awq_kv4_append": (c_int32, [c_void_p, c_void_p, c_int32, c_int64, c_int64, c_int64, c_int64, c_int64,
+                                         c_void_p, c_void_p, c_int64, kvp, c_void_p]),
+            "awq_kv4_gather": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, kvp, c_void_p, c_void_p, c_int32,
+                                         c_void_p]),
+            "awq_kv4_attention_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, kvp]),
+            "awq_kv4_attention": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_int64, c_void_p, c_int64,
+                                            c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_float, kvp,
+                                            c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -398,6 +429,203 @@ def w4a16_gemm(Xp, qweight, scales, zeros, cfg: QCfg, ws=None, out=None):
     _check(lib().awq_w4a16_gemm(_ptr(Xp), dt, _ptr(qweight), _ptr(scales), _ptr(zeros), N, d_out, d_in,
                                 ctypes.byref(cfg), _ptr(out), _ptr(ws), ws.numel(), _stream()), "awq_w4a16_gemm")
     return out
+
+
+def _req_here(t, dtype, shape, name):
+    """A contiguous CUDA tensor of the current device (calls run on its current stream)."""
+    _req(t, dtype, shape, name)
+    _same_device(t, name)
+
+
+def _same_device(t, name):
+    here = _torch().cuda.current_device()
+    if t.device.index != here:
+        raise ValueError(f"{name} must be on the current device cuda:{here}, got {t.device}")
+
+
+def _req_rows(t, shape, name):
+    """A CUDA tensor of the current device whose last axis is contiguous; the others may be strided."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    _same_device(t, name)
+
+
+# --------------------------------------------------------------------------- 8-bit integer linear layer
+def quantize_int8(X, s=None, inverse=False, outputs=None):
+    """Codes int8 [rows, d_in] and steps float32 [rows] of the symmetric 8-bit
+    quantiser, one step per row, of X (bf16 or fp16 [rows, d_in]; rows may be
+    strided). s (float32 [d_in]): the channels are multiplied by it first (a
+    weight: W S) or, with inverse=True, by 1 / s (activations: X S^-1); without
+    it X is taken as it is."""
+    torch = _torch()
+    dt = _dtype_code(X, "X")
+    _req_rows(X, (None, None), "X")
+    rows, d_in = X.shape
+    mode = 0
+    if s is not None:
+        _req_here(s, torch.float32, (d_in,), "s")
+        mode = 2 if inverse else 1
+    if outputs is None:
+        q = torch.empty((rows, d_in), dtype=torch.int8, device=X.device)
+        step = torch.empty(rows, dtype=torch.float32, device=X.device)
+    else:
+        q, step = outputs
+        _req_here(q, torch.int8, (rows, d_in), "q")
+        _req_here(step, torch.float32, (rows,), "step")
+    _check(lib().awq_quantize_int8(X.data_ptr(), dt, X.stride(0) if rows > 1 else max(d_in, 8), _ptr(s), mode, rows,
+                                   d_in, q.data_ptr(), step.data_ptr(), _stream()), "awq_quantize_int8")
+    return q, step
+
+
+def w8a8_workspace_size(N, d_out, d_in) -> int:
+    return int(lib().awq_w8a8_workspace_size(N, d_out, d_in))
+
+
+def w8a8_gemm(xq, x_step, wq, w_step, dtype=None, bias=None, ws=None, out=None):
+    """Y [N, d_out] (dtype bf16 by default, or fp16) = (xq wq^T) * x_step[:, None]
+    * w_step (+ bias, float32 [d_out]), the integer sum exact; xq int8 [N, d_in]
+    and wq int8 [d_out, d_in] with their steps from quantize_int8."""
+    torch = _torch()
+    _req_here(xq, torch.int8, None, "xq")
+    _req_here(wq, torch.int8, None, "wq")
+    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
+        raise ValueError("xq must be [N, d_in] and wq [d_out, d_in]")
+    N, d_in = xq.shape
+    d_out = wq.shape[0]
+    _req_here(x_step, torch.float32, (N,), "x_step")
+    _req_here(w_step, torch.float32, (d_out,), "w_step")
+    if bias is not None:
+        _req_here(bias, torch.float32, (d_out,), "bias")
+    if out is None:
+        out = torch.empty((N, d_out), dtype=dtype or torch.bfloat16, device=xq.device)
+    else:
+        _req_here(out, dtype or out.dtype, (N, d_out), "out")
+    dt = _dtype_code(out, "out")
+    if ws is None:
+        ws = workspace(w8a8_workspace_size(N, d_out, d_in))
+    else:
+        _same_device(ws, "ws")
+    _check(lib().awq_w8a8_gemm(xq.data_ptr(), x_step.data_ptr(), wq.data_ptr(), w_step.data_ptr(), _ptr(bias), dt, N,
+                               d_out, d_in, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream()),
+           "awq_w8a8_gemm")
+    return out
+
+
+# --------------------------------------------------------------------------- 4-bit key/value cache
+def kv4_page_bytes(cfg: Kv4Cfg) -> int:
+    """Bytes of one (page, kv head) of a cache (0: invalid cfg)."""
+    return int(lib().awq_kv4_page_bytes(ctypes.byref(cfg)))
+
+
+def kv4_new_cache(n_pages, cfg: Kv4Cfg):
+    """An empty cache: int32 zeros [n_pages, n_kv_heads, page words]."""
+    nbytes = kv4_page_bytes(cfg)
+    if not nbytes:
+        raise AwqError(1, "kv4_new_cache")
+    return _torch().zeros((n_pages, cfg.n_kv_heads, nbytes // 4), dtype=_torch().int32, device="cuda")
+
+
+def _req_cache(cache, cfg):
+    torch = _torch()
+    _req_here(cache, torch.int32, None, "cache")
+    words = kv4_page_bytes(cfg) // 4
+    if cache.dim() != 3 or (words and tuple(cache.shape[1:]) != (cfg.n_kv_heads, words)):
+        raise ValueError(f"cache must be [n_pages, {cfg.n_kv_heads}, {words}], got {tuple(cache.shape)}")
+
+
+def kv4_append(k, v, slots, cache, cfg: Kv4Cfg):
+    """Write the keys and values k, v (bf16 or fp16 [T, n_kv_heads, head_dim],
+    tokens and heads may be strided) of T tokens to their slots (int32 [T]: page
+    * page_size + position; outside the cache: skipped) of the cache, in place."""
+    torch = _torch()
+    dt = _dtype_code(k, "k")
+    T = k.shape[0] if k.dim() else 0
+    for t, name in ((k, "k"), (v, "v")):
+        _req_rows(t, (T, cfg.n_kv_heads, cfg.head_dim), name)
+    if v.dtype != k.dtype:
+        raise ValueError("k and v must have one dtype")
+    _req_here(slots, torch.int32, (T,), "slots")
+    _req_cache(cache, cfg)
+    _check(lib().awq_kv4_append(k.data_ptr(), v.data_ptr(), dt, T, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                                slots.data_ptr(), cache.data_ptr(), cache.shape[0], ctypes.byref(cfg), _stream()),
+           "awq_kv4_append")
+    return cache
+
+
+def kv4_gather(cache, slots, cfg: Kv4Cfg, dtype=None, outputs=None):
+    """Keys and values [T, n_kv_heads, head_dim] (bf16 by default, or fp16) that
+    the cache holds for the T slots; a slot outside the cache reads as zeros."""
+    torch = _torch()
+    _req_cache(cache, cfg)
+    _req_here(slots, torch.int32, None, "slots")
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    shape = (slots.shape[0], cfg.n_kv_heads, cfg.head_dim)
+    if outputs is None:
+        outputs = tuple(torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.device) for _ in range(2))
+    else:
+        for t, name in zip(outputs, ("k", "v")):
+            _req_here(t, dtype or outputs[0].dtype, shape, name)
+    k, v = outputs
+    _check(lib().awq_kv4_gather(cache.data_ptr(), cache.shape[0], slots.data_ptr(), shape[0], ctypes.byref(cfg),
+                                k.data_ptr(), v.data_ptr(), _dtype_code(k, "k"), _stream()), "awq_kv4_gather")
+    return k, v
+
+
+def kv4_attention_workspace_size(batch, n_q_heads, max_q, cfg: Kv4Cfg) -> int:
+    return int(lib().awq_kv4_attention_workspace_size(batch, n_q_heads, max_q, ctypes.byref(cfg)))
+
+
+def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, scale=None, lse=False, ws=None,
+                  out=None):
+    """Attention of q (bf16 or fp16 [T, n_q_heads, head_dim], tokens and heads
+    may be strided) over the cache: sequence b's context is lens[b] tokens
+    (int32 [batch]) in the pages table[b] (int32 [batch, table_pages]), its
+    queries the rows q_start[b] .. q_start[b+1] - 1 (int32 [batch + 1], with
+    max_q at least the longest; default: one row a sequence), the last tokens of
+    that context. scale: default 1 / sqrt(head_dim). Returns out [T, n_q_heads,
+    head_dim], or (out, lse float32 [T, n_q_heads]) with lse=True. Rows of no
+    sequence are left as they were (unset in a fresh output)."""
+    torch = _torch()
+    dt = _dtype_code(q, "q")
+    _req_rows(q, (None, None, cfg.head_dim), "q")
+    T, n_q_heads, D = q.shape
+    _req_cache(cache, cfg)
+    _req_here(lens, torch.int32, None, "lens")
+    _req_here(table, torch.int32, None, "table")
+    batch = lens.shape[0] if lens.dim() == 1 else -1
+    if batch < 0 or table.dim() != 2 or table.shape[0] != batch:
+        raise ValueError("lens must be [batch] and table [batch, table_pages]")
+    if q_start is not None:
+        _req_here(q_start, torch.int32, (batch + 1,), "q_start")
+        if max_q is None:
+            raise ValueError("q_start needs max_q, the most rows of a sequence")
+    elif T != batch:
+        raise ValueError("without q_start, q must have one row a sequence")
+    max_q = 1 if max_q is None else int(max_q)
+    if out is None:
+        out = torch.empty((T, n_q_heads, D), dtype=q.dtype, device=q.device)
+    else:
+        _req_here(out, q.dtype, (T, n_q_heads, D), "out")
+    lse_t = torch.empty((T, n_q_heads), dtype=torch.float32, device=q.device) if lse else None
+    if ws is None:
+        ws = workspace(kv4_attention_workspace_size(batch, n_q_heads, max_q, cfg))
+    else:
+        _same_device(ws, "ws")
+    if scale is None:
+        scale = D ** -0.5
+    _check(lib().awq_kv4_attention(q.data_ptr(), dt, q.stride(0), q.stride(1), T, n_q_heads, _ptr(q_start), max_q,
+                                   cache.data_ptr(), cache.shape[0], table.data_ptr(), table.shape[1], lens.data_ptr(),
+                                   batch, float(scale), ctypes.byref(cfg), out.data_ptr(), _ptr(lse_t), ws.data_ptr(),
+                                   ws.numel() * ws.element_size(), _stream()), "awq_kv4_attention")
+    return (out, lse_t) if lse else out
 
 
 def selftest_bounded_wait(ws):

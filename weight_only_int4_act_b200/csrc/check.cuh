@@ -49,6 +49,15 @@ enum BoundsSite : int {
   BS_GRAM_FIX,      // gram_tail_fixup: partial pieces and G'
   BS_FOLD_S,        // fold_inv_scales_kernel: s
   BS_FOLD_P,        // fold_inv_scales_kernel: the folded tensor
+  BS_Q8_CODES,      // quantize_int8_rows: codes
+  BS_Q8_STEP,       // quantize_int8_rows: steps
+  BS_W8_Y,          // the 8-bit integer product: Y stores
+  BS_KV4_IN,        // kv4_append_kernel: key / value rows
+  BS_KV4_CACHE,     // kv4_append_kernel / kv4_gather_kernel: the cache
+  BS_KV4_OUT,       // kv4_gather_kernel: dense keys / values
+  BS_KV4_Q,         // 4-bit attention: query rows
+  BS_KV4_STRIP,     // 4-bit attention: strips of the cache
+  BS_KV4_O,         // 4-bit attention: output rows
   BS_SELFTEST = 0x7F,
 };
 

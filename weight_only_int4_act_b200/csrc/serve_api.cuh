@@ -1,0 +1,254 @@
+// C ABI of the serving-side operators: the 8-bit integer linear layer and the
+// 4-bit key/value cache with its attention (declared in include/awq.h).
+// Included after awq_api.cu, whose host helpers it uses.
+#pragma once
+#include "kv4_sm100.cuh"
+#include "w8a8_sm100.cuh"
+
+namespace {
+
+bool dtype_ok(awq_dtype d) { return d == AWQ_DTYPE_BF16 || d == AWQ_DTYPE_F16; }
+
+// ------------------------------------------------------------------ 8-bit integer linear layer
+awq_status check_w8(int64_t N, int64_t d_out, int64_t d_in) {
+  if (N < 1 || d_out < 1 || d_in < 16 || d_in % 16 != 0 || d_in > W8_MAX_K) return AWQ_ERR_SHAPE;
+  if (d_out > (1 << 24) || N > (1 << 24)) return AWQ_ERR_SHAPE;
+  if (cdiv(N, 64) > 65535) return AWQ_ERR_SHAPE;
+  return AWQ_OK;
+}
+
+// ------------------------------------------------------------------ 4-bit cache
+awq_status check_kv4(const awq_kv4cfg* c) {
+  if (!c) return AWQ_ERR_INVALID_ARG;
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 1024) return AWQ_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 256) return AWQ_ERR_INVALID_ARG;
+  if (c->group != 32 && c->group != 64 && c->group != 128) return AWQ_ERR_INVALID_ARG;
+  if (c->head_dim % c->group != 0) return AWQ_ERR_INVALID_ARG;
+  const int p = c->page_size;
+  if (p < 16 || p > 256 || (p & (p - 1)) != 0) return AWQ_ERR_INVALID_ARG;
+  return AWQ_OK;
+}
+
+size_t kv4_head_bytes(const awq_kv4cfg* c) {
+  return (size_t)(c->page_size / KV4_STRIP) * kv4_strip_bytes(c->head_dim, c->group);
+}
+
+awq_status check_kv4_cache(const awq_kv4cfg* c, const void* cache, int64_t n_pages) {
+  if (!cache || !aligned(cache, 16)) return AWQ_ERR_INVALID_ARG;
+  if (n_pages < 1 || n_pages * c->page_size > (int64_t)INT32_MAX) return AWQ_ERR_SHAPE;
+  return AWQ_OK;
+}
+
+Kv4Cache kv4_cache(const awq_kv4cfg* c, const void* cache, int64_t n_pages) {
+  Kv4Cache k{};
+  k.base = static_cast<uint8_t*>(const_cast<void*>(cache));
+  k.n_pages = n_pages;
+  k.heads = c->n_kv_heads;
+  k.dim = c->head_dim;
+  k.group = c->group;
+  while ((1 << k.page_shift) < c->page_size) ++k.page_shift;
+  k.strip_bytes = kv4_strip_bytes(c->head_dim, c->group);
+  k.head_bytes = (long long)kv4_head_bytes(c);
+  return k;
+}
+
+bool strides_ok(int64_t tok, int64_t head) {
+  const int64_t lim = (int64_t)1 << 40;
+  return tok % 8 == 0 && head % 8 == 0 && tok >= 0 && head >= 0 && tok < lim && head < lim;
+}
+
+awq_status check_kv4_attention(int64_t batch, int64_t n_q_heads, int64_t max_q, const awq_kv4cfg* c) {
+  awq_status st = check_kv4(c);
+  if (st != AWQ_OK) return st;
+  if (batch < 1 || batch > 65535 || n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c->n_kv_heads != 0)
+    return AWQ_ERR_SHAPE;
+  if (max_q < 1 || max_q > (1 << 24)) return AWQ_ERR_SHAPE;
+  return AWQ_OK;
+}
+
+size_t kv4_attention_ws(int64_t, int64_t, int64_t, const awq_kv4cfg*) { return kAlign; }
+
+// One launch per (head dimension, group); f is called with the two as constants.
+template <typename F>
+awq_status kv4_shapes(int dim, int group, F f) {
+  auto go = [&](auto d, auto g) { return f(d, g); };
+#define AWQ_KV4_SHAPE(D, G) \
+  if (dim == D && group == G) return go(std::integral_constant<int, D>{}, std::integral_constant<int, G>{})
+  AWQ_KV4_SHAPE(64, 32);
+  AWQ_KV4_SHAPE(64, 64);
+  AWQ_KV4_SHAPE(96, 32);
+  AWQ_KV4_SHAPE(128, 32);
+  AWQ_KV4_SHAPE(128, 64);
+  AWQ_KV4_SHAPE(128, 128);
+  AWQ_KV4_SHAPE(256, 32);
+  AWQ_KV4_SHAPE(256, 64);
+  AWQ_KV4_SHAPE(256, 128);
+#undef AWQ_KV4_SHAPE
+  return AWQ_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" awq_status awq_quantize_int8(const void* x, awq_dtype dtype, int64_t ldx, const float* s,
+                                        awq_scale_mode mode, int64_t rows, int64_t d_in, int8_t* q, float* step,
+                                        awq_stream_t stream) {
+  if (!dtype_ok(dtype) || mode < AWQ_SCALE_NONE || mode > AWQ_SCALE_DIV) return AWQ_ERR_INVALID_ARG;
+  if (!x || !q || !step || (mode != AWQ_SCALE_NONE && !s)) return AWQ_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(step, 4) || (mode != AWQ_SCALE_NONE && !aligned(s, 16)))
+    return AWQ_ERR_INVALID_ARG;
+  if (rows < 1 || rows > INT32_MAX / 2 || d_in < 16 || d_in % 16 != 0 || d_in > W8_MAX_K) return AWQ_ERR_SHAPE;
+  if (ldx < d_in || ldx % 8 != 0) return AWQ_ERR_SHAPE;
+  awq_status st = check_device(nullptr);
+  if (st != AWQ_OK) return st;
+  cudaStream_t cs = as_stream(stream);
+  auto launch = [&](auto f16, auto m) {
+    quantize_int8_rows<decltype(f16)::value, decltype(m)::value>
+        <<<(unsigned)rows, 256, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
+    return launch_status();
+  };
+  auto modes = [&](auto f16) {
+    if (mode == AWQ_SCALE_MUL) return launch(f16, std::integral_constant<int, Q8_MUL>{});
+    if (mode == AWQ_SCALE_DIV) return launch(f16, std::integral_constant<int, Q8_DIV>{});
+    return launch(f16, std::integral_constant<int, Q8_PLAIN>{});
+  };
+  return dtype == AWQ_DTYPE_F16 ? modes(std::true_type{}) : modes(std::false_type{});
+}
+
+extern "C" size_t awq_w8a8_workspace_size(int64_t N, int64_t d_out, int64_t d_in) {
+  if (check_w8(N, d_out, d_in) != AWQ_OK) return 0;
+  return kAlign;
+}
+
+extern "C" awq_status awq_w8a8_gemm(const int8_t* xq, const float* x_step, const int8_t* wq, const float* w_step,
+                                    const float* bias, awq_dtype dtype, int64_t N, int64_t d_out, int64_t d_in, void* Y,
+                                    void* ws, size_t ws_bytes, awq_stream_t stream) {
+  awq_status st = check_w8(N, d_out, d_in);
+  if (st != AWQ_OK) return st;
+  if (!dtype_ok(dtype) || !xq || !x_step || !wq || !w_step || !Y || !ws) return AWQ_ERR_INVALID_ARG;
+  if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(Y, 16) || !aligned(x_step, 4) || !aligned(w_step, 4) ||
+      !aligned(bias, 4) || !aligned(ws, 256))
+    return AWQ_ERR_INVALID_ARG;
+  if (ws_bytes < awq_w8a8_workspace_size(N, d_out, d_in)) return AWQ_ERR_WORKSPACE;
+  if ((st = check_device(nullptr)) != AWQ_OK) return st;
+  cudaStream_t cs = as_stream(stream);
+  if (cudaMemsetAsync(ws, 0, sizeof(int), cs) != cudaSuccess) return AWQ_ERR_CUDA;
+  const dim3 grid((unsigned)cdiv(d_out, 64), (unsigned)cdiv(N, 64));
+  if (dtype == AWQ_DTYPE_F16)
+    w8a8_gemm_tiles<true><<<grid, 256, 0, cs>>>(xq, x_step, wq, w_step, bias, (int)N, (int)d_out, (int)d_in, Y);
+  else
+    w8a8_gemm_tiles<false><<<grid, 256, 0, cs>>>(xq, x_step, wq, w_step, bias, (int)N, (int)d_out, (int)d_in, Y);
+  return launch_status();
+}
+
+extern "C" size_t awq_kv4_page_bytes(const awq_kv4cfg* cfg) {
+  return check_kv4(cfg) == AWQ_OK ? kv4_head_bytes(cfg) : 0;
+}
+
+extern "C" awq_status awq_kv4_append(const void* k, const void* v, awq_dtype dtype, int64_t T, int64_t k_tok,
+                                     int64_t k_head, int64_t v_tok, int64_t v_head, const int32_t* slots, void* cache,
+                                     int64_t n_pages, const awq_kv4cfg* cfg, awq_stream_t stream) {
+  awq_status st = check_kv4(cfg);
+  if (st != AWQ_OK) return st;
+  if (T < 0 || T > (1 << 28)) return AWQ_ERR_SHAPE;
+  if ((st = check_kv4_cache(cfg, cache, n_pages)) != AWQ_OK) return st;
+  if (!dtype_ok(dtype) || !strides_ok(k_tok, k_head) || !strides_ok(v_tok, v_head)) return AWQ_ERR_INVALID_ARG;
+  if (T == 0) return AWQ_OK;
+  if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return AWQ_ERR_INVALID_ARG;
+  if ((st = check_device(nullptr)) != AWQ_OK) return st;
+  Kv4AppendArgs a{};
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.k_tok = k_tok;
+  a.k_head = k_head;
+  a.v_tok = v_tok;
+  a.v_head = v_head;
+  a.slots = slots;
+  a.T = (int)T;
+  a.c = kv4_cache(cfg, cache, n_pages);
+  const long long threads = 2 * T * cfg->n_kv_heads * (cfg->head_dim / 8);
+  if (cdiv(threads, 256) > INT32_MAX) return AWQ_ERR_SHAPE;
+  const unsigned grid = (unsigned)cdiv(threads, 256);
+  if (dtype == AWQ_DTYPE_F16)
+    kv4_append_kernel<true><<<grid, 256, 0, as_stream(stream)>>>(a);
+  else
+    kv4_append_kernel<false><<<grid, 256, 0, as_stream(stream)>>>(a);
+  return launch_status();
+}
+
+extern "C" awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const int32_t* slots, int64_t T,
+                                     const awq_kv4cfg* cfg, void* k, void* v, awq_dtype dtype, awq_stream_t stream) {
+  awq_status st = check_kv4(cfg);
+  if (st != AWQ_OK) return st;
+  if (T < 0 || T > (1 << 28)) return AWQ_ERR_SHAPE;
+  if ((st = check_kv4_cache(cfg, cache, n_pages)) != AWQ_OK) return st;
+  if (!dtype_ok(dtype)) return AWQ_ERR_INVALID_ARG;
+  if (T == 0 || (!k && !v)) return AWQ_OK;
+  if (!slots || !aligned(slots, 4) || !aligned(k, 16) || !aligned(v, 16)) return AWQ_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = check_device(&sms)) != AWQ_OK) return st;
+  const Kv4Cache c = kv4_cache(cfg, cache, n_pages);
+  const long long blocks = cdiv(2 * T * cfg->n_kv_heads * (cfg->head_dim / 8), 256);
+  const unsigned grid = (unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms);
+  if (dtype == AWQ_DTYPE_F16)
+    kv4_gather_kernel<true><<<grid, 256, 0, as_stream(stream)>>>(c, slots, (int)T, k, v);
+  else
+    kv4_gather_kernel<false><<<grid, 256, 0, as_stream(stream)>>>(c, slots, (int)T, k, v);
+  return launch_status();
+}
+
+extern "C" size_t awq_kv4_attention_workspace_size(int64_t batch, int64_t n_q_heads, int64_t max_q,
+                                                   const awq_kv4cfg* cfg) {
+  if (check_kv4_attention(batch, n_q_heads, max_q, cfg) != AWQ_OK) return 0;
+  return kv4_attention_ws(batch, n_q_heads, max_q, cfg);
+}
+
+extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t q_tok, int64_t q_head, int64_t T,
+                                        int64_t n_q_heads, const int32_t* q_start, int64_t max_q, const void* cache,
+                                        int64_t n_pages, const int32_t* table, int64_t table_pages, const int32_t* lens,
+                                        int64_t batch, float scale, const awq_kv4cfg* cfg, void* out, float* lse,
+                                        void* ws, size_t ws_bytes, awq_stream_t stream) {
+  awq_status st = check_kv4_attention(batch, n_q_heads, max_q, cfg);
+  if (st != AWQ_OK) return st;
+  if ((st = check_kv4_cache(cfg, cache, n_pages)) != AWQ_OK) return st;
+  if (T < 0 || T > (1 << 28) || table_pages < 1 || table_pages * cfg->page_size > (int64_t)INT32_MAX)
+    return AWQ_ERR_SHAPE;
+  if (!q_start && (T < batch || max_q != 1)) return AWQ_ERR_SHAPE;
+  if (!dtype_ok(dtype) || !strides_ok(q_tok, q_head) || !std::isfinite(scale)) return AWQ_ERR_INVALID_ARG;
+  if (!q || !table || !lens || !out || !ws) return AWQ_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_start, 4) ||
+      !aligned(lse, 4) || !aligned(ws, 256))
+    return AWQ_ERR_INVALID_ARG;
+  if (ws_bytes < kv4_attention_ws(batch, n_q_heads, max_q, cfg)) return AWQ_ERR_WORKSPACE;
+  if ((st = check_device(nullptr)) != AWQ_OK) return st;
+  cudaStream_t cs = as_stream(stream);
+  Kv4AttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_tok = q_tok;
+  a.q_head = q_head;
+  a.T = T;
+  a.q_heads = (int)n_q_heads;
+  a.share = (int)(n_q_heads / cfg->n_kv_heads);
+  a.q_start = q_start;
+  a.max_q = (int)max_q;
+  a.table = table;
+  a.table_pages = (int)table_pages;
+  a.lens = lens;
+  a.batch = (int)batch;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.c = kv4_cache(cfg, cache, n_pages);
+  a.out = out;
+  a.lse = lse;
+  a.err = at<int>(ws, 0);
+  if (cudaMemsetAsync(ws, 0, sizeof(int), cs) != cudaSuccess) return AWQ_ERR_CUDA;
+  const long long tiles = cdiv(max_q * a.share, 8);
+  if (tiles > INT32_MAX) return AWQ_ERR_SHAPE;
+  const dim3 grid((unsigned)tiles, (unsigned)cfg->n_kv_heads, (unsigned)batch);
+  return kv4_shapes(cfg->head_dim, cfg->group, [&](auto d, auto g) {
+    constexpr int D = decltype(d)::value, G = decltype(g)::value;
+    if (dtype == AWQ_DTYPE_F16)
+      kv4_attention_tiles<D, G, true><<<grid, 32 * KV4_WARPS, 0, cs>>>(a);
+    else
+      kv4_attention_tiles<D, G, false><<<grid, 32 * KV4_WARPS, 0, cs>>>(a);
+    return launch_status();
+  });
+}
