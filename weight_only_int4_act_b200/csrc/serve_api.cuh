@@ -13,8 +13,84 @@ bool dtype_ok(awq_dtype d) { return d == AWQ_DTYPE_BF16 || d == AWQ_DTYPE_F16; }
 awq_status check_w8(int64_t N, int64_t d_out, int64_t d_in) {
   if (N < 1 || d_out < 1 || d_in < 16 || d_in % 16 != 0 || d_in > W8_MAX_K) return AWQ_ERR_SHAPE;
   if (d_out > (1 << 24) || N > (1 << 24)) return AWQ_ERR_SHAPE;
-  if (cdiv(N, 64) > 65535) return AWQ_ERR_SHAPE;
+  if (N * d_out > (int64_t)INT32_MAX * 8) return AWQ_ERR_SHAPE;
   return AWQ_OK;
+}
+
+struct W8Plan {
+  bool pair;
+  int bm, bn, b_rows, workers, slots, smem;
+  long long tiles;
+  W8Args a;
+  size_t ws;
+};
+
+W8Plan w8_plan(int64_t N, int64_t d_out, int64_t d_in) {
+  W8Plan p{};
+  p.pair = N > 64;
+  p.bm = p.pair ? 2 * W8_BM : W8_BM;
+  const int step = p.pair ? 32 : 16;
+  const long long nb = cdiv(N, 256);
+  p.bn = (int)(cdiv(cdiv(N, nb), step) * step);
+  p.b_rows = p.pair ? p.bn / 2 : p.bn;
+  W8Args& a = p.a;
+  a.N = (int)N;
+  a.d_out = (int)d_out;
+  a.bn = p.bn;
+  a.n_mb = (int)cdiv(d_out, p.bm);
+  a.n_nb = (int)cdiv(N, p.bn);
+  a.n_kb = (int)cdiv(d_in, W8_BK);
+  a.group_nb = a.n_nb < 8 ? a.n_nb : 8;
+  int st = (W8_SMEM_LIMIT - w8_smem_bytes(0, p.b_rows)) / w8_stage_bytes(p.b_rows);
+  a.stages = st < W8_MAX_STAGES ? st : W8_MAX_STAGES;
+  p.smem = w8_smem_bytes(a.stages, p.b_rows);
+  p.tiles = (long long)a.n_mb * a.n_nb;
+  const int G = p.pair ? W8_SMS / 2 : W8_SMS;
+  // whole waves first; what is left (one to two waves, or all tiles where
+  // there are fewer) in equal ranges, unless it is whole waves as well or the
+  // uneven last wave is a small part of the whole
+  const long long waves = p.tiles / G;
+  const bool even = p.tiles % G == 0 || waves >= 4 || a.n_kb < 2;
+  const long long split = even ? 0 : p.tiles - (waves > 1 ? (waves - 1) * G : 0);
+  a.whole = (int)(p.tiles - split);
+  a.units = split * a.n_kb;
+  // at least 4 K steps a worker
+  p.workers = split == 0 ? (int)(p.tiles < G ? p.tiles : G) : a.whole ? G : (int)(a.units / 4 < G ? (a.units / 4 > 1 ? a.units / 4 : 1) : G);
+  p.slots = 1;
+  for (long long t = 0; t < split; ++t) {
+    const long long n = w4_sk_cta(t * a.n_kb + a.n_kb - 1, p.workers, a.units) - w4_sk_cta(t * a.n_kb, p.workers, a.units) + 1;
+    if (n > p.slots) p.slots = (int)n;
+  }
+  a.p_stride = (N * d_out + 3) / 4 * 4;
+  p.ws = kAlign + (p.slots > 1 ? align_up((size_t)p.slots * a.p_stride * sizeof(int)) : 0);
+  return p;
+}
+
+// The split tiles of a plan (each found at its first inner range boundary), with their slab counts.
+void w8_fixups(const W8Plan& p, W8Fixups& fx) {
+  fx.n = 0;
+  const long long U = p.a.units, k = p.a.n_kb;
+  for (long long c = 1; c < p.workers && U > 0; ++c) {
+    const long long b = w4_sk_begin(c, p.workers, U), tile = b / k, t0 = tile * k;
+    if (b == t0 || w4_sk_cta(t0, p.workers, U) != c - 1) continue;
+    fx.tile[fx.n] = (int)(p.a.whole + tile);
+    fx.ns[fx.n] = (short)(w4_sk_cta(t0 + k - 1, p.workers, U) - (c - 1) + 1);
+    ++fx.n;
+  }
+}
+
+// 2-D map of bytes over a row-major [rows, cols] matrix, box of 128 columns (one swizzled row) x box_rows.
+bool make_map_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols};
+  cuuint32_t box[2] = {W8_BK, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
 }
 
 // ------------------------------------------------------------------ 4-bit cache
@@ -116,7 +192,7 @@ extern "C" awq_status awq_quantize_int8(const void* x, awq_dtype dtype, int64_t 
 
 extern "C" size_t awq_w8a8_workspace_size(int64_t N, int64_t d_out, int64_t d_in) {
   if (check_w8(N, d_out, d_in) != AWQ_OK) return 0;
-  return kAlign;
+  return w8_plan(N, d_out, d_in).ws;
 }
 
 extern "C" awq_status awq_w8a8_gemm(const int8_t* xq, const float* x_step, const int8_t* wq, const float* w_step,
@@ -128,15 +204,37 @@ extern "C" awq_status awq_w8a8_gemm(const int8_t* xq, const float* x_step, const
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(Y, 16) || !aligned(x_step, 4) || !aligned(w_step, 4) ||
       !aligned(bias, 4) || !aligned(ws, 256))
     return AWQ_ERR_INVALID_ARG;
-  if (ws_bytes < awq_w8a8_workspace_size(N, d_out, d_in)) return AWQ_ERR_WORKSPACE;
+  W8Plan p = w8_plan(N, d_out, d_in);
+  if (ws_bytes < p.ws) return AWQ_ERR_WORKSPACE;
   if ((st = check_device(nullptr)) != AWQ_OK) return st;
   cudaStream_t cs = as_stream(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(int), cs) != cudaSuccess) return AWQ_ERR_CUDA;
-  const dim3 grid((unsigned)cdiv(d_out, 64), (unsigned)cdiv(N, 64));
-  if (dtype == AWQ_DTYPE_F16)
-    w8a8_gemm_tiles<true><<<grid, 256, 0, cs>>>(xq, x_step, wq, w_step, bias, (int)N, (int)d_out, (int)d_in, Y);
+  W8Args& a = p.a;
+  a.dx = x_step;
+  a.dw = w_step;
+  a.bias = bias;
+  a.Y = Y;
+  a.P = at<int>(ws, kAlign);
+  a.err = at<int>(ws, 0);
+  CUtensorMap tw, tx;
+  if (!make_map_u8(&tw, wq, d_out, d_in, W8_BM) || !make_map_u8(&tx, xq, N, d_in, p.b_rows)) return AWQ_ERR_CUDA;
+  const bool f16 = dtype == AWQ_DTYPE_F16;
+  auto launch = [&](auto kernel) -> awq_status {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem) != cudaSuccess)
+      return AWQ_ERR_CUDA;
+    kernel<<<p.pair ? 2 * p.workers : p.workers, W8_THREADS, p.smem, cs>>>(tw, tx, a);
+    return launch_status();
+  };
+  st = p.pair ? (f16 ? launch(w8a8_gemm_pair_tcgen05<true>) : launch(w8a8_gemm_pair_tcgen05<false>))
+              : (f16 ? launch(w8a8_gemm_tcgen05<true>) : launch(w8a8_gemm_tcgen05<false>));
+  if (st != AWQ_OK || p.slots == 1) return st;
+  W8Fixups fx;
+  w8_fixups(p, fx);
+  if (fx.n == 0) return AWQ_OK;
+  const dim3 rgrid((unsigned)fx.n, (unsigned)cdiv((long long)p.bm * p.bn, 1024));
+  if (f16)
+    w8a8_reduce<true><<<rgrid, 256, 0, cs>>>(a, p.bm, fx);
   else
-    w8a8_gemm_tiles<false><<<grid, 256, 0, cs>>>(xq, x_step, wq, w_step, bias, (int)N, (int)d_out, (int)d_in, Y);
+    w8a8_reduce<false><<<rgrid, 256, 0, cs>>>(a, p.bm, fx);
   return launch_status();
 }
 

@@ -108,55 +108,387 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Plain tile product: 64 tokens x 64 channels a block, 64 channels of K a turn.
+// ------------------------------------------------------------------ tensor-core product
+// Output channels are the M rows of tcgen05.mma kind::i8 (128 a CTA; 256 over a
+// CTA pair) and tokens the N columns (BN of them, a multiple of 16, or of 32 in
+// a pair), so a few tokens still fill an instruction and a TMEM lane is an
+// output channel: an epilogue warp stores 32 consecutive channels of a token.
+// One K step is 128 channels (128 bytes, one swizzled row; 4 MMAs of K = 32).
+// Roles (192 threads, one CTA per SM): warp 0 TMA, warp 1 TMEM and MMAs, warps
+// 2..5 epilogue out of two accumulators, so that it runs under the next tile.
+//
+// Work: G workers (CTAs, or pairs) first take whole tiles c, c + G, ...; the
+// last one to two waves (all tiles, where there are fewer) are cut into G equal
+// contiguous ranges of (tile, K step) units. A tile that several workers touch
+// leaves int32 partials in slabs which w8a8_reduce adds: the sum is exact, so
+// the split changes no bit.
+constexpr int W8_THREADS = 192;
+constexpr int W8_BM = 128;
+constexpr int W8_BK = 128;
+constexpr int W8_A_STAGE = W8_BM * W8_BK;
+constexpr int W8_MAX_STAGES = 12;
+constexpr int W8_NBARS = 2 * W8_MAX_STAGES + 5;
+constexpr int W8_TMEM_COLS = 512;
+constexpr int W8_SMEM_LIMIT = 232448;
+constexpr int W8_SMS = 148;  // workers of the plan: one CTA per SM
+
+__host__ __device__ constexpr int w8_stage_bytes(int b_rows) { return W8_A_STAGE + b_rows * W8_BK; }
+__host__ __device__ constexpr int w8_smem_bytes(int stages, int b_rows) {
+  return 1024 + stages * w8_stage_bytes(b_rows) + W8_NBARS * 8 + 64 + 4 * 256 * 4;
+}
+
+constexpr int ERR_W8_EMPTY = 0x501, ERR_W8_FULL = 0x502, ERR_W8_TFULL = 0x503, ERR_W8_TEMPTY = 0x504;
+
+struct W8Args {
+  int N, d_out;
+  int bn;                // tokens of a tile
+  int n_mb, n_nb, n_kb;  // tiles of channels and tokens, K steps
+  int group_nb;          // token tiles that neighbouring workers share a weight tile over
+  int stages;
+  int whole;             // tiles [0, whole) are taken whole, strided by the workers
+  long long units;       // (tiles - whole) * n_kb, cut into ranges
+  const float *dx, *dw, *bias;
+  void* Y;
+  int* P;                // [slots][N, d_out] partials
+  long long p_stride;
+  int* err;
+};
+
+__host__ __device__ inline void w8_tile(const W8Args& a, long long t, int& mb, int& nb) {
+  const long long per = (long long)a.n_mb * a.group_nb, grp = t / per, in = t - grp * per;
+  const int first = (int)grp * a.group_nb;
+  const int width = a.n_nb - first < a.group_nb ? a.n_nb - first : a.group_nb;
+  nb = first + (int)(in % width);
+  mb = (int)(in / width);
+}
+
+struct W8Seg {
+  int mb, nb, kb0, kb1, slot;
+  bool whole;  // no other worker touches the tile
+};
+
+// The segments of worker c of G, in order; every role walks the same sequence.
+struct W8Sched {
+  long long t, u, u1;
+  int c, G;
+  __device__ W8Sched(const W8Args& a, int c_, int G_) : t(c_), c(c_), G(G_) {
+    u = w4_sk_begin(c, G, a.units);
+    u1 = w4_sk_begin(c + 1, G, a.units);
+  }
+  __device__ bool next(const W8Args& a, W8Seg& g) {
+    long long tile;
+    g.kb0 = 0;
+    g.kb1 = a.n_kb;
+    g.slot = 0;
+    g.whole = true;
+    if (t < a.whole) {
+      tile = t;
+      t += G;
+    } else {
+      if (u >= u1) return false;
+      const long long k = u / a.n_kb, t0 = k * a.n_kb;
+      tile = a.whole + k;
+      g.kb0 = (int)(u - t0);
+      g.kb1 = (int)min((long long)a.n_kb, (long long)g.kb0 + (u1 - u));
+      const long long first = w4_sk_cta(t0, G, a.units);
+      g.whole = w4_sk_cta(t0 + a.n_kb - 1, G, a.units) == first;
+      g.slot = (int)(c - first);
+      u += g.kb1 - g.kb0;
+    }
+    w8_tile(a, tile, g.mb, g.nb);
+    return true;
+  }
+};
+
+// Instruction descriptor, kind::i8: signed 8-bit A and B (K-major), int32 D.
+__host__ __device__ constexpr uint32_t idesc_i8_s32(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
 template <bool F16>
-__global__ void __launch_bounds__(256)
-    w8a8_gemm_tiles(const int8_t* __restrict__ xq, const float* __restrict__ dx, const int8_t* __restrict__ wq,
-                    const float* __restrict__ dw, const float* __restrict__ bias, int N, int d_out, int d_in,
-                    void* __restrict__ Yv) {
+__device__ __forceinline__ float w8_scale(int acc, float dx, float dw) {
+  return __fmul_rn(__fmul_rn(__int2float_rn(acc), dx), dw);
+}
+
+template <bool PAIR, bool F16>
+__device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensorMap& tmX, const W8Args& args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int bn = args.bn, stages = args.stages;
+  const int b_rows = PAIR ? bn / 2 : bn;  // token rows this CTA loads
+  const uint32_t b_stage = (uint32_t)b_rows * W8_BK, stage_bytes = W8_A_STAGE + b_stage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + stages * stage_bytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + W8_NBARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sdx = reinterpret_cast<float*>(tmem_slot + 16);  // [4 epilogue warps][256]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? (cluster_ctarank() & 1u) : 0u;
+  const bool lead = rank == 0;
+  const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, G = PAIR ? gridDim.x >> 1 : gridDim.x;
+  auto full = [&](int s) { return smem_u32(bars + s); };
+  auto empty = [&](int s) { return smem_u32(bars + W8_MAX_STAGES + s); };
+  auto tfull = [&](int a) { return smem_u32(bars + 2 * W8_MAX_STAGES + a); };
+  auto tempty = [&](int a) { return smem_u32(bars + 2 * W8_MAX_STAGES + 2 + a); };
+  const uint32_t drain_bar = smem_u32(bars + 2 * W8_MAX_STAGES + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), PAIR ? 8 : 4);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    // the error word of this call: only waits that give up after two seconds write it
+    if (blockIdx.x == 0) *args.err = 0;
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), W8_TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), W8_TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // barriers of both CTAs initialised before any remote use
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int acc_stride = 256;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA: this CTA's 128 weight rows and b_rows token rows of each K step
+      Ring ring;
+      uint32_t issued = 0, last_parity = 0;
+      bool ok = true;
+      W8Sched sched(args, worker, G);
+      W8Seg g;
+      while (ok && sched.next(args, g)) {
+        for (int kb = g.kb0; kb < g.kb1; ++kb) {
+          if (!mbar_wait(empty(ring.stage), ring.phase ^ 1u, abort_flag, args.err, ERR_W8_EMPTY)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = smem_u32(smem + ring.stage * stage_bytes), sb = sa + W8_A_STAGE;
+          const int wrow = (g.mb * (PAIR ? 2 : 1) + (int)rank) * W8_BM, xrow = g.nb * bn + (int)rank * b_rows;
+          if constexpr (PAIR) {
+            const uint32_t bar = mapa_shared(full(ring.stage), 0);
+            if (lead) mbar_arrive_expect_tx(full(ring.stage), 2 * stage_bytes);
+            tma_load_2d_pair(sa, &tmW, bar, kb * W8_BK, wrow);
+            tma_load_2d_pair(sb, &tmX, bar, kb * W8_BK, xrow);
+          } else {
+            mbar_arrive_expect_tx(full(ring.stage), stage_bytes);
+            tma_load_2d(sa, &tmW, full(ring.stage), kb * W8_BK, wrow);
+            tma_load_2d(sb, &tmX, full(ring.stage), kb * W8_BK, xrow);
+          }
+          issued |= 1u << ring.stage;
+          last_parity = (last_parity & ~(1u << ring.stage)) | (ring.phase << ring.stage);
+          ring.next(stages);
+        }
+      }
+      if (lead) {
+        for (int s = 0; s < stages; ++s)
+          if (issued & (1u << s)) mbar_wait_drain(full(s), (last_parity >> s) & 1u);
+      } else if (*abort_flag) {
+        // on an aborted run, give this CTA's unconsumed loads time to land
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && lead) {
+      // ---------------- MMA issuer
+      const uint32_t idesc = idesc_i8_s32(PAIR ? 2 * W8_BM : W8_BM, bn);
+      const uint64_t d0 = desc_kmajor_sw128(smem_u32(smem));
+      Ring ring;
+      bool ok = true;
+      W8Sched sched(args, worker, G);
+      W8Seg g;
+      for (int local = 0; ok && sched.next(args, g); ++local) {
+        const int acc = local & 1;
+        if (!mbar_wait(tempty(acc), ((local >> 1) & 1) ^ 1u, abort_flag, args.err, ERR_W8_TEMPTY)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * acc_stride;
+        for (int kb = g.kb0; kb < g.kb1; ++kb) {
+          if (!mbar_wait(full(ring.stage), ring.phase, abort_flag, args.err, ERR_W8_FULL)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = d0 + ((uint64_t)(ring.stage * stage_bytes) >> 4), db = da + (W8_A_STAGE >> 4);
+#pragma unroll
+          for (int k = 0; k < W8_BK / 32; ++k) mma_i8<PAIR>(d_tmem, da + 2 * k, db + 2 * k, idesc, (kb != g.kb0) || k);
+          if constexpr (PAIR)
+            mma_commit_pair(empty(ring.stage), 0x3);
+          else
+            mma_commit(empty(ring.stage));
+          ring.next(stages);
+        }
+        if (ok) {
+          if constexpr (PAIR)
+            mma_commit_pair(tfull(acc), 0x3);
+          else
+            mma_commit(tfull(acc));
+        }
+      }
+      if constexpr (PAIR)
+        mma_commit_pair(drain_bar, 0x1);
+      else
+        mma_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0);
+    }
+  } else {
+    // ---------------- epilogue (warp w reads TMEM lanes 32 (w % 4) ..)
+    using Ty = W4Type<F16>;
+    const int quad = warp & 3;
+    float* dxs = sdx + (warp - 2) * 256;
+    W8Sched sched(args, worker, G);
+    W8Seg g;
+    for (int local = 0; sched.next(args, g); ++local) {
+      const int acc = local & 1;
+      const int t0 = g.nb * bn, toks = min(bn, args.N - t0);
+      const int o = (g.mb * (PAIR ? 2 : 1) + (int)rank) * W8_BM + quad * 32 + lane;
+      const bool in = o < args.d_out;
+      if (g.whole)
+        for (int j = lane; j < toks; j += 32) dxs[j] = __ldg(args.dx + t0 + j);
+      const float dw = g.whole && in ? __ldg(args.dw + o) : 0.0f;
+      const float bias = g.whole && in && args.bias ? __ldg(args.bias + o) : 0.0f;
+      __syncwarp();
+      const bool ready = mbar_wait_sleep(tfull(acc), (local >> 1) & 1u, abort_flag, args.err, ERR_W8_TFULL, 64);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * acc_stride;
+      for (int c = 0; c * 32 < toks; ++c) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(taddr + c * 32, v);
+        tmem_ld_wait();
+        const int jn = min(32, toks - c * 32);
+        const long long e0 = (long long)(t0 + c * 32) * args.d_out + o;
+        if (in && g.whole) {
+          typename Ty::T* y = static_cast<typename Ty::T*>(args.Y) + e0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float r = w8_scale<F16>((int)v[j], dxs[c * 32 + j], dw);
+            if (args.bias) r = __fadd_rn(r, bias);
+            if (j < jn && AWQ_IDX_OK(e0 + (long long)j * args.d_out, (long long)args.N * args.d_out, BS_W8_Y))
+              y[(long long)j * args.d_out] = Ty::from_float(r);
+          }
+        } else if (in) {
+          int* P = args.P + (long long)g.slot * args.p_stride + e0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j < jn && AWQ_IDX_OK(e0 + (long long)j * args.d_out, (long long)args.N * args.d_out, BS_W8_P))
+              P[(long long)j * args.d_out] = (int)v[j];
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (lead)
+          mbar_arrive(tempty(acc));
+        else
+          mbar_arrive_remote(mapa_shared(tempty(acc), 0));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // all MMAs drained, all TMEM reads and remote arrivals done in both CTAs
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, W8_TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, W8_TMEM_COLS);
+  }
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(W8_THREADS, 1)
+    w8a8_gemm_tcgen05(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                      const __grid_constant__ W8Args args) {
+  w8a8_body<false, F16>(tmW, tmX, args);
+}
+template <bool F16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W8_THREADS, 1)
+    w8a8_gemm_pair_tcgen05(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                           const __grid_constant__ W8Args args) {
+  w8a8_body<true, F16>(tmW, tmX, args);
+}
+
+// Tiles that two or more workers touch, found on the host from the shapes.
+struct W8Fixups {
+  int n;
+  int tile[W8_SMS];
+  short ns[W8_SMS];
+};
+
+// Block (b, y) adds the partials of split tile fx.tile[b] for 1024 of its
+// elements (channel fastest) and writes them scaled and rounded.
+template <bool F16>
+__global__ void __launch_bounds__(256) w8a8_reduce(const W8Args a, int bm, const __grid_constant__ W8Fixups fx) {
   using Ty = W4Type<F16>;
-  __shared__ int sx[64][17], sw[64][17];
-  const long long t0 = (long long)blockIdx.y * 64, o0 = (long long)blockIdx.x * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (int k = 0; k < d_in; k += 64) {
-    for (int e = threadIdx.x; e < 64 * 4; e += 256) {
-      const int row = e >> 2, c = e & 3;
-      int4 a = make_int4(0, 0, 0, 0), b = a;
-      if (k + 16 * c < d_in) {
-        if (t0 + row < N) a = __ldg(reinterpret_cast<const int4*>(xq + (t0 + row) * d_in + k + 16 * c));
-        if (o0 + row < d_out) b = __ldg(reinterpret_cast<const int4*>(wq + (o0 + row) * d_in + k + 16 * c));
-      }
-      int* pa = &sx[row][4 * c];
-      int* pb = &sw[row][4 * c];
-      pa[0] = a.x, pa[1] = a.y, pa[2] = a.z, pa[3] = a.w;
-      pb[0] = b.x, pb[1] = b.y, pb[2] = b.z, pb[3] = b.w;
-    }
-    __syncthreads();
+  if (!AWQ_IDX_OK(blockIdx.x, fx.n, BS_W8_P)) return;
+  int mb, nb;
+  w8_tile(a, fx.tile[blockIdx.x], mb, nb);
+  const int ns = fx.ns[blockIdx.x];
+  const int o0 = mb * bm, t0 = nb * a.bn;
+  const int rows = min(bm, a.d_out - o0), toks = min(a.bn, a.N - t0);
+  long long idx[4];
+  bool in[4];
+  int acc[4], oo[4], tt[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      int a[4], b[4];
+  for (int k = 0; k < 4; ++k) {
+    const int e = blockIdx.y * 1024 + k * 256 + threadIdx.x;
+    const int j = e / rows, r = e - j * rows;
+    tt[k] = t0 + j;
+    oo[k] = o0 + r;
+    idx[k] = (long long)tt[k] * a.d_out + oo[k];
+    in[k] = e < rows * toks && AWQ_IDX_OK(idx[k], (long long)a.N * a.d_out, BS_W8_P);
+    acc[k] = 0;
+  }
+  for (int s = 0; s < ns; ++s) {
+    const int* P = a.P + (long long)s * a.p_stride;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        a[u] = sx[ty + 16 * u][i];
-        b[u] = sw[tx + 16 * u][i];
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) acc[u][w] = __dp4a(a[u], b[w], acc[u][w]);
-    }
-    __syncthreads();
+    for (int k = 0; k < 4; ++k)
+      if (in[k]) acc[k] += P[idx[k]];
   }
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const long long t = t0 + ty + 16 * u, o = o0 + tx + 16 * w;
-      if (t >= N || o >= d_out || !AWQ_IDX_OK(t * d_out + o, (long long)N * d_out, BS_W8_Y)) continue;
-      float y = __fmul_rn(__fmul_rn((float)acc[u][w], dx[t]), dw[o]);
-      if (bias) y = __fadd_rn(y, bias[o]);
-      static_cast<typename Ty::T*>(Yv)[t * d_out + o] = Ty::from_float(y);
+  for (int k = 0; k < 4; ++k)
+    if (in[k]) {
+      float y = w8_scale<F16>(acc[k], __ldg(a.dx + tt[k]), __ldg(a.dw + oo[k]));
+      if (a.bias) y = __fadd_rn(y, __ldg(a.bias + oo[k]));
+      static_cast<typename Ty::T*>(a.Y)[idx[k]] = Ty::from_float(y);
     }
 }
 
