@@ -339,7 +339,7 @@ def test_decode_step_captured_and_replayed():
     v = _rand((3, heads, dim), "bf16", 2)
     q = _rand((3, heads * share, dim), "bf16", 3)
     slot = torch.zeros(3, dtype=torch.int32, device="cuda")
-    outs, graphs = [], []
+    outs, graphs, works = [], [], []  # a graph's workspace lives as long as the graph
     for _ in range(2):
         out = torch.zeros((3, heads * share, dim), dtype=torch.bfloat16, device="cuda")
         work = awq.workspace(awq.kv4_attention_workspace_size(3, heads * share, 1, cfg))
@@ -351,6 +351,7 @@ def test_decode_step_captured_and_replayed():
             awq.kv4_attention(q, cache, table, lens, cfg, ws=work, out=out)
         outs.append(out)
         graphs.append(g)
+        works.append(work)
     first = np.concatenate([[0], np.cumsum([n + 20 for n in lens0])])[:-1]
     for i in range(18):
         now = [n + i + 1 for n in lens0]

@@ -195,20 +195,22 @@ struct Kv4AttnArgs {
   long long q_tok, q_head;  // strides in elements
   long long T;              // rows of q
   int q_heads, share;       // query heads, query heads of a kv head
-  const int* q_start;       // [batch + 1], or NULL: sequence b is row b
+  const int* q_start;       // [batch + 1], or NULL: sequence b is row row_first + b
+  int row_first;
   int max_q;
   const int* table;  // [batch, table_pages]
   int table_pages;
   const int* lens;  // [batch]
   int batch;
   float scale_log2;  // softmax scale * log2(e)
+  bool f16;          // q and out are fp16 (else bf16)
   Kv4Cache c;
   void* out;   // [T, q_heads, D] contiguous
   float* lse;  // [T, q_heads] or NULL
   int* err;
 };
 
-constexpr int ERR_KV4_PAGE = 0x401;
+constexpr int ERR_KV4_PAGE = 0x401, ERR_KV4_COPY = 0x402;
 
 // One sequence's rows and context, clamped to what the arguments can hold:
 // rows [row0, row0 + n), context length L. bad: something was clamped.
@@ -219,7 +221,7 @@ struct Kv4Seq {
 };
 __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int b) {
   Kv4Seq s;
-  long long r0 = a.q_start ? a.q_start[b] : b, r1 = a.q_start ? a.q_start[b + 1] : b + 1;
+  long long r0 = a.q_start ? a.q_start[b] : a.row_first + b, r1 = a.q_start ? a.q_start[b + 1] : r0 + 1;
   const long long cap = (long long)a.table_pages << a.c.page_shift;
   const int len = a.lens[b];
   s.bad = r0 < 0 || r1 < r0 || r1 > a.T || r1 - r0 > a.max_q || len < 0 || len > cap;
@@ -229,6 +231,11 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int b) {
   s.n = (int)(r1 - r0 < a.max_q ? r1 - r0 : a.max_q);
   s.L = len < 0 ? 0 : (int)(len < cap ? len : cap);
   return s;
+}
+
+// x rounded to the output type
+__device__ __forceinline__ uint16_t kv4_narrow(const Kv4AttnArgs& a, float x) {
+  return a.f16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
 // D[16 x 8] += A[16 x 16] B[16 x 8], fp16 operands, fp32 accumulators.
@@ -247,6 +254,27 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 }
 __device__ __forceinline__ float exp2_fast(float x) { return exp2f(x); }
 
+// N consecutive words at p, aligned to the largest power of two that divides 4 N (at most 16).
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const uint2 v = reinterpret_cast<const uint2*>(p)[i];
+      w[2 * i] = v.x, w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+}
+
 // What a warp knows of a tile of 8 NT query rows of one (sequence, kv head).
 // Column j of n-tile u is row 8 u + j of the tile; a lane works on columns
 // 2 q and 2 q + 1 of each n-tile.
@@ -259,11 +287,11 @@ struct Kv4Warp {
   int vis[NT][2];              // keys [0, vis) are visible to the column's query
   int vis_min, vis_max;        // over the tile's rows
   float o[NT][NJ][2][4];       // accumulators: channels 32 p + 16 n + ..., value 2^-24 (n = 0) or 2^-20 units
-  float zs[NT][NG][2];         // sum of w zero over this lane's tokens
+  float mid[NT][NG][4];        // -8 2^-24 sum of w since the last recentre(), in every row
+  float zs[NT][NG][2];         // sum of w (zero - 8) over this lane's tokens
   float m[NT][2], l[NT][2];    // reference exponent (the same in all lanes of a column), sum of p over this lane's tokens
 
   // Rows [r0, r0 + 8 NT) of the sequence's n * share query rows (row = token * share + head in the group).
-  template <bool F16>
   __device__ __forceinline__ void load_queries(const Kv4AttnArgs& a, const Kv4Seq& s, int head, long long r0, int lane) {
     const int g = lane >> 2, q = lane & 3;
     const long long rows = (long long)s.n * a.share;
@@ -286,7 +314,7 @@ struct Kv4Warp {
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 f = widen2<F16>(ww[i]);
+          const float2 f = a.f16 ? widen2<true>(ww[i]) : widen2<false>(ww[i]);
           x[j][2 * i] = f.x;
           x[j][2 * i + 1] = f.y;
           top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
@@ -361,7 +389,11 @@ struct Kv4Warp {
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[u][p][n][i] = 0.0f;
 #pragma unroll
-      for (int gi = 0; gi < NG; ++gi) zs[u][gi][0] = zs[u][gi][1] = 0.0f;
+      for (int gi = 0; gi < NG; ++gi) {
+        zs[u][gi][0] = zs[u][gi][1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mid[u][gi][i] = 0.0f;
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         m[u][c] = -INFINITY;
@@ -376,8 +408,9 @@ struct Kv4Warp {
   template <bool EDGE>
   __device__ __forceinline__ void strip(const uint8_t* s, int t0, int lane) {
     const int g = lane >> 2, q = lane & 3;
-    const uint32_t* kw0 = reinterpret_cast<const uint32_t*>(s + g * (D / 2)) + q * NJ;
-    const uint32_t* kw1 = kw0 + 8 * (D / 8);
+    uint32_t kw0[NJ], kw1[NJ];
+    load_words<NJ>(s + g * (D / 2) + 4 * q * NJ, kw0);
+    load_words<NJ>(s + (g + 8) * (D / 2) + 4 * q * NJ, kw1);
     const uint32_t* kpar = reinterpret_cast<const uint32_t*>(s + 16 * D);
     const uint32_t* vpar = kpar + 16 * NG;
     // scores: token rows g and g + 8, columns 2 q and 2 q + 1
@@ -444,7 +477,11 @@ struct Kv4Warp {
           m[u][c] = mn;
           l[u][c] *= f;
 #pragma unroll
-          for (int gi = 0; gi < NG; ++gi) zs[u][gi][c] *= f;
+          for (int gi = 0; gi < NG; ++gi) {
+            zs[u][gi][c] *= f;
+            mid[u][gi][c] *= f;
+            mid[u][gi][c + 2] *= f;
+          }
 #pragma unroll
           for (int p = 0; p < NJ; ++p)
 #pragma unroll
@@ -475,7 +512,8 @@ struct Kv4Warp {
         }
         const uint32_t r0 = pack2<true>(w[0], w[1]), r1 = pack2<true>(w[2], w[3]);
         const float2 b0 = widen2<true>(r0), b1 = widen2<true>(r1);  // the rounded weights, which the codes meet too
-        float z[4] = {b0.x * vp[gi][0].y, b0.y * vp[gi][0].y, b1.x * vp[gi][1].y, b1.y * vp[gi][1].y};
+        const float z0 = vp[gi][0].y - 8.0f, z1 = vp[gi][1].y - 8.0f;
+        float z[4] = {b0.x * z0, b0.y * z0, b1.x * z1, b1.y * z1};
         if (EDGE) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -485,6 +523,7 @@ struct Kv4Warp {
         zs[u][gi][1] += z[1] + z[3];
         wb[u][gi][0] = transpose_8x8(r0);
         wb[u][gi][1] = transpose_8x8(r1);
+        mma_16816(mid[u][gi], 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, wb[u][gi][0], wb[u][gi][1]);
       }
     }
     const uint2* vw = reinterpret_cast<const uint2*>(s + 8 * D) + lane;
@@ -501,8 +540,32 @@ struct Kv4Warp {
     }
   }
 
+  // Take 8 sum(w) off the accumulated codes (16 times that where codes count
+  // 16-fold): they then hold sum w (c - 8), which wanders about zero, while
+  // sum w c would grow with the context and the fp32 accumulators would drop
+  // bits of it at every step. Measured at 131072 tokens: relative error of the
+  // output against 64 bits 4.6e-3 without it, 1.7e-3 (bf16's own rounding) with it.
+  __device__ __forceinline__ void recentre() {
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int p = 0; p < NJ; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[u][p][0][i] += mid[u][p / JG][i];
+          o[u][p][1][i] = fmaf(16.0f, mid[u][p / JG][i], o[u][p][1][i]);
+        }
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mid[u][gi][i] = 0.0f;
+  }
+
   // Sums over the lanes of a column.
   __device__ __forceinline__ void finish() {
+    recentre();
 #pragma unroll
     for (int u = 0; u < NT; ++u)
 #pragma unroll
@@ -516,22 +579,26 @@ struct Kv4Warp {
       }
   }
 
-  // This warp's state into part (layout [8 NT][D + 2]: unnormalised output, m, l).
+  // The finished state of column 2 q + c of n-tile u: channel 32 p + 16 n + 8 h + g, unnormalised.
+  __device__ __forceinline__ float value(int u, int c, int p, int n, int h) const {
+    return fmaf(o[u][p][n][2 * h + c], n ? 1048576.0f : 16777216.0f, -zs[u][p / JG][c]);
+  }
+
+  // This warp's finished state into part (layout [8 NT][D + 4]: unnormalised output, m, l).
   __device__ __forceinline__ void store(float* part, int lane) const {
     const int g = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int u = 0; u < NT; ++u)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float* row = part + (8 * u + 2 * q + c) * (D + 2);
+        float* row = part + (8 * u + 2 * q + c) * (D + 4);
 #pragma unroll
         for (int p = 0; p < NJ; ++p)
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              row[32 * p + 16 * n + 8 * h + g] =
-                  fmaf(o[u][p][n][2 * h + c], n ? 1048576.0f : 16777216.0f, -zs[u][p / JG][c]);
+              row[32 * p + 16 * n + 8 * h + g] = value(u, c, p, n, h);
         if (g == 0) {
           row[D] = m[u][c];
           row[D + 1] = l[u][c];
@@ -540,14 +607,15 @@ struct Kv4Warp {
   }
 };
 
+constexpr int KV4_RECENTRE = 8;  // strips between recentre()s
 constexpr int KV4_WARPS = 4;
 
 // One block per (tile of 8 query rows, kv head, sequence); the warps take the
 // strips in turn and their states are joined at the end.
-template <int D, int G, bool F16>
+template <int D, int G>
 __global__ void __launch_bounds__(32 * KV4_WARPS) kv4_attention_tiles(const Kv4AttnArgs a) {
   using W = Kv4Warp<D, G, 1>;
-  __shared__ float part[KV4_WARPS][8 * (D + 2)];
+  __shared__ float part[KV4_WARPS][8 * (D + 4)];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.y, b = blockIdx.z;
   const Kv4Seq s = kv4_seq(a, b);
@@ -556,8 +624,9 @@ __global__ void __launch_bounds__(32 * KV4_WARPS) kv4_attention_tiles(const Kv4A
   if (bad && threadIdx.x == 0) atomicCAS(a.err, 0, ERR_KV4_PAGE);
   if (r0 >= rows) return;
   W w;
-  w.template load_queries<F16>(a, s, head, r0, lane);
+  w.load_queries(a, s, head, r0, lane);
   const int n_strips = (w.vis_max + 15) >> 4;
+  int done = 0;
   for (int i = warp; i < n_strips; i += KV4_WARPS) {
     const int t0 = 16 * i;
     const int page = __ldg(a.table + (long long)b * a.table_pages + (t0 >> a.c.page_shift));
@@ -571,20 +640,20 @@ __global__ void __launch_bounds__(32 * KV4_WARPS) kv4_attention_tiles(const Kv4A
       w.template strip<true>(a.c.base + off, t0, lane);
     else
       w.template strip<false>(a.c.base + off, t0, lane);
+    if (++done % KV4_RECENTRE == 0) w.recentre();
   }
   w.finish();
   w.store(part[warp], lane);
   __syncthreads();
-  using Ty = W4Type<F16>;
   for (int e = threadIdx.x; e < 8 * D; e += blockDim.x) {
     const int j = e / D, d = e - j * D;
     const long long r = r0 + j;
     if (r >= rows) break;
     float m = -INFINITY;
-    for (int k = 0; k < KV4_WARPS; ++k) m = fmaxf(m, part[k][j * (D + 2) + D]);
+    for (int k = 0; k < KV4_WARPS; ++k) m = fmaxf(m, part[k][j * (D + 4) + D]);
     float o = 0.0f, l = 0.0f;
     for (int k = 0; k < KV4_WARPS; ++k) {
-      const float* row = part[k] + j * (D + 2);
+      const float* row = part[k] + j * (D + 4);
       if (row[D] == -INFINITY && row[D + 1] == 0.0f) continue;
       const float f = exp2_fast(row[D] - m);
       o += f * row[d];
@@ -593,8 +662,448 @@ __global__ void __launch_bounds__(32 * KV4_WARPS) kv4_attention_tiles(const Kv4A
     const long long tok = s.row0 + r / a.share;
     const int qh = head * a.share + (int)(r % a.share);
     if (!AWQ_IDX_OK(tok, a.T, BS_KV4_O)) break;
-    static_cast<typename Ty::T*>(a.out)[(tok * a.q_heads + qh) * D + d] = Ty::from_float(l == 0.0f ? 0.0f : o / l);
+    static_cast<uint16_t*>(a.out)[(tok * a.q_heads + qh) * D + d] = kv4_narrow(a, l == 0.0f ? 0.0f : o / l);
     if (a.lse && d == 0) a.lse[tok * a.q_heads + qh] = l == 0.0f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
+  }
+}
+
+
+// ------------------------------------------------------------------ attention, split evenly over the GPU
+// Work is counted in units of one strip of one tile (8 NT query rows of one
+// sequence and kv head), ordered by sequence, head, tile, strip. Every warp of
+// the grid takes one contiguous range of equal length, whatever the contexts'
+// lengths, and streams its strips through a ring of its own in shared memory
+// (one cp.async.bulk a strip, issued KV4_STAGES ahead, across tiles too); no
+// warp waits for another until its range is done. A tile that lies in one
+// warp's range is written out by it; the at most two that it shares (its first
+// and its last) go to the workspace as (unnormalised output, m, l), are joined
+// within the block, and where they cross blocks by kv4_attention_join. All
+// joins run in the order of the ranges, so the result is the same every time.
+constexpr int KV4_MAX_BATCH = 1024;  // sequences of a launch: their unit counts sit in shared memory
+constexpr int KV4_CTAS = 148;        // blocks of the grid, one per SM
+constexpr int KV4_STAGES = 4;
+// Warps of a block: as many as their state lets have enough registers.
+constexpr int kv4_warps(int dim, int group, int nt) {
+  return dim * nt > 128 ? 8 : dim / group * nt <= (dim * nt <= 64 ? 2 : 1) ? 16 : 12;
+}
+
+struct Kv4SplitArgs {
+  Kv4AttnArgs a;
+  int tile_rows;    // 8 NT
+  float* warp_part; // [warps of the grid][2][8 NT][D + 4]
+  float* cta_part;  // [KV4_CTAS][2][8 NT][D + 4]
+  long long* cta_seg;  // [KV4_CTAS][2] tile of a block partial (-1: none)
+  int* cta_bad;     // [KV4_CTAS]
+  int clear_err;    // the first launch of a call sets the error word, later ones add to it
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+      "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Units of the batch: prefix[b] = units before sequence b, strips and tiles of each.
+struct Kv4Plan {
+  long long prefix[KV4_MAX_BATCH + 1];
+  int strips[KV4_MAX_BATCH], tiles[KV4_MAX_BATCH];
+  int bad;
+};
+
+// Filled by the whole block (a multiple of 32 threads, at least 32).
+__device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, long long* warp_sums) {
+  const Kv4AttnArgs& a = s.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (threadIdx.x == 0) {
+    p.prefix[0] = 0;
+    p.bad = 0;
+  }
+  __syncthreads();
+  long long before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    long long n = 0;
+    if (b < a.batch) {
+      const Kv4Seq q = kv4_seq(a, b);
+      if (q.bad) p.bad = 1;
+      const long long rows = (long long)q.n * a.share;
+      // a sequence without context still has its rows to write: one unit, which reads nothing
+      const int strips = q.n > 0 ? max(1, (int)(((long long)q.L + 15) >> 4)) : 0;
+      const int tiles = (int)((rows + s.tile_rows - 1) / s.tile_rows);
+      p.strips[b] = strips;
+      p.tiles[b] = tiles;
+      n = (long long)strips * tiles * a.c.heads;
+    }
+    long long inc = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += t;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) inc += warp_sums[w];
+    if (b < a.batch) p.prefix[b + 1] = before + inc;
+    for (int w = 0; w < warps; ++w) before += warp_sums[w];
+    __syncthreads();
+  }
+}
+
+// Workers that take part: at least KV4_MIN_STRIPS units each.
+constexpr int KV4_MIN_STRIPS = 4;
+__device__ __forceinline__ long long kv4_workers(long long units, long long most) {
+  const long long w = (units + KV4_MIN_STRIPS - 1) / KV4_MIN_STRIPS;
+  return w < most ? (w > 0 ? w : 1) : most;
+}
+__device__ __forceinline__ long long kv4_begin(long long w, long long workers, long long units) {
+  return w < workers ? w * units / workers : units;
+}
+
+// A place in the order of units.
+struct Kv4Cursor {
+  int b, strip, strips, tile, tiles, head;
+  __device__ __forceinline__ void seek(const Kv4Plan& p, int batch, long long u) {
+    int lo = 0, hi = batch;  // prefix[lo] <= u < prefix[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.prefix[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    strips = p.strips[b];
+    tiles = p.tiles[b];
+    const long long in = u - p.prefix[b], seg = in / strips;
+    strip = (int)(in - seg * strips);
+    head = (int)(seg / tiles);
+    tile = (int)(seg - (long long)head * tiles);
+  }
+  // to the next unit; true if it begins another tile
+  __device__ __forceinline__ bool step(const Kv4Plan& p, const Kv4AttnArgs& a) {
+    if (++strip < strips) return false;
+    strip = 0;
+    if (++tile == tiles) {
+      tile = 0;
+      if (++head == a.c.heads) {
+        head = 0;
+        do ++b;
+        while (b < a.batch && p.strips[b] == 0);
+        if (b < a.batch) {
+          strips = p.strips[b];
+          tiles = p.tiles[b];
+        }
+      }
+    }
+    return true;
+  }
+  __device__ __forceinline__ long long id(const Kv4AttnArgs& a) const {
+    return ((long long)b * a.c.heads + head) << 32 | (unsigned)tile;
+  }
+};
+
+// Query row r (in the sequence's n * share) of a kv head: its element offset in out, and in lse; -1 if there is none.
+__device__ __forceinline__ long long kv4_out_row(const Kv4AttnArgs& a, const Kv4Seq& s, int head, long long r) {
+  if (r >= (long long)s.n * a.share) return -1;
+  const long long tok = s.row0 + r / a.share;
+  if (!AWQ_IDX_OK(tok, a.T, BS_KV4_O)) return -1;
+  return tok * a.q_heads + head * a.share + (int)(r % a.share);
+}
+
+// Joins entries part(e), e in [e0, e1), of row `row` of a tile by one warp:
+// lane's channels 4 lane + 128 k. Returns m and l; v holds the unnormalised sums.
+template <int D>
+struct Kv4Joined {
+  static constexpr int K = (D + 127) / 128;
+  float4 v[K];
+  float m, l;
+  template <typename Part>
+  __device__ __forceinline__ void join(Part part, int e0, int e1, int row, int lane) {
+    m = -INFINITY;
+    for (int e = e0; e < e1; ++e) m = fmaxf(m, part(e)[row * (D + 4) + D]);
+    l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int e = e0; e < e1; ++e) {
+      const float* r = part(e) + row * (D + 4);
+      const float me = r[D], le = r[D + 1];
+      // a part that saw nothing holds m = -inf and zeros; NaN in l passes on
+      const float f = me == -INFINITY ? (le == 0.0f ? 0.0f : le) : exp2_fast(me - m);
+      l = fmaf(f, le, l);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = 4 * lane + 128 * k;
+        if (c < D) {
+          const float4 x = *reinterpret_cast<const float4*>(r + c);
+          v[k].x = fmaf(f, x.x, v[k].x);
+          v[k].y = fmaf(f, x.y, v[k].y);
+          v[k].z = fmaf(f, x.z, v[k].z);
+          v[k].w = fmaf(f, x.w, v[k].w);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* r, int lane) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (4 * lane + 128 * k < D) *reinterpret_cast<float4*>(r + 4 * lane + 128 * k) = v[k];
+    if (lane == 0) {
+      r[D] = m;
+      r[D + 1] = l;
+    }
+  }
+  __device__ __forceinline__ void write(const Kv4AttnArgs& a, long long at, int lane) const {
+    if (at < 0) return;
+    const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = 4 * lane + 128 * k;
+      if (c < D)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + c) =
+            a.f16 ? make_uint2(pack2<true>(v[k].x * inv, v[k].y * inv), pack2<true>(v[k].z * inv, v[k].w * inv))
+                  : make_uint2(pack2<false>(v[k].x * inv, v[k].y * inv), pack2<false>(v[k].z * inv, v[k].w * inv));
+    }
+    if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
+  }
+};
+
+template <int D, int G, int NT>
+struct Kv4SplitSmem {
+  static constexpr int W = kv4_warps(D, G, NT);
+  static constexpr int STRIP = kv4_strip_bytes(D, G);
+  alignas(128) uint8_t ring[W][KV4_STAGES][STRIP];
+  alignas(8) uint64_t bar[W][KV4_STAGES];
+  Kv4Plan plan;
+  long long sums[W];
+  long long seg[W][2];   // tile of a warp's first and last part (-1: none)
+  int flags[W][2];       // bit 0: the part begins its tile, bit 1: it ends it
+  int chain[2 * W + 1], chains, bad;
+  int abort;
+};
+
+template <int D, int G, int NT>
+__global__ void __launch_bounds__(32 * kv4_warps(D, G, NT), 1) kv4_attention_split(const __grid_constant__ Kv4SplitArgs s) {
+  using Sm = Kv4SplitSmem<D, G, NT>;
+  using St = Kv4Warp<D, G, NT>;
+  constexpr int W = Sm::W, PART = 8 * NT * (D + 4);
+  extern __shared__ uint8_t smem_raw[];
+  // (offset, not address, arithmetic keeps the accesses shared-memory ones)
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u));
+  const Kv4AttnArgs& a = s.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < KV4_STAGES; ++i) mbar_init(smem_u32(&sm.bar[warp][i]), 1);
+    fence_barrier_init();
+    sm.seg[warp][0] = sm.seg[warp][1] = -1;
+  }
+  if (threadIdx.x == 0) {
+    sm.bad = 0;
+    sm.abort = 0;
+  }
+  kv4_plan(s, sm.plan, sm.sums);
+  const long long units = sm.plan.prefix[a.batch];
+  const long long workers = kv4_workers(units, (long long)gridDim.x * W);
+  const long long me = (long long)blockIdx.x * W + warp;
+  const long long u0 = kv4_begin(me, workers, units), u1 = kv4_begin(me + 1, workers, units);
+  float* my_part = s.warp_part + me * 2 * PART;
+  if (u0 < u1) {
+    Kv4Cursor cur, ahead;
+    cur.seek(sm.plan, a.batch, u0);
+    ahead = cur;
+    const int page_mask = (1 << a.c.page_shift) - 1;
+    int left = (int)(u1 - u0), to_load = left;
+    unsigned have = 0;  // stages whose strip is there to be read
+    int win_b = -1, win_p = 0, win = 0;  // lane i: page win_p + i of sequence win_b
+    int ahead_len = a.lens[ahead.b];
+    auto issue = [&](int stage) {
+      const int t0 = 16 * ahead.strip, p = t0 >> a.c.page_shift;
+      if (ahead.b != win_b || p < win_p || p >= win_p + 32) {
+        win_b = ahead.b;
+        win_p = p;
+        win = p + lane < a.table_pages ? __ldg(a.table + (long long)ahead.b * a.table_pages + p + lane) : -1;
+        ahead_len = a.lens[ahead.b];
+      }
+      const int page = __shfl_sync(0xffffffffu, win, p - win_p);
+      const bool in = t0 < ahead_len, good = in && page >= 0 && page < a.c.n_pages;
+      bool copied = false;
+      if (good) {
+        const long long off = a.c.strip(page, ahead.head, t0 & page_mask);
+        if (AWQ_SPAN_OK(off, Sm::STRIP, a.c.bytes(), BS_KV4_STRIP)) {
+          copied = true;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&sm.bar[warp][stage]);
+            mbar_arrive_expect_tx(bar, Sm::STRIP);
+            bulk_load(smem_u32(sm.ring[warp][stage]), a.c.base + off, Sm::STRIP, bar);
+          }
+        }
+      } else if (in && lane == 0) {
+        sm.bad = ERR_KV4_PAGE;
+      }
+      have = copied ? have | (1u << stage) : have & ~(1u << stage);
+      --to_load;
+      if (to_load > 0) ahead.step(sm.plan, a);
+    };
+    for (int i = 0; i < KV4_STAGES && to_load > 0; ++i) issue(i);
+    St w;
+    int stage = 0;
+    unsigned phases = 0;
+    bool ok = true, begins = cur.strip == 0, first = true;
+    Kv4Seq seq = kv4_seq(a, cur.b);
+    w.load_queries(a, seq, cur.head, (long long)cur.tile * s.tile_rows, lane);
+    int done = 0;
+    while (ok) {
+      const int t0 = 16 * cur.strip;
+      if (have >> stage & 1u) {
+        ok = mbar_wait(smem_u32(&sm.bar[warp][stage]), phases >> stage & 1u, &sm.abort, nullptr, 0);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        phases ^= 1u << stage;
+        have &= ~(1u << stage);
+        if (t0 < w.vis_max) {
+          if (t0 + 16 > w.vis_min)
+            w.template strip<true>(sm.ring[warp][stage], t0, lane);
+          else
+            w.template strip<false>(sm.ring[warp][stage], t0, lane);
+          if (++done % KV4_RECENTRE == 0) w.recentre();
+        }
+      }
+      __syncwarp();
+      if (to_load > 0) issue(stage);
+      if (++stage == KV4_STAGES) stage = 0;
+      --left;
+      const bool ends = cur.strip + 1 == cur.strips;
+      if (ends || left == 0) {
+        w.finish();
+        if (begins && ends) {
+          // the whole tile: write it
+          const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const long long at = kv4_out_row(a, seq, cur.head, (long long)cur.tile * s.tile_rows + 8 * u + 2 * q + c);
+              if (at < 0) continue;
+              const float inv = w.l[u][c] == 0.0f ? 0.0f : __fdividef(1.0f, w.l[u][c]);
+              uint16_t* o = static_cast<uint16_t*>(a.out) + at * D + g;
+#pragma unroll
+              for (int p = 0; p < D / 32; ++p)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) o[32 * p + 16 * n + 8 * h] = kv4_narrow(a, w.value(u, c, p, n, h) * inv);
+              if (a.lse && g == 0)
+                a.lse[at] = w.l[u][c] == 0.0f ? -INFINITY : 0.69314718055994531f * (w.m[u][c] + log2f(w.l[u][c]));
+            }
+          __syncwarp();
+        } else {
+          const int k = first ? 0 : 1;
+          w.store(my_part + k * PART, lane);
+          if (lane == 0) {
+            sm.seg[warp][k] = cur.id(a);
+            sm.flags[warp][k] = (begins ? 1 : 0) | (ends ? 2 : 0);
+          }
+        }
+        first = false;
+        if (left == 0) break;
+      }
+      if (cur.step(sm.plan, a)) {
+        const int b = cur.b;
+        begins = true;
+        seq = kv4_seq(a, b);
+        w.load_queries(a, seq, cur.head, (long long)cur.tile * s.tile_rows, lane);
+        done = 0;
+      }
+    }
+    if (!ok) {
+      // a copy that never came: wait (bounded) for the others, report, write nothing
+      if (lane == 0) {
+        sm.bad = ERR_KV4_COPY;
+        for (int i = 0; i < KV4_STAGES; ++i)
+          if (have >> i & 1u) mbar_wait_drain(smem_u32(&sm.bar[warp][i]), phases >> i & 1u);
+      }
+      __syncwarp();
+    }
+  }
+  __threadfence_block();
+  __syncthreads();
+  // ---------------- join the warps' parts: chains of consecutive parts of one tile
+  if (threadIdx.x == 0) {
+    int n = 0;
+    long long last = -1;
+    for (int e = 0; e < 2 * W; ++e) {
+      const long long g = sm.seg[e >> 1][e & 1];
+      if (g < 0) continue;
+      if (g != last) sm.chain[n++] = e;
+      last = g;
+    }
+    sm.chain[n] = 2 * W;
+    sm.chains = n;
+    s.cta_bad[blockIdx.x] = sm.bad ? sm.bad : sm.plan.bad ? ERR_KV4_PAGE : 0;
+    s.cta_seg[2 * blockIdx.x] = s.cta_seg[2 * blockIdx.x + 1] = -1;
+  }
+  __syncthreads();
+  const float* base = s.warp_part + (long long)blockIdx.x * W * 2 * PART;
+  for (int it = warp; it < sm.chains * 8 * NT; it += W) {
+    const int ch = it / (8 * NT), row = it - ch * 8 * NT;
+    const int e0 = sm.chain[ch];
+    int entries = 0;
+    const long long seg = sm.seg[e0 >> 1][e0 & 1];
+    // a chain's parts: the first one, then the slot 0 of the following warps (a warp's slot 1 begins another tile)
+    int flags = 0;
+    for (int e = e0; e < sm.chain[ch + 1]; ++e)
+      if (sm.seg[e >> 1][e & 1] >= 0) {
+        flags |= sm.flags[e >> 1][e & 1];
+        ++entries;
+      }
+    Kv4Joined<D> j;
+    auto part = [&](int i) {
+      // the i-th part of the chain: e0, then warp (e0 / 2 + i), slot 0
+      const int e = i == 0 ? e0 : 2 * ((e0 >> 1) + i);
+      return base + (long long)e * PART;
+    };
+    j.join(part, 0, entries, row, lane);
+    if (flags == 3) {
+      const int head_b = (int)(seg >> 32), b = head_b / a.c.heads, head = head_b - b * a.c.heads;
+      const Kv4Seq seq = kv4_seq(a, b);
+      j.write(a, kv4_out_row(a, seq, head, (long long)(int)(seg & 0xffffffff) * s.tile_rows + row), lane);
+    } else {
+      // shared with other blocks: slot 1 if it begins here, else 0
+      const int k = flags & 1;
+      j.store(s.cta_part + ((long long)blockIdx.x * 2 + k) * PART + row * (D + 4), lane);
+      if (row == 0 && lane == 0) s.cta_seg[2 * blockIdx.x + k] = seg;
+    }
+  }
+}
+
+// Block c joins the tile that block c of the split began and did not end:
+// its slot 1, then slot 0 of the following blocks while they hold that tile.
+// Block 0 sets the call's error word.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) kv4_attention_join(const __grid_constant__ Kv4SplitArgs s, int ctas) {
+  constexpr int PART = 8 * NT * (D + 4);
+  const Kv4AttnArgs& a = s.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
+  if (c == 0 && threadIdx.x < 32) {
+    int bad = 0;
+    for (int i = lane; i < ctas; i += 32) bad = max(bad, s.cta_bad[i]);
+    bad = __reduce_max_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      if (s.clear_err) *a.err = bad;
+      else if (bad) *a.err = bad;
+    }
+  }
+  const long long seg = s.cta_seg[2 * c + 1];
+  if (seg < 0) return;
+  int n = 1;
+  while (c + n < ctas && s.cta_seg[2 * (c + n)] == seg) ++n;
+  const int head_b = (int)(seg >> 32), b = head_b / a.c.heads, head = head_b - b * a.c.heads;
+  const Kv4Seq seq = kv4_seq(a, b);
+  for (int row = warp; row < 8 * NT; row += 8) {
+    const long long at = kv4_out_row(a, seq, head, (long long)(int)(seg & 0xffffffff) * s.tile_rows + row);
+    if (at < 0) continue;
+    Kv4Joined<D> j;
+    j.join([&](int i) { return s.cta_part + ((long long)(c + i) * 2 + (i == 0)) * PART; }, 0, n, row, lane);
+    j.write(a, at, lane);
   }
 }
 

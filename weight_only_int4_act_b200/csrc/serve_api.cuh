@@ -142,7 +142,29 @@ awq_status check_kv4_attention(int64_t batch, int64_t n_q_heads, int64_t max_q, 
   return AWQ_OK;
 }
 
-size_t kv4_attention_ws(int64_t, int64_t, int64_t, const awq_kv4cfg*) { return kAlign; }
+// Workspace of the attention: [0, kAlign) error word, then the block flags and
+// tiles and the partial outputs of blocks and warps.
+struct Kv4Layout {
+  int nt, warps;
+  bool split;
+  size_t off_bad, off_seg, off_cta, off_warp, total;
+};
+
+Kv4Layout kv4_layout(int64_t n_q_heads, int64_t max_q, const awq_kv4cfg* c) {
+  Kv4Layout L{};
+  const long long rows = max_q * (n_q_heads / c->n_kv_heads);
+  L.nt = rows > 8 && c->head_dim <= 128 ? 2 : 1;
+  L.split = rows <= 64;
+  L.warps = kv4_warps(c->head_dim, c->group, L.nt);
+  const size_t part = (size_t)8 * L.nt * (c->head_dim + 4) * sizeof(float);
+  size_t off = kAlign;
+  L.off_bad = off;   off += align_up(KV4_CTAS * sizeof(int));
+  L.off_seg = off;   off += align_up(KV4_CTAS * 2 * sizeof(long long));
+  L.off_cta = off;   off += align_up(KV4_CTAS * 2 * part);
+  L.off_warp = off;  off += align_up((size_t)KV4_CTAS * L.warps * 2 * part);
+  L.total = L.split ? off : kAlign;
+  return L;
+}
 
 // One launch per (head dimension, group); f is called with the two as constants.
 template <typename F>
@@ -297,7 +319,7 @@ extern "C" awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const i
 extern "C" size_t awq_kv4_attention_workspace_size(int64_t batch, int64_t n_q_heads, int64_t max_q,
                                                    const awq_kv4cfg* cfg) {
   if (check_kv4_attention(batch, n_q_heads, max_q, cfg) != AWQ_OK) return 0;
-  return kv4_attention_ws(batch, n_q_heads, max_q, cfg);
+  return kv4_layout(n_q_heads, max_q, cfg).total;
 }
 
 extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t q_tok, int64_t q_head, int64_t T,
@@ -316,7 +338,8 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_start, 4) ||
       !aligned(lse, 4) || !aligned(ws, 256))
     return AWQ_ERR_INVALID_ARG;
-  if (ws_bytes < kv4_attention_ws(batch, n_q_heads, max_q, cfg)) return AWQ_ERR_WORKSPACE;
+  const Kv4Layout L = kv4_layout(n_q_heads, max_q, cfg);
+  if (ws_bytes < L.total) return AWQ_ERR_WORKSPACE;
   if ((st = check_device(nullptr)) != AWQ_OK) return st;
   cudaStream_t cs = as_stream(stream);
   Kv4AttnArgs a{};
@@ -333,20 +356,51 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   a.lens = lens;
   a.batch = (int)batch;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.f16 = dtype == AWQ_DTYPE_F16;
   a.c = kv4_cache(cfg, cache, n_pages);
   a.out = out;
   a.lse = lse;
   a.err = at<int>(ws, 0);
+  if (L.split) {
+    Kv4SplitArgs sa{};
+    sa.tile_rows = 8 * L.nt;
+    sa.warp_part = at<float>(ws, L.off_warp);
+    sa.cta_part = at<float>(ws, L.off_cta);
+    sa.cta_seg = at<long long>(ws, L.off_seg);
+    sa.cta_bad = at<int>(ws, L.off_bad);
+    for (int64_t first = 0; first < batch; first += KV4_MAX_BATCH) {
+      sa.a = a;
+      sa.a.batch = (int)(batch - first < KV4_MAX_BATCH ? batch - first : KV4_MAX_BATCH);
+      sa.a.table += first * table_pages;
+      sa.a.lens += first;
+      if (q_start) sa.a.q_start += first;
+      sa.a.row_first = (int)first;
+      sa.clear_err = first == 0;
+      st = kv4_shapes(cfg->head_dim, cfg->group, [&](auto d, auto g) -> awq_status {
+        constexpr int D = decltype(d)::value, G = decltype(g)::value;
+        auto launch = [&](auto nt) -> awq_status {
+          constexpr int NT = decltype(nt)::value;
+          constexpr int smem = (int)sizeof(Kv4SplitSmem<D, G, NT>) + 128;
+          static_assert(smem <= 232448, "shared memory of the split attention");
+          auto k = kv4_attention_split<D, G, NT>;
+          if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return AWQ_ERR_CUDA;
+          k<<<KV4_CTAS, 32 * kv4_warps(D, G, NT), smem, cs>>>(sa);
+          kv4_attention_join<D, NT><<<KV4_CTAS, 256, 0, cs>>>(sa, KV4_CTAS);
+          return launch_status();
+        };
+        return L.nt == 2 ? launch(std::integral_constant<int, D <= 128 ? 2 : 1>{}) : launch(std::integral_constant<int, 1>{});
+      });
+      if (st != AWQ_OK) return st;
+    }
+    return AWQ_OK;
+  }
   if (cudaMemsetAsync(ws, 0, sizeof(int), cs) != cudaSuccess) return AWQ_ERR_CUDA;
   const long long tiles = cdiv(max_q * a.share, 8);
   if (tiles > INT32_MAX) return AWQ_ERR_SHAPE;
   const dim3 grid((unsigned)tiles, (unsigned)cfg->n_kv_heads, (unsigned)batch);
   return kv4_shapes(cfg->head_dim, cfg->group, [&](auto d, auto g) {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    if (dtype == AWQ_DTYPE_F16)
-      kv4_attention_tiles<D, G, true><<<grid, 32 * KV4_WARPS, 0, cs>>>(a);
-    else
-      kv4_attention_tiles<D, G, false><<<grid, 32 * KV4_WARPS, 0, cs>>>(a);
+    kv4_attention_tiles<D, G><<<grid, 32 * KV4_WARPS, 0, cs>>>(a);
     return launch_status();
   });
 }
