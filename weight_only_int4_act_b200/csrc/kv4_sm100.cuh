@@ -252,8 +252,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ float exp2_fast(float x) { return exp2f(x); }
-
 // N consecutive words at p, aligned to the largest power of two that divides 4 N (at most 16).
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
@@ -275,20 +273,34 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
+// 2^x, at most 2 units off; -inf gives 0
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr int KV4_UNIT = 32;       // tokens a warp takes at a time: two strips
+constexpr int KV4_RECENTRE = 4;    // units between recentre()s
+constexpr float KV4_LOWEST = -1.7e38f;  // reference exponent of a part that saw no token
+
 // What a warp knows of a tile of 8 NT query rows of one (sequence, kv head).
 // Column j of n-tile u is row 8 u + j of the tile; a lane works on columns
 // 2 q and 2 q + 1 of each n-tile.
 template <int D, int G, int NT>
 struct Kv4Warp {
   static constexpr int NJ = D / 32, NG = D / G, JG = G / 32;
+  static constexpr int STRIP = kv4_strip_bytes(D, G);
+  // strips worked on at once: two hide each other's latencies where there are registers for it
+  static constexpr int NS = D * NT <= 128 && NG * NT <= 3 ? 2 : 1;
   uint32_t qf[NT][NJ][4];      // B operands: queries, even channels then odd ones (times 2^-4)
   float qsum[NT][NG][2];       // 2^-24 sum of the scaled query over a group, columns 2 q, 2 q + 1
   float qscale[NT][2];         // score (log2) per accumulator unit
   int vis[NT][2];              // keys [0, vis) are visible to the column's query
   int vis_min, vis_max;        // over the tile's rows
+  bool fresh;                  // no tokens yet: the first ones set the reference
   float o[NT][NJ][2][4];       // accumulators: channels 32 p + 16 n + ..., value 2^-24 (n = 0) or 2^-20 units
-  float mid[NT][NG][4];        // -8 2^-24 sum of w since the last recentre(), in every row
-  float zs[NT][NG][2];         // sum of w (zero - 8) over this lane's tokens
+  float mid[NT][NG][4];        // -2^-24 sum of w zero since the last recentre(), in every row
   float m[NT][2], l[NT][2];    // reference exponent (the same in all lanes of a column), sum of p over this lane's tokens
 
   // Rows [r0, r0 + 8 NT) of the sequence's n * share query rows (row = token * share + head in the group).
@@ -323,7 +335,7 @@ struct Kv4Warp {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // Scale the row by a power of two so that its largest entry lies in
-      // [2^10, 2^11): fp16 then holds every entry down to 2^-21 of it to 11
+      // [2^10, 2^11): fp16 then holds every entry down to 2^-20 of it to 11
       // bits, also the odd channels' 2^-4. Exact back through the scale.
       const int ex = top > 0.0f ? min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -110), 127) : 0;
       const float f1 = __uint_as_float((uint32_t)(127 + (10 - ex) / 2) << 23);
@@ -363,7 +375,7 @@ struct Kv4Warp {
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi)
           qsum[u][gi][c] = __shfl_sync(0xffffffffu, part[gi], from) * 5.9604644775390625e-8f;
-        m[u][c] = -INFINITY;
+        m[u][c] = 0.0f;
         l[u][c] = 0.0f;
       }
       if (in) {
@@ -371,15 +383,9 @@ struct Kv4Warp {
         vis_max = max(vis_max, see);
       }
     }
-#pragma unroll
-    for (int o_ = 4; o_ < 32; o_ <<= 1) {
-      vis_min = min(vis_min, __shfl_xor_sync(0xffffffffu, vis_min, o_));
-      vis_max = max(vis_max, __shfl_xor_sync(0xffffffffu, vis_max, o_));
-    }
-    clear();
-  }
-
-  __device__ __forceinline__ void clear() {
+    fresh = true;
+    vis_min = __reduce_min_sync(0xffffffffu, vis_min);
+    vis_max = __reduce_max_sync(0xffffffffu, vis_max);
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
 #pragma unroll
@@ -389,159 +395,227 @@ struct Kv4Warp {
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[u][p][n][i] = 0.0f;
 #pragma unroll
-      for (int gi = 0; gi < NG; ++gi) {
-        zs[u][gi][0] = zs[u][gi][1] = 0.0f;
+      for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
         for (int i = 0; i < 4; ++i) mid[u][gi][i] = 0.0f;
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        m[u][c] = -INFINITY;
-        l[u][c] = 0.0f;
-      }
     }
   }
 
-  // One strip: tokens t0 .. t0 + 15 of the context, its bytes at `s`. EDGE:
-  // some of the tile's queries do not see all of its tokens, whose bytes may
-  // hold anything then.
-  template <bool EDGE>
-  __device__ __forceinline__ void strip(const uint8_t* s, int t0, int lane) {
-    const int g = lane >> 2, q = lane & 3;
-    uint32_t kw0[NJ], kw1[NJ];
-    load_words<NJ>(s + g * (D / 2) + 4 * q * NJ, kw0);
-    load_words<NJ>(s + (g + 8) * (D / 2) + 4 * q * NJ, kw1);
-    const uint32_t* kpar = reinterpret_cast<const uint32_t*>(s + 16 * D);
-    const uint32_t* vpar = kpar + 16 * NG;
-    // scores: token rows g and g + 8, columns 2 q and 2 q + 1
-    float sc[NT][4];
+  // Reference exponents that admit these scores (d: score - m; dv: value
+  // steps of the lane's two tokens a strip): the largest score plus the
+  // exponent of its token's value step, so that w = p step <= 2 whatever the
+  // steps are. Moves d along. Taken for a tile's first tokens and then only
+  // when a weight passes 2^8. (A column that sees none of a tile's first tokens
+  // sees none of the later ones either: rows see a prefix of the context.)
+  template <int N>
+  __device__ __forceinline__ void raise(float (&d)[N][NT][4], const float (&dv)[N][NG][2]) {
+    float e[N][2];
 #pragma unroll
-    for (int gi = 0; gi < NG; ++gi) {
-      float acc[NT][4];
+    for (int s = 0; s < N; ++s)
 #pragma unroll
-      for (int u = 0; u < NT; ++u)
+      for (int h = 0; h < 2; ++h) {
+        float x = dv[s][0][h];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[u][i] = 0.0f;
-#pragma unroll
-      for (int jj = 0; jj < JG; ++jj) {
-        const int j = gi * JG + jj;
-        const uint32_t w0 = kw0[j], w1 = kw1[j], v0 = w0 >> 8, v1 = w1 >> 8;
-#pragma unroll
-        for (int u = 0; u < NT; ++u) {
-          mma_16816(acc[u], w0 & 0x000F000Fu, w1 & 0x000F000Fu, v0 & 0x000F000Fu, v1 & 0x000F000Fu, qf[u][j][0], qf[u][j][1]);
-          mma_16816(acc[u], w0 & 0x00F000F0u, w1 & 0x00F000F0u, v0 & 0x00F000F0u, v1 & 0x00F000F0u, qf[u][j][2], qf[u][j][3]);
-        }
+        for (int gi = 1; gi < NG; ++gi) x = fmaxf(x, dv[s][gi][h]);
+        e[s][h] = (float)((int)(__float_as_uint(x) >> 23) - 127);
       }
-      const float2 p0 = widen2<true>(kpar[16 * gi + g]), p1 = widen2<true>(kpar[16 * gi + 8 + g]);
-#pragma unroll
-      for (int u = 0; u < NT; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 p = i < 2 ? p0 : p1;
-          const float x = p.x * fmaf(-p.y, qsum[u][gi][i & 1], acc[u][i]);
-          sc[u][i] = gi == 0 ? x : sc[u][i] + x;
-        }
-    }
-    // the exponent of the value step joins the running reference, so that
-    // w = p step stays below 2^9 whatever the steps are
-    float2 vp[NG][2];
-    int e0 = -1000, e1 = -1000;
-#pragma unroll
-    for (int gi = 0; gi < NG; ++gi) {
-      vp[gi][0] = widen2<true>(vpar[16 * gi + g]);
-      vp[gi][1] = widen2<true>(vpar[16 * gi + 8 + g]);
-      e0 = max(e0, (int)(__float_as_uint(vp[gi][0].x) >> 23) - 127);
-      e1 = max(e1, (int)(__float_as_uint(vp[gi][1].x) >> 23) - 127);
-    }
-    const float ve[2] = {(float)e0, (float)e1};
-    bool grow = false;
 #pragma unroll
     for (int u = 0; u < NT; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sc[u][i] *= qscale[u][i & 1];
-        if (EDGE && t0 + g + 8 * (i >> 1) >= vis[u][i & 1]) sc[u][i] = -INFINITY;
-        grow |= sc[u][i] + ve[i >> 1] > m[u][i & 1] + 8.0f;
+      for (int c = 0; c < 2; ++c) {
+        float up = fresh ? -INFINITY : 0.0f;
+#pragma unroll
+        for (int s = 0; s < N; ++s) up = fmaxf(up, fmaxf(d[s][u][c] + e[s][0], d[s][u][c + 2] + e[s][1]));
+        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
+        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
+        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
+        if (up == -INFINITY) up = 0.0f;
+        // (d moves by what m really moved)
+        const float mn = m[u][c] + up, by = mn - m[u][c], f = exp2_fast(-by);
+        m[u][c] = mn;
+        l[u][c] *= f;
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+          mid[u][gi][c] *= f;
+          mid[u][gi][c + 2] *= f;
+        }
+#pragma unroll
+        for (int p = 0; p < NJ; ++p)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            o[u][p][n][c] *= f;
+            o[u][p][n][c + 2] *= f;
+          }
+#pragma unroll
+        for (int s = 0; s < N; ++s) {
+          d[s][u][c] -= by;
+          d[s][u][c + 2] -= by;
+        }
       }
-    if (__any_sync(0xffffffffu, grow)) {
+    fresh = false;
+  }
+
+  // N strips at `base`, tokens t0 .. of the context. EDGE: some of the tile's
+  // queries do not see all of the tokens, whose bytes may hold anything then;
+  // drop: strips (by bit) that are left out.
+  template <bool EDGE, int N>
+  __device__ __forceinline__ void strips(const uint8_t* base, int t0, unsigned drop, int lane) {
+    const int g = lane >> 2, q = lane & 3;
+    // scores: token rows g and g + 8 of a strip, columns 2 q and 2 q + 1
+    float d[N][NT][4];
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+      const uint8_t* b = base + s * STRIP;
+      uint32_t kw0[NJ], kw1[NJ];
+      load_words<NJ>(b + g * (D / 2) + 4 * q * NJ, kw0);
+      load_words<NJ>(b + (g + 8) * (D / 2) + 4 * q * NJ, kw1);
+      const uint32_t* kpar = reinterpret_cast<const uint32_t*>(b + 16 * D) + g;
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) {
+        float acc[NT][4];
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[u][i] = 0.0f;
+#pragma unroll
+        for (int jj = 0; jj < JG; ++jj) {
+          const int j = gi * JG + jj;
+          const uint32_t w0 = kw0[j], w1 = kw1[j], v0 = w0 >> 8, v1 = w1 >> 8;
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            mma_16816(acc[u], w0 & 0x000F000Fu, w1 & 0x000F000Fu, v0 & 0x000F000Fu, v1 & 0x000F000Fu, qf[u][j][0], qf[u][j][1]);
+            mma_16816(acc[u], w0 & 0x00F000F0u, w1 & 0x00F000F0u, v0 & 0x00F000F0u, v1 & 0x00F000F0u, qf[u][j][2], qf[u][j][3]);
+          }
+        }
+        const float2 p0 = widen2<true>(kpar[16 * gi]), p1 = widen2<true>(kpar[16 * gi + 8]);
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 p = i < 2 ? p0 : p1;
+            const float x = fmaf(-p.y, qsum[u][gi][i & 1], acc[u][i]);
+            d[s][u][i] = gi == 0 ? (NG == 1 ? fmaf(x, p.x * qscale[u][i & 1], -m[u][i & 1]) : x * p.x)
+                                 : fmaf(x, p.x, d[s][u][i]);
+          }
+      }
+      if (NG > 1) {
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[s][u][i] = fmaf(d[s][u][i], qscale[u][i & 1], -m[u][i & 1]);
+      }
+    }
+    // value steps of tokens g and g + 8, zeros (as codes, negative) of tokens
+    // 2 q, 2 q + 1 and 2 q + 8, 2 q + 9: an A operand whose 16 rows are alike
+    float dv[N][NG][2];
+    uint32_t zc[N][NG][2];
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+      const uint32_t* vpar = reinterpret_cast<const uint32_t*>(base + s * STRIP + 16 * D) + 16 * NG;
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          dv[s][gi][h] = __low2float(*reinterpret_cast<const __half2*>(vpar + 16 * gi + 8 * h + g));
+          const uint2 pz = *reinterpret_cast<const uint2*>(vpar + 16 * gi + 8 * h + 2 * q);
+          uint32_t z = __byte_perm(pz.x, pz.y, 0x7632);
+          if (EDGE) {
+            const __half2 ok = __hmin2(__hmax2(*reinterpret_cast<const __half2*>(&z), __float2half2_rn(0.0f)),
+                                       __float2half2_rn(15.0f));
+            z = *reinterpret_cast<const uint32_t*>(&ok);
+          }
+          const uint32_t unit = 0x80018001u;  // -2^-24 twice
+          const __half2 zz = __hmul2(*reinterpret_cast<const __half2*>(&z), *reinterpret_cast<const __half2*>(&unit));
+          zc[s][gi][h] = *reinterpret_cast<const uint32_t*>(&zz);
+        }
+    }
+    bool hidden[N][NT][4];
+#pragma unroll
+    for (int s = 0; s < N; ++s)
 #pragma unroll
       for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float top = fmaxf(sc[u][c] + ve[0], sc[u][c + 2] + ve[1]);
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          const float mn = fmaxf(m[u][c], top);
-          const float f = m[u][c] == -INFINITY ? 0.0f : exp2_fast(m[u][c] - mn);
-          m[u][c] = mn;
-          l[u][c] *= f;
-#pragma unroll
-          for (int gi = 0; gi < NG; ++gi) {
-            zs[u][gi][c] *= f;
-            mid[u][gi][c] *= f;
-            mid[u][gi][c + 2] *= f;
-          }
-#pragma unroll
-          for (int p = 0; p < NJ; ++p)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              o[u][p][n][c] *= f;
-              o[u][p][n][c + 2] *= f;
-            }
-        }
-    }
-    uint32_t wb[NT][NG][2];
-#pragma unroll
-    for (int u = 0; u < NT; ++u) {
-      float p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float ref = m[u][i & 1];
-        p[i] = exp2_fast(sc[u][i] - (ref == -INFINITY ? 0.0f : ref));
-      }
-      l[u][0] += p[0] + p[2];
-      l[u][1] += p[1] + p[3];
-#pragma unroll
-      for (int gi = 0; gi < NG; ++gi) {
-        float w[4];
-#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          w[i] = p[i] * vp[gi][i >> 1].x;
-          if (EDGE && t0 + g + 8 * (i >> 1) >= vis[u][i & 1]) w[i] = 0.0f;
+          hidden[s][u][i] = EDGE && (t0 + 16 * s + g + 8 * (i >> 1) >= vis[u][i & 1] || (drop >> s & 1u));
+          if (hidden[s][u][i]) d[s][u][i] = -INFINITY;
         }
-        const uint32_t r0 = pack2<true>(w[0], w[1]), r1 = pack2<true>(w[2], w[3]);
-        const float2 b0 = widen2<true>(r0), b1 = widen2<true>(r1);  // the rounded weights, which the codes meet too
-        const float z0 = vp[gi][0].y - 8.0f, z1 = vp[gi][1].y - 8.0f;
-        float z[4] = {b0.x * z0, b0.y * z0, b1.x * z1, b1.y * z1};
-        if (EDGE) {
+    float w[N][NT][NG][4];
+    float p[N][NT][4];
+    auto weigh = [&]() {
+      bool big = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (t0 + g + 8 * (i >> 1) >= vis[u][i & 1]) z[i] = 0.0f;
-        }
-        zs[u][gi][0] += z[0] + z[2];
-        zs[u][gi][1] += z[1] + z[3];
-        wb[u][gi][0] = transpose_8x8(r0);
-        wb[u][gi][1] = transpose_8x8(r1);
-        mma_16816(mid[u][gi], 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, wb[u][gi][0], wb[u][gi][1]);
-      }
+      for (int s = 0; s < N; ++s)
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[s][u][i] = exp2_fast(d[s][u][i]);
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) {
+              const float x = p[s][u][i] * dv[s][gi][i >> 1];
+              w[s][u][gi][i] = hidden[s][u][i] ? 0.0f : x;
+              big |= w[s][u][gi][i] > 256.0f;
+            }
+          }
+      return fresh || __any_sync(0xffffffffu, big);
+    };
+    if (weigh()) {
+      raise<N>(d, dv);
+      weigh();
     }
-    const uint2* vw = reinterpret_cast<const uint2*>(s + 8 * D) + lane;
+    uint32_t wb[N][NT][NG][2];
 #pragma unroll
-    for (int p = 0; p < NJ; ++p) {
-      const uint2 w = vw[32 * p];
-      const uint32_t x = w.x >> 8, y = w.y >> 8;
+    for (int s = 0; s < N; ++s)
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        const uint32_t b0 = wb[u][p / JG][0], b1 = wb[u][p / JG][1];
-        mma_16816(o[u][p][0], w.x & 0x000F000Fu, w.y & 0x000F000Fu, x & 0x000F000Fu, y & 0x000F000Fu, b0, b1);
-        mma_16816(o[u][p][1], w.x & 0x00F000F0u, w.y & 0x00F000F0u, x & 0x00F000F0u, y & 0x00F000F0u, b0, b1);
+        l[u][0] += p[s][u][0] + p[s][u][2];
+        l[u][1] += p[s][u][1] + p[s][u][3];
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+          const float(&x)[4] = w[s][u][gi];
+          wb[s][u][gi][0] = transpose_8x8(pack2<true>(x[0], x[1]));
+          wb[s][u][gi][1] = transpose_8x8(pack2<true>(x[2], x[3]));
+          mma_16816(mid[u][gi], zc[s][gi][0], zc[s][gi][0], zc[s][gi][1], zc[s][gi][1], wb[s][u][gi][0], wb[s][u][gi][1]);
+        }
+      }
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+      const uint2* vw = reinterpret_cast<const uint2*>(base + s * STRIP + 8 * D) + lane;
+#pragma unroll
+      for (int pp = 0; pp < NJ; ++pp) {
+        const uint2 c = vw[32 * pp];
+        const uint32_t x = c.x >> 8, y = c.y >> 8;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          const uint32_t b0 = wb[s][u][pp / JG][0], b1 = wb[s][u][pp / JG][1];
+          mma_16816(o[u][pp][0], c.x & 0x000F000Fu, c.y & 0x000F000Fu, x & 0x000F000Fu, y & 0x000F000Fu, b0, b1);
+          mma_16816(o[u][pp][1], c.x & 0x00F000F0u, c.y & 0x00F000F0u, x & 0x00F000F0u, y & 0x00F000F0u, b0, b1);
+        }
       }
     }
   }
 
-  // Take 8 sum(w) off the accumulated codes (16 times that where codes count
-  // 16-fold): they then hold sum w (c - 8), which wanders about zero, while
+  // One unit (two strips) at `base`, tokens t0 .. t0 + 31.
+  __device__ __forceinline__ void unit(const uint8_t* base, int t0, unsigned drop, int lane) {
+    if constexpr (NS == 2) {
+      if (t0 + 32 > vis_min || drop)
+        strips<true, 2>(base, t0, drop, lane);
+      else
+        strips<false, 2>(base, t0, 0, lane);
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < 2; ++s) {
+        if (t0 + 16 * s >= vis_max) break;
+        if (t0 + 16 * s + 16 > vis_min || drop)
+          strips<true, 1>(base + s * STRIP, t0 + 16 * s, drop >> s, lane);
+        else
+          strips<false, 1>(base + s * STRIP, t0 + 16 * s, 0, lane);
+      }
+    }
+  }
+
+  // Take sum(w zero) off the accumulated codes (16 times that where codes count
+  // 16-fold): they then hold sum w (c - zero), which wanders about zero, while
   // sum w c would grow with the context and the fp32 accumulators would drop
   // bits of it at every step. Measured at 131072 tokens: relative error of the
   // output against 64 bits 4.6e-3 without it, 1.7e-3 (bf16's own rounding) with it.
@@ -569,19 +643,14 @@ struct Kv4Warp {
 #pragma unroll
     for (int u = 0; u < NT; ++u)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          l[u][c] += __shfl_xor_sync(0xffffffffu, l[u][c], d);
-#pragma unroll
-          for (int gi = 0; gi < NG; ++gi) zs[u][gi][c] += __shfl_xor_sync(0xffffffffu, zs[u][gi][c], d);
-        }
-      }
+        for (int d = 4; d < 32; d <<= 1) l[u][c] += __shfl_xor_sync(0xffffffffu, l[u][c], d);
   }
 
   // The finished state of column 2 q + c of n-tile u: channel 32 p + 16 n + 8 h + g, unnormalised.
   __device__ __forceinline__ float value(int u, int c, int p, int n, int h) const {
-    return fmaf(o[u][p][n][2 * h + c], n ? 1048576.0f : 16777216.0f, -zs[u][p / JG][c]);
+    return o[u][p][n][2 * h + c] * (n ? 1048576.0f : 16777216.0f);
   }
 
   // This warp's finished state into part (layout [8 NT][D + 4]: unnormalised output, m, l).
@@ -597,100 +666,42 @@ struct Kv4Warp {
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              row[32 * p + 16 * n + 8 * h + g] = value(u, c, p, n, h);
+            for (int h = 0; h < 2; ++h) row[32 * p + 16 * n + 8 * h + g] = value(u, c, p, n, h);
         if (g == 0) {
-          row[D] = m[u][c];
+          row[D] = l[u][c] == 0.0f ? KV4_LOWEST : m[u][c];
           row[D + 1] = l[u][c];
         }
       }
   }
 };
 
-constexpr int KV4_RECENTRE = 8;  // strips between recentre()s
-constexpr int KV4_WARPS = 4;
-
-// One block per (tile of 8 query rows, kv head, sequence); the warps take the
-// strips in turn and their states are joined at the end.
-template <int D, int G>
-__global__ void __launch_bounds__(32 * KV4_WARPS) kv4_attention_tiles(const Kv4AttnArgs a) {
-  using W = Kv4Warp<D, G, 1>;
-  __shared__ float part[KV4_WARPS][8 * (D + 4)];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = blockIdx.y, b = blockIdx.z;
-  const Kv4Seq s = kv4_seq(a, b);
-  bool bad = s.bad;
-  const long long r0 = 8ll * blockIdx.x, rows = (long long)s.n * a.share;
-  if (bad && threadIdx.x == 0) atomicCAS(a.err, 0, ERR_KV4_PAGE);
-  if (r0 >= rows) return;
-  W w;
-  w.load_queries(a, s, head, r0, lane);
-  const int n_strips = (w.vis_max + 15) >> 4;
-  int done = 0;
-  for (int i = warp; i < n_strips; i += KV4_WARPS) {
-    const int t0 = 16 * i;
-    const int page = __ldg(a.table + (long long)b * a.table_pages + (t0 >> a.c.page_shift));
-    if (page < 0 || page >= a.c.n_pages) {
-      if (lane == 0) atomicCAS(a.err, 0, ERR_KV4_PAGE);
-      continue;
-    }
-    const long long off = a.c.strip(page, head, t0 & ((1 << a.c.page_shift) - 1));
-    if (!AWQ_SPAN_OK(off, a.c.strip_bytes, a.c.bytes(), BS_KV4_STRIP)) continue;
-    if (t0 + 16 > w.vis_min)
-      w.template strip<true>(a.c.base + off, t0, lane);
-    else
-      w.template strip<false>(a.c.base + off, t0, lane);
-    if (++done % KV4_RECENTRE == 0) w.recentre();
-  }
-  w.finish();
-  w.store(part[warp], lane);
-  __syncthreads();
-  for (int e = threadIdx.x; e < 8 * D; e += blockDim.x) {
-    const int j = e / D, d = e - j * D;
-    const long long r = r0 + j;
-    if (r >= rows) break;
-    float m = -INFINITY;
-    for (int k = 0; k < KV4_WARPS; ++k) m = fmaxf(m, part[k][j * (D + 4) + D]);
-    float o = 0.0f, l = 0.0f;
-    for (int k = 0; k < KV4_WARPS; ++k) {
-      const float* row = part[k] + j * (D + 4);
-      if (row[D] == -INFINITY && row[D + 1] == 0.0f) continue;
-      const float f = exp2_fast(row[D] - m);
-      o += f * row[d];
-      l += f * row[D + 1];
-    }
-    const long long tok = s.row0 + r / a.share;
-    const int qh = head * a.share + (int)(r % a.share);
-    if (!AWQ_IDX_OK(tok, a.T, BS_KV4_O)) break;
-    static_cast<uint16_t*>(a.out)[(tok * a.q_heads + qh) * D + d] = kv4_narrow(a, l == 0.0f ? 0.0f : o / l);
-    if (a.lse && d == 0) a.lse[tok * a.q_heads + qh] = l == 0.0f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
-  }
-}
-
-
 // ------------------------------------------------------------------ attention, split evenly over the GPU
-// Work is counted in units of one strip of one tile (8 NT query rows of one
-// sequence and kv head), ordered by sequence, head, tile, strip. Every warp of
-// the grid takes one contiguous range of equal length, whatever the contexts'
-// lengths, and streams its strips through a ring of its own in shared memory
-// (one cp.async.bulk a strip, issued KV4_STAGES ahead, across tiles too); no
-// warp waits for another until its range is done. A tile that lies in one
-// warp's range is written out by it; the at most two that it shares (its first
-// and its last) go to the workspace as (unnormalised output, m, l), are joined
-// within the block, and where they cross blocks by kv4_attention_join. All
-// joins run in the order of the ranges, so the result is the same every time.
-constexpr int KV4_MAX_BATCH = 1024;  // sequences of a launch: their unit counts sit in shared memory
-constexpr int KV4_CTAS = 148;        // blocks of the grid, one per SM
-constexpr int KV4_STAGES = 4;
-// Warps of a block: as many as their state lets have enough registers.
+// Work is counted in units of two strips of one tile (8 NT query rows of one
+// sequence and kv head), ordered by sequence, head, tile, tokens. Every working
+// warp of the grid takes one contiguous range of equal length, whatever the
+// contexts' lengths, out of a ring of its own in shared memory that the block's
+// producer warp keeps filled (lane i serves working warp i: one cp.async.bulk a
+// unit, two with pages of 16, on across tiles); no working warp waits for
+// another until its range is done. A tile that lies in one warp's range is
+// written out by it; the at most two that it shares (its first and its last) go
+// to the workspace as (unnormalised output, m, l), are joined within the block,
+// and where they cross blocks by kv4_attention_join. All joins run in the order
+// of the ranges, so the result is the same every time.
+constexpr int KV4_MAX_BATCH = 512;  // sequences of a launch: what the block needs of them sits in shared memory
+constexpr int KV4_CTAS = 148;       // blocks of the grid, one per SM
+// Working warps of a block: as many as their state leaves registers for.
 constexpr int kv4_warps(int dim, int group, int nt) {
-  return dim * nt > 128 ? 8 : dim / group * nt <= (dim * nt <= 64 ? 2 : 1) ? 16 : 12;
+  return dim * nt > 128 ? 7 : dim / group * nt == 1 || (dim == 64 && nt == 1) ? 15 : 11;
+}
+// units in a warp's ring: three, or two where shared memory holds no more
+constexpr int kv4_stages(int dim, int group, int warps) {
+  return 3 * warps * 2 * kv4_strip_bytes(dim, group) + 17 * 1024 <= 227 * 1024 ? 3 : 2;
 }
 
 struct Kv4SplitArgs {
   Kv4AttnArgs a;
   int tile_rows;    // 8 NT
-  float* warp_part; // [warps of the grid][2][8 NT][D + 4]
+  float* warp_part; // [working warps of the grid][2][8 NT][D + 4]
   float* cta_part;  // [KV4_CTAS][2][8 NT][D + 4]
   long long* cta_seg;  // [KV4_CTAS][2] tile of a block partial (-1: none)
   int* cta_bad;     // [KV4_CTAS]
@@ -703,15 +714,36 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "r"(bytes), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
-// Units of the batch: prefix[b] = units before sequence b, strips and tiles of each.
+// Units of the batch: prefix[b] = units before sequence b, units of a tile
+// (span) and tiles of a head of each, and its rows and context.
 struct Kv4Plan {
   long long prefix[KV4_MAX_BATCH + 1];
-  int strips[KV4_MAX_BATCH], tiles[KV4_MAX_BATCH];
+  int span[KV4_MAX_BATCH], tiles[KV4_MAX_BATCH], row0[KV4_MAX_BATCH], n[KV4_MAX_BATCH], len[KV4_MAX_BATCH];
   int bad;
+  __device__ __forceinline__ Kv4Seq seq(int b) const {
+    Kv4Seq s;
+    s.row0 = row0[b];
+    s.n = n[b];
+    s.L = len[b];
+    s.bad = false;
+    return s;
+  }
 };
 
-// Filled by the whole block (a multiple of 32 threads, at least 32).
+// Filled by the whole block.
 __device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, long long* warp_sums) {
   const Kv4AttnArgs& a = s.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -729,11 +761,14 @@ __device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, long
       if (q.bad) p.bad = 1;
       const long long rows = (long long)q.n * a.share;
       // a sequence without context still has its rows to write: one unit, which reads nothing
-      const int strips = q.n > 0 ? max(1, (int)(((long long)q.L + 15) >> 4)) : 0;
+      const int span = q.n > 0 ? max(1, (int)(((long long)q.L + KV4_UNIT - 1) / KV4_UNIT)) : 0;
       const int tiles = (int)((rows + s.tile_rows - 1) / s.tile_rows);
-      p.strips[b] = strips;
+      p.span[b] = span;
       p.tiles[b] = tiles;
-      n = (long long)strips * tiles * a.c.heads;
+      p.row0[b] = (int)q.row0;
+      p.n[b] = q.n;
+      p.len[b] = q.L;
+      n = (long long)span * tiles * a.c.heads;
     }
     long long inc = n;
 #pragma unroll
@@ -745,24 +780,23 @@ __device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, long
     __syncthreads();
     for (int w = 0; w < warp; ++w) inc += warp_sums[w];
     if (b < a.batch) p.prefix[b + 1] = before + inc;
-    for (int w = 0; w < warps; ++w) before += warp_sums[w];
-    __syncthreads();
+    if (b0 + (int)blockDim.x < a.batch) {
+      for (int w = 0; w < warps; ++w) before += warp_sums[w];
+      __syncthreads();
+    }
   }
+  __syncthreads();
 }
 
-// Workers that take part: at least KV4_MIN_STRIPS units each.
-constexpr int KV4_MIN_STRIPS = 4;
-__device__ __forceinline__ long long kv4_workers(long long units, long long most) {
-  const long long w = (units + KV4_MIN_STRIPS - 1) / KV4_MIN_STRIPS;
-  return w < most ? (w > 0 ? w : 1) : most;
-}
-__device__ __forceinline__ long long kv4_begin(long long w, long long workers, long long units) {
+// First unit of worker w: one unit each at least.
+__device__ __forceinline__ long long kv4_begin(long long w, long long most, long long units) {
+  const long long workers = units < most ? units : most;
   return w < workers ? w * units / workers : units;
 }
 
 // A place in the order of units.
 struct Kv4Cursor {
-  int b, strip, strips, tile, tiles, head;
+  int b, at, span, tile, tiles, head;  // unit `at` of `span` of a tile
   __device__ __forceinline__ void seek(const Kv4Plan& p, int batch, long long u) {
     int lo = 0, hi = batch;  // prefix[lo] <= u < prefix[hi]
     while (hi - lo > 1) {
@@ -771,25 +805,25 @@ struct Kv4Cursor {
       else hi = mid;
     }
     b = lo;
-    strips = p.strips[b];
+    span = p.span[b];
     tiles = p.tiles[b];
-    const long long in = u - p.prefix[b], seg = in / strips;
-    strip = (int)(in - seg * strips);
+    const long long in = u - p.prefix[b], seg = in / span;
+    at = (int)(in - seg * span);
     head = (int)(seg / tiles);
     tile = (int)(seg - (long long)head * tiles);
   }
   // to the next unit; true if it begins another tile
   __device__ __forceinline__ bool step(const Kv4Plan& p, const Kv4AttnArgs& a) {
-    if (++strip < strips) return false;
-    strip = 0;
+    if (++at < span) return false;
+    at = 0;
     if (++tile == tiles) {
       tile = 0;
       if (++head == a.c.heads) {
         head = 0;
         do ++b;
-        while (b < a.batch && p.strips[b] == 0);
+        while (b < a.batch && p.span[b] == 0);
         if (b < a.batch) {
-          strips = p.strips[b];
+          span = p.span[b];
           tiles = p.tiles[b];
         }
       }
@@ -801,7 +835,7 @@ struct Kv4Cursor {
   }
 };
 
-// Query row r (in the sequence's n * share) of a kv head: its element offset in out, and in lse; -1 if there is none.
+// Query row r (in the sequence's n * share) of a kv head: its row in out and lse; -1 if there is none.
 __device__ __forceinline__ long long kv4_out_row(const Kv4AttnArgs& a, const Kv4Seq& s, int head, long long r) {
   if (r >= (long long)s.n * a.share) return -1;
   const long long tok = s.row0 + r / a.share;
@@ -809,35 +843,53 @@ __device__ __forceinline__ long long kv4_out_row(const Kv4AttnArgs& a, const Kv4
   return tok * a.q_heads + head * a.share + (int)(r % a.share);
 }
 
-// Joins entries part(e), e in [e0, e1), of row `row` of a tile by one warp:
-// lane's channels 4 lane + 128 k. Returns m and l; v holds the unnormalised sums.
+// Row `row` of a tile joined by one warp out of n parts part(0), part(1), ...:
+// the lane's channels 4 lane + 128 k, unnormalised, and m and l.
 template <int D>
 struct Kv4Joined {
   static constexpr int K = (D + 127) / 128;
   float4 v[K];
   float m, l;
   template <typename Part>
-  __device__ __forceinline__ void join(Part part, int e0, int e1, int row, int lane) {
-    m = -INFINITY;
-    for (int e = e0; e < e1; ++e) m = fmaxf(m, part(e)[row * (D + 4) + D]);
+  __device__ __forceinline__ void join(Part part, int n, int row, int lane) {
+    m = KV4_LOWEST;
     l = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int e = e0; e < e1; ++e) {
-      const float* r = part(e) + row * (D + 4);
-      const float me = r[D], le = r[D + 1];
-      // a part that saw nothing holds m = -inf and zeros; NaN in l passes on
-      const float f = me == -INFINITY ? (le == 0.0f ? 0.0f : le) : exp2_fast(me - m);
-      l = fmaf(f, le, l);
+    for (int e0 = 0; e0 < n; e0 += 32) {  // 32 parts at a time: lane i takes the i-th one's m and l
+      const int cnt = min(32, n - e0);
+      float2 ml = make_float2(KV4_LOWEST, 0.0f);
+      if (lane < cnt) ml = *reinterpret_cast<const float2*>(part(e0 + lane) + row * (D + 4) + D);
+      float top = fmaxf(m, ml.x);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float old = exp2_fast(m - top), f = exp2_fast(ml.x - top);  // (NaN in a part's sums passes on)
+      m = top;
+      float add = f * ml.y;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+      l = fmaf(l, old, add);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int c = 4 * lane + 128 * k;
-        if (c < D) {
-          const float4 x = *reinterpret_cast<const float4*>(r + c);
-          v[k].x = fmaf(f, x.x, v[k].x);
-          v[k].y = fmaf(f, x.y, v[k].y);
-          v[k].z = fmaf(f, x.z, v[k].z);
-          v[k].w = fmaf(f, x.w, v[k].w);
+        v[k].x *= old;
+        v[k].y *= old;
+        v[k].z *= old;
+        v[k].w *= old;
+      }
+#pragma unroll 4
+      for (int e = 0; e < cnt; ++e) {
+        const float* r = part(e0 + e) + row * (D + 4);
+        const float fe = __shfl_sync(0xffffffffu, f, e);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const int c = 4 * lane + 128 * k;
+          if (c < D) {
+            const float4 x = *reinterpret_cast<const float4*>(r + c);
+            v[k].x = fmaf(fe, x.x, v[k].x);
+            v[k].y = fmaf(fe, x.y, v[k].y);
+            v[k].z = fmaf(fe, x.z, v[k].z);
+            v[k].w = fmaf(fe, x.w, v[k].w);
+          }
         }
       }
     }
@@ -846,10 +898,7 @@ struct Kv4Joined {
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (4 * lane + 128 * k < D) *reinterpret_cast<float4*>(r + 4 * lane + 128 * k) = v[k];
-    if (lane == 0) {
-      r[D] = m;
-      r[D + 1] = l;
-    }
+    if (lane == 0) *reinterpret_cast<float2*>(r + D) = make_float2(m, l);
   }
   __device__ __forceinline__ void write(const Kv4AttnArgs& a, long long at, int lane) const {
     if (at < 0) return;
@@ -870,29 +919,119 @@ template <int D, int G, int NT>
 struct Kv4SplitSmem {
   static constexpr int W = kv4_warps(D, G, NT);
   static constexpr int STRIP = kv4_strip_bytes(D, G);
-  alignas(128) uint8_t ring[W][KV4_STAGES][STRIP];
-  alignas(8) uint64_t bar[W][KV4_STAGES];
+  static constexpr int STAGES = kv4_stages(D, G, W);
+  alignas(128) uint8_t ring[W][STAGES][2 * STRIP];
+  alignas(8) uint64_t full[W][STAGES];
+  uint64_t empty[W][STAGES];
   Kv4Plan plan;
-  long long sums[W];
+  long long sums[W + 1];
   long long seg[W][2];   // tile of a warp's first and last part (-1: none)
   int flags[W][2];       // bit 0: the part begins its tile, bit 1: it ends it
-  int chain[2 * W + 1], chains, bad;
+  uint8_t lost[W][4];    // strips of a stage's unit that are not there to be read (by bit)
+  int bad;
   int abort;
 };
 
+// Lane i of the producer warp: the units of working warp i.
 template <int D, int G, int NT>
-__global__ void __launch_bounds__(32 * kv4_warps(D, G, NT), 1) kv4_attention_split(const __grid_constant__ Kv4SplitArgs s) {
+__device__ __forceinline__ void kv4_produce(const Kv4SplitArgs& s, Kv4SplitSmem<D, G, NT>& sm, long long units, int lane) {
+  using Sm = Kv4SplitSmem<D, G, NT>;
+  constexpr int W = Sm::W, STAGES = Sm::STAGES, STRIP = Sm::STRIP;
+  const Kv4AttnArgs& a = s.a;
+  const long long me = (long long)blockIdx.x * W + lane, most = (long long)gridDim.x * W;
+  const long long u0 = kv4_begin(me, most, units), u1 = kv4_begin(me + 1, most, units);
+  int left = lane < W ? (int)(u1 - u0) : 0;
+  int stage = 0, sent = 0;
+  uint32_t phase = 1;  // a fresh ring is empty
+  Kv4Cursor cur;
+  int page[2] = {-1, -1};
+  // pages of 16 tokens hold one strip of the unit each, larger ones both, one behind the other
+  const bool two = a.c.page_shift == 4;
+  auto look = [&]() {
+    const int p = KV4_UNIT * cur.at >> a.c.page_shift;
+    const int* row = a.table + (long long)cur.b * a.table_pages;
+    page[0] = p < a.table_pages ? __ldg(row + p) : -1;
+    if (two) page[1] = p + 1 < a.table_pages ? __ldg(row + p + 1) : -1;
+  };
+  if (left > 0) {
+    cur.seek(sm.plan, a.batch, u0);
+    look();
+  }
+  uint64_t idle_since = 0;
+  while (__any_sync(0xffffffffu, left > 0)) {
+    bool moved = false;
+    if (left > 0 && mbar_test(smem_u32(&sm.empty[lane][stage]), phase)) {
+      moved = true;
+      const uint32_t bar = smem_u32(&sm.full[lane][stage]), dst = smem_u32(sm.ring[lane][stage]);
+      const int t0 = KV4_UNIT * cur.at, len = sm.plan.len[cur.b];
+      unsigned lost = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !two) break;
+        const uint32_t n = two ? STRIP : 2 * STRIP;
+        const bool in = t0 + 16 * h < len;
+        bool good = in && page[h] >= 0 && page[h] < a.c.n_pages;
+        if (in && !good) sm.bad = ERR_KV4_PAGE;
+        const long long off = good ? a.c.strip(page[h], cur.head, t0 & ((1 << a.c.page_shift) - 1)) : 0;
+        good = good && AWQ_SPAN_OK(off, n, a.c.bytes(), BS_KV4_STRIP);
+        if (good) {
+          mbar_expect_tx(bar, n);
+          bulk_load(dst + h * STRIP, a.c.base + off, n, bar);
+        } else {
+          lost |= two ? 1u << h : 3u;
+        }
+      }
+      sm.lost[lane][stage] = (uint8_t)lost;
+      mbar_arrive(bar);
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      ++sent;
+      if (--left > 0) {
+        cur.step(sm.plan, a);
+        look();
+      }
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+      idle_since = 0;
+    } else {
+      // nothing to fill: a unit takes a warp over a microsecond
+      __nanosleep(64);
+      if (*(volatile int*)&sm.abort) break;
+      const uint64_t now = globaltimer_ns();
+      if (idle_since == 0) idle_since = now;
+      if (__any_sync(0xffffffffu, now - idle_since > 2 * AWQ_WAIT_LIMIT_NS)) break;
+    }
+  }
+  // copies in flight end before the block does (their units are waited for by
+  // the working warps, unless a wait there gave up)
+  __syncwarp();
+  if (*(volatile int*)&sm.abort && lane < W && sent > 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000ull) {
+    }
+  }
+  __syncwarp();
+}
+
+template <int D, int G, int NT>
+__global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
+    kv4_attention_split(const __grid_constant__ Kv4SplitArgs s) {
   using Sm = Kv4SplitSmem<D, G, NT>;
   using St = Kv4Warp<D, G, NT>;
-  constexpr int W = Sm::W, PART = 8 * NT * (D + 4);
+  constexpr int W = Sm::W, STAGES = Sm::STAGES, PART = 8 * NT * (D + 4);
   extern __shared__ uint8_t smem_raw[];
   // (offset, not address, arithmetic keeps the accesses shared-memory ones)
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u));
   const Kv4AttnArgs& a = s.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) {
+  if (lane == 0 && warp < W) {
 #pragma unroll
-    for (int i = 0; i < KV4_STAGES; ++i) mbar_init(smem_u32(&sm.bar[warp][i]), 1);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&sm.full[warp][i]), 1);
+      mbar_init(smem_u32(&sm.empty[warp][i]), 1);
+    }
     fence_barrier_init();
     sm.seg[warp][0] = sm.seg[warp][1] = -1;
   }
@@ -902,80 +1041,52 @@ __global__ void __launch_bounds__(32 * kv4_warps(D, G, NT), 1) kv4_attention_spl
   }
   kv4_plan(s, sm.plan, sm.sums);
   const long long units = sm.plan.prefix[a.batch];
-  const long long workers = kv4_workers(units, (long long)gridDim.x * W);
-  const long long me = (long long)blockIdx.x * W + warp;
-  const long long u0 = kv4_begin(me, workers, units), u1 = kv4_begin(me + 1, workers, units);
-  float* my_part = s.warp_part + me * 2 * PART;
-  if (u0 < u1) {
-    Kv4Cursor cur, ahead;
-    cur.seek(sm.plan, a.batch, u0);
-    ahead = cur;
-    const int page_mask = (1 << a.c.page_shift) - 1;
-    int left = (int)(u1 - u0), to_load = left;
-    unsigned have = 0;  // stages whose strip is there to be read
-    int win_b = -1, win_p = 0, win = 0;  // lane i: page win_p + i of sequence win_b
-    int ahead_len = a.lens[ahead.b];
-    auto issue = [&](int stage) {
-      const int t0 = 16 * ahead.strip, p = t0 >> a.c.page_shift;
-      if (ahead.b != win_b || p < win_p || p >= win_p + 32) {
-        win_b = ahead.b;
-        win_p = p;
-        win = p + lane < a.table_pages ? __ldg(a.table + (long long)ahead.b * a.table_pages + p + lane) : -1;
-        ahead_len = a.lens[ahead.b];
-      }
-      const int page = __shfl_sync(0xffffffffu, win, p - win_p);
-      const bool in = t0 < ahead_len, good = in && page >= 0 && page < a.c.n_pages;
-      bool copied = false;
-      if (good) {
-        const long long off = a.c.strip(page, ahead.head, t0 & page_mask);
-        if (AWQ_SPAN_OK(off, Sm::STRIP, a.c.bytes(), BS_KV4_STRIP)) {
-          copied = true;
-          if (lane == 0) {
-            const uint32_t bar = smem_u32(&sm.bar[warp][stage]);
-            mbar_arrive_expect_tx(bar, Sm::STRIP);
-            bulk_load(smem_u32(sm.ring[warp][stage]), a.c.base + off, Sm::STRIP, bar);
-          }
-        }
-      } else if (in && lane == 0) {
-        sm.bad = ERR_KV4_PAGE;
-      }
-      have = copied ? have | (1u << stage) : have & ~(1u << stage);
-      --to_load;
-      if (to_load > 0) ahead.step(sm.plan, a);
-    };
-    for (int i = 0; i < KV4_STAGES && to_load > 0; ++i) issue(i);
+  if (warp == W) {
+    kv4_produce<D, G, NT>(s, sm, units, lane);
+  } else {
+    const long long me = (long long)blockIdx.x * W + warp, most = (long long)gridDim.x * W;
+    const long long u0 = kv4_begin(me, most, units), u1 = kv4_begin(me + 1, most, units);
+    float* my_part = s.warp_part + me * 2 * PART;
+    Kv4Cursor cur;
+    int left = (int)(u1 - u0), stage = 0;
+    uint32_t phase = 0;
+    bool fresh_tile = true, first = true, begins = false;
+    if (left > 0) {
+      cur.seek(sm.plan, a.batch, u0);
+      begins = cur.at == 0;
+    }
     St w;
-    int stage = 0;
-    unsigned phases = 0;
-    bool ok = true, begins = cur.strip == 0, first = true;
-    Kv4Seq seq = kv4_seq(a, cur.b);
-    w.load_queries(a, seq, cur.head, (long long)cur.tile * s.tile_rows, lane);
     int done = 0;
-    while (ok) {
-      const int t0 = 16 * cur.strip;
-      if (have >> stage & 1u) {
-        ok = mbar_wait(smem_u32(&sm.bar[warp][stage]), phases >> stage & 1u, &sm.abort, nullptr, 0);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        phases ^= 1u << stage;
-        have &= ~(1u << stage);
-        if (t0 < w.vis_max) {
-          if (t0 + 16 > w.vis_min)
-            w.template strip<true>(sm.ring[warp][stage], t0, lane);
-          else
-            w.template strip<false>(sm.ring[warp][stage], t0, lane);
-          if (++done % KV4_RECENTRE == 0) w.recentre();
-        }
+    while (left > 0) {
+      if (fresh_tile) {
+        w.load_queries(a, sm.plan.seq(cur.b), cur.head, (long long)cur.tile * s.tile_rows, lane);
+        fresh_tile = false;
+        done = 0;
+      }
+      const bool here = mbar_wait(smem_u32(&sm.full[warp][stage]), phase, &sm.abort, nullptr, 0);
+      if (!__all_sync(0xffffffffu, here)) {
+        // a copy that never came: report, write nothing
+        if (lane == 0) sm.bad = ERR_KV4_COPY;
+        break;
+      }
+      const unsigned lost = sm.lost[warp][stage];
+      if (lost != 3u && KV4_UNIT * cur.at < w.vis_max) {
+        w.unit(sm.ring[warp][stage], KV4_UNIT * cur.at, lost, lane);
+        if (++done % KV4_RECENTRE == 0) w.recentre();
       }
       __syncwarp();
-      if (to_load > 0) issue(stage);
-      if (++stage == KV4_STAGES) stage = 0;
+      if (lane == 0) mbar_arrive(smem_u32(&sm.empty[warp][stage]));
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
       --left;
-      const bool ends = cur.strip + 1 == cur.strips;
+      const bool ends = cur.at + 1 == cur.span;
       if (ends || left == 0) {
         w.finish();
         if (begins && ends) {
           // the whole tile: write it
+          const Kv4Seq seq = sm.plan.seq(cur.b);
           const int g = lane >> 2, q = lane & 3;
 #pragma unroll
           for (int u = 0; u < NT; ++u)
@@ -1004,68 +1115,48 @@ __global__ void __launch_bounds__(32 * kv4_warps(D, G, NT), 1) kv4_attention_spl
           }
         }
         first = false;
-        if (left == 0) break;
+        if (left > 0) {
+          cur.step(sm.plan, a);
+          begins = true;
+          fresh_tile = true;
+        }
+      } else {
+        ++cur.at;
       }
-      if (cur.step(sm.plan, a)) {
-        const int b = cur.b;
-        begins = true;
-        seq = kv4_seq(a, b);
-        w.load_queries(a, seq, cur.head, (long long)cur.tile * s.tile_rows, lane);
-        done = 0;
-      }
-    }
-    if (!ok) {
-      // a copy that never came: wait (bounded) for the others, report, write nothing
-      if (lane == 0) {
-        sm.bad = ERR_KV4_COPY;
-        for (int i = 0; i < KV4_STAGES; ++i)
-          if (have >> i & 1u) mbar_wait_drain(smem_u32(&sm.bar[warp][i]), phases >> i & 1u);
-      }
-      __syncwarp();
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __threadfence_block();
   __syncthreads();
   // ---------------- join the warps' parts: chains of consecutive parts of one tile
+  // lane e of every warp looks at part e (2 W <= 32): which parts begin a chain
+  static_assert(2 * W <= 32, "parts of a block");
+  const long long my_seg = lane < 2 * W ? sm.seg[lane >> 1][lane & 1] : -1;
+  const unsigned valid = __ballot_sync(0xffffffffu, my_seg >= 0);
+  const unsigned below = valid & ((1u << lane) - 1u);
+  const long long prev = __shfl_sync(0xffffffffu, my_seg, below ? 31 - __clz(below) : 0);
+  const unsigned heads = __ballot_sync(0xffffffffu, my_seg >= 0 && (!below || prev != my_seg));
+  const int chains = __popc(heads);
+  const int my_flags = lane < 2 * W ? sm.flags[lane >> 1][lane & 1] : 0;
   if (threadIdx.x == 0) {
-    int n = 0;
-    long long last = -1;
-    for (int e = 0; e < 2 * W; ++e) {
-      const long long g = sm.seg[e >> 1][e & 1];
-      if (g < 0) continue;
-      if (g != last) sm.chain[n++] = e;
-      last = g;
-    }
-    sm.chain[n] = 2 * W;
-    sm.chains = n;
     s.cta_bad[blockIdx.x] = sm.bad ? sm.bad : sm.plan.bad ? ERR_KV4_PAGE : 0;
+    // slot 0: a tile that an earlier block began, slot 1: one that a later block ends
     s.cta_seg[2 * blockIdx.x] = s.cta_seg[2 * blockIdx.x + 1] = -1;
   }
   __syncthreads();
   const float* base = s.warp_part + (long long)blockIdx.x * W * 2 * PART;
-  for (int it = warp; it < sm.chains * 8 * NT; it += W) {
+  for (int it = warp; it < chains * 8 * NT; it += W + 1) {
     const int ch = it / (8 * NT), row = it - ch * 8 * NT;
-    const int e0 = sm.chain[ch];
-    int entries = 0;
-    const long long seg = sm.seg[e0 >> 1][e0 & 1];
-    // a chain's parts: the first one, then the slot 0 of the following warps (a warp's slot 1 begins another tile)
-    int flags = 0;
-    for (int e = e0; e < sm.chain[ch + 1]; ++e)
-      if (sm.seg[e >> 1][e & 1] >= 0) {
-        flags |= sm.flags[e >> 1][e & 1];
-        ++entries;
-      }
+    const int e0 = __fns(heads, 0, ch + 1);
+    const long long seg = __shfl_sync(0xffffffffu, my_seg, e0);
+    const unsigned mine = __ballot_sync(0xffffffffu, my_seg == seg);
+    const int flags = __reduce_or_sync(0xffffffffu, (unsigned)(my_seg == seg ? my_flags : 0));
     Kv4Joined<D> j;
-    auto part = [&](int i) {
-      // the i-th part of the chain: e0, then warp (e0 / 2 + i), slot 0
-      const int e = i == 0 ? e0 : 2 * ((e0 >> 1) + i);
-      return base + (long long)e * PART;
-    };
-    j.join(part, 0, entries, row, lane);
+    // the i-th part of the chain: e0, then slot 0 of the warps behind
+    j.join([&](int i) { return base + (long long)(i == 0 ? e0 : 2 * ((e0 >> 1) + i)) * PART; }, __popc(mine), row, lane);
     if (flags == 3) {
       const int head_b = (int)(seg >> 32), b = head_b / a.c.heads, head = head_b - b * a.c.heads;
-      const Kv4Seq seq = kv4_seq(a, b);
-      j.write(a, kv4_out_row(a, seq, head, (long long)(int)(seg & 0xffffffff) * s.tile_rows + row), lane);
+      j.write(a, kv4_out_row(a, sm.plan.seq(b), head, (long long)(int)(seg & 0xffffffff) * s.tile_rows + row), lane);
     } else {
       // shared with other blocks: slot 1 if it begins here, else 0
       const int k = flags & 1;
@@ -1077,32 +1168,36 @@ __global__ void __launch_bounds__(32 * kv4_warps(D, G, NT), 1) kv4_attention_spl
 
 // Block c joins the tile that block c of the split began and did not end:
 // its slot 1, then slot 0 of the following blocks while they hold that tile.
-// Block 0 sets the call's error word.
+// Block 0 sets the call's error word. Launched to overlap the split's end.
 template <int D, int NT>
 __global__ void __launch_bounds__(256) kv4_attention_join(const __grid_constant__ Kv4SplitArgs s, int ctas) {
   constexpr int PART = 8 * NT * (D + 4);
   const Kv4AttnArgs& a = s.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
-  if (c == 0 && threadIdx.x < 32) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c == 0 && warp == 0) {
     int bad = 0;
     for (int i = lane; i < ctas; i += 32) bad = max(bad, s.cta_bad[i]);
     bad = __reduce_max_sync(0xffffffffu, bad);
-    if (lane == 0) {
-      if (s.clear_err) *a.err = bad;
-      else if (bad) *a.err = bad;
-    }
+    if (lane == 0 && (s.clear_err || bad)) *a.err = bad;
   }
   const long long seg = s.cta_seg[2 * c + 1];
   if (seg < 0) return;
   int n = 1;
-  while (c + n < ctas && s.cta_seg[2 * (c + n)] == seg) ++n;
+  for (int i = c + 1; i < ctas; i += 32) {  // how many blocks behind hold the tile
+    const bool same = i + lane < ctas && s.cta_seg[2 * (i + lane)] == seg;
+    const unsigned run = __ballot_sync(0xffffffffu, same);
+    const int k = run == 0xffffffffu ? 32 : __ffs(~run) - 1;
+    n += k;
+    if (k < 32) break;
+  }
   const int head_b = (int)(seg >> 32), b = head_b / a.c.heads, head = head_b - b * a.c.heads;
   const Kv4Seq seq = kv4_seq(a, b);
   for (int row = warp; row < 8 * NT; row += 8) {
     const long long at = kv4_out_row(a, seq, head, (long long)(int)(seg & 0xffffffff) * s.tile_rows + row);
     if (at < 0) continue;
     Kv4Joined<D> j;
-    j.join([&](int i) { return s.cta_part + ((long long)(c + i) * 2 + (i == 0)) * PART; }, 0, n, row, lane);
+    j.join([&](int i) { return s.cta_part + ((long long)(c + i) * 2 + (i == 0)) * PART; }, n, row, lane);
     j.write(a, at, lane);
   }
 }

@@ -7,6 +7,32 @@
 
 namespace {
 
+// A kernel launched behind another that uses most of shared memory asks for the
+// same split of L1, so that the SMs are not reconfigured between the two.
+template <typename K>
+bool big_carveout(K kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
+         cudaSuccess;
+}
+
+// Launch that may start while the kernel before it on the stream ends
+// (programmatic dependent launch): the kernel waits for it by
+// griddepcontrol.wait before it touches memory.
+template <typename... P, typename... A>
+awq_status launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t cs, A... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = cs;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...) == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
 bool dtype_ok(awq_dtype d) { return d == AWQ_DTYPE_BF16 || d == AWQ_DTYPE_F16; }
 
 // ------------------------------------------------------------------ 8-bit integer linear layer
@@ -146,7 +172,6 @@ awq_status check_kv4_attention(int64_t batch, int64_t n_q_heads, int64_t max_q, 
 // tiles and the partial outputs of blocks and warps.
 struct Kv4Layout {
   int nt, warps;
-  bool split;
   size_t off_bad, off_seg, off_cta, off_warp, total;
 };
 
@@ -154,7 +179,6 @@ Kv4Layout kv4_layout(int64_t n_q_heads, int64_t max_q, const awq_kv4cfg* c) {
   Kv4Layout L{};
   const long long rows = max_q * (n_q_heads / c->n_kv_heads);
   L.nt = rows > 8 && c->head_dim <= 128 ? 2 : 1;
-  L.split = rows <= 64;
   L.warps = kv4_warps(c->head_dim, c->group, L.nt);
   const size_t part = (size_t)8 * L.nt * (c->head_dim + 4) * sizeof(float);
   size_t off = kAlign;
@@ -162,7 +186,7 @@ Kv4Layout kv4_layout(int64_t n_q_heads, int64_t max_q, const awq_kv4cfg* c) {
   L.off_seg = off;   off += align_up(KV4_CTAS * 2 * sizeof(long long));
   L.off_cta = off;   off += align_up(KV4_CTAS * 2 * part);
   L.off_warp = off;  off += align_up((size_t)KV4_CTAS * L.warps * 2 * part);
-  L.total = L.split ? off : kAlign;
+  L.total = off;
   return L;
 }
 
@@ -361,46 +385,37 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   a.out = out;
   a.lse = lse;
   a.err = at<int>(ws, 0);
-  if (L.split) {
-    Kv4SplitArgs sa{};
-    sa.tile_rows = 8 * L.nt;
-    sa.warp_part = at<float>(ws, L.off_warp);
-    sa.cta_part = at<float>(ws, L.off_cta);
-    sa.cta_seg = at<long long>(ws, L.off_seg);
-    sa.cta_bad = at<int>(ws, L.off_bad);
-    for (int64_t first = 0; first < batch; first += KV4_MAX_BATCH) {
-      sa.a = a;
-      sa.a.batch = (int)(batch - first < KV4_MAX_BATCH ? batch - first : KV4_MAX_BATCH);
-      sa.a.table += first * table_pages;
-      sa.a.lens += first;
-      if (q_start) sa.a.q_start += first;
-      sa.a.row_first = (int)first;
-      sa.clear_err = first == 0;
-      st = kv4_shapes(cfg->head_dim, cfg->group, [&](auto d, auto g) -> awq_status {
-        constexpr int D = decltype(d)::value, G = decltype(g)::value;
-        auto launch = [&](auto nt) -> awq_status {
-          constexpr int NT = decltype(nt)::value;
-          constexpr int smem = (int)sizeof(Kv4SplitSmem<D, G, NT>) + 128;
-          static_assert(smem <= 232448, "shared memory of the split attention");
-          auto k = kv4_attention_split<D, G, NT>;
-          if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return AWQ_ERR_CUDA;
-          k<<<KV4_CTAS, 32 * kv4_warps(D, G, NT), smem, cs>>>(sa);
-          kv4_attention_join<D, NT><<<KV4_CTAS, 256, 0, cs>>>(sa, KV4_CTAS);
-          return launch_status();
-        };
-        return L.nt == 2 ? launch(std::integral_constant<int, D <= 128 ? 2 : 1>{}) : launch(std::integral_constant<int, 1>{});
-      });
-      if (st != AWQ_OK) return st;
-    }
-    return AWQ_OK;
+  Kv4SplitArgs sa{};
+  sa.tile_rows = 8 * L.nt;
+  sa.warp_part = at<float>(ws, L.off_warp);
+  sa.cta_part = at<float>(ws, L.off_cta);
+  sa.cta_seg = at<long long>(ws, L.off_seg);
+  sa.cta_bad = at<int>(ws, L.off_bad);
+  for (int64_t first = 0; first < batch; first += KV4_MAX_BATCH) {
+    sa.a = a;
+    sa.a.batch = (int)(batch - first < KV4_MAX_BATCH ? batch - first : KV4_MAX_BATCH);
+    sa.a.table += first * table_pages;
+    sa.a.lens += first;
+    if (q_start) sa.a.q_start += first;
+    sa.a.row_first = (int)first;
+    sa.clear_err = first == 0;
+    st = kv4_shapes(cfg->head_dim, cfg->group, [&](auto d, auto g) -> awq_status {
+      constexpr int D = decltype(d)::value, G = decltype(g)::value;
+      auto launch = [&](auto nt) -> awq_status {
+        constexpr int NT = decltype(nt)::value;
+        constexpr int smem = (int)sizeof(Kv4SplitSmem<D, G, NT>) + 128;
+        static_assert(smem <= 232448, "shared memory of the split attention");
+        auto k = kv4_attention_split<D, G, NT>;
+        auto j = kv4_attention_join<D, NT>;
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess || !big_carveout(j))
+          return AWQ_ERR_CUDA;
+        k<<<KV4_CTAS, 32 * (kv4_warps(D, G, NT) + 1), smem, cs>>>(sa);
+        if ((st = launch_status()) != AWQ_OK) return st;
+        return launch_behind(j, dim3(KV4_CTAS), dim3(256), 0, cs, sa, KV4_CTAS);
+      };
+      return L.nt == 2 ? launch(std::integral_constant<int, D <= 128 ? 2 : 1>{}) : launch(std::integral_constant<int, 1>{});
+    });
+    if (st != AWQ_OK) return st;
   }
-  if (cudaMemsetAsync(ws, 0, sizeof(int), cs) != cudaSuccess) return AWQ_ERR_CUDA;
-  const long long tiles = cdiv(max_q * a.share, 8);
-  if (tiles > INT32_MAX) return AWQ_ERR_SHAPE;
-  const dim3 grid((unsigned)tiles, (unsigned)cfg->n_kv_heads, (unsigned)batch);
-  return kv4_shapes(cfg->head_dim, cfg->group, [&](auto d, auto g) {
-    constexpr int D = decltype(d)::value, G = decltype(g)::value;
-    kv4_attention_tiles<D, G><<<grid, 32 * KV4_WARPS, 0, cs>>>(a);
-    return launch_status();
-  });
+  return AWQ_OK;
 }
