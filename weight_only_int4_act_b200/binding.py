@@ -12,6 +12,7 @@ switches later calls to the other.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
 
@@ -93,6 +94,8 @@ def select_library(variant: str) -> str:
 
 def lib() -> ctypes.CDLL:
     """The selected build of the CUDA library (raises if it has not been built)."""
+    if _active in _libs:
+        return _libs[_active]
     if _active not in VARIANTS:
         raise ValueError(f"AWQ_B200_LIB={_active!r}; one of {sorted(VARIANTS)}")
     if _active not in _libs:
@@ -431,30 +434,68 @@ def w4a16_gemm(Xp, qweight, scales, zeros, cfg: QCfg, ws=None, out=None):
     return out
 
 
-def _req_here(t, dtype, shape, name):
-    """A contiguous CUDA tensor of the current device (calls run on its current stream)."""
-    _req(t, dtype, shape, name)
-    _same_device(t, name)
+# The calls below are made once a layer and token, so their checks are short:
+# one expression for a good argument, the full checks only to name what is wrong.
+@functools.lru_cache(maxsize=None)
+def _torch_names():
+    """(Tensor, current_device, raw stream of a device, 16-bit types by code) of torch."""
+    torch = _torch()
+    torch.cuda.init()
+    return (torch.Tensor, torch.cuda.current_device, torch._C._cuda_getCurrentRawStream,
+            {torch.bfloat16: AWQ_DTYPE_BF16, torch.float16: AWQ_DTYPE_F16})
 
 
-def _same_device(t, name):
-    here = _torch().cuda.current_device()
-    if t.device.index != here:
-        raise ValueError(f"{name} must be on the current device cuda:{here}, got {t.device}")
-
-
-def _req_rows(t, shape, name):
-    """A CUDA tensor of the current device whose last axis is contiguous; the others may be strided."""
+def _here(t, name):
+    """(current device, its current stream, ...): t must be a CUDA tensor of that device."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    _, current, stream, codes = _torch_names()
+    dev = current()
+    _same_device(t, dev, name)
+    return dev, stream(dev), codes
+
+
+def _same_device(t, dev, name):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device cuda:{dev}, got {t.device}")
+
+
+def _req_here(t, dtype, shape, dev, name):
+    """A contiguous tensor of device dev (calls run on its current stream)."""
+    if isinstance(t, _torch_names()[0]) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return
+    _req(t, dtype, shape, name)
+    _same_device(t, dev, name)
+
+
+def _req_rows(t, dtype, shape, dev, name):
+    """A tensor of device dev whose last axis is contiguous; the others may be strided."""
+    if not isinstance(t, _torch_names()[0]):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, got {tuple(t.shape)}")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    _same_device(t, name)
+    _same_device(t, dev, name)
+
+
+def _code(dtype, codes, name):
+    code = codes.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _scratch(like, nbytes):
+    return like.new_empty(max(nbytes, 256), dtype=_torch().uint8)
 
 
 # --------------------------------------------------------------------------- 8-bit integer linear layer
@@ -465,25 +506,29 @@ def quantize_int8(X, s=None, inverse=False, outputs=None):
     weight: W S) or, with inverse=True, by 1 / s (activations: X S^-1); without
     it X is taken as it is."""
     torch = _torch()
-    dt = _dtype_code(X, "X")
-    _req_rows(X, (None, None), "X")
+    dev, stream, codes = _here(X, "X")
+    dt = _code(X.dtype, codes, "X")
+    _req_rows(X, X.dtype, (None, None), dev, "X")
     rows, d_in = X.shape
     mode = 0
     if s is not None:
-        _req_here(s, torch.float32, (d_in,), "s")
+        _req_here(s, torch.float32, (d_in,), dev, "s")
         mode = 2 if inverse else 1
     if outputs is None:
-        q = torch.empty((rows, d_in), dtype=torch.int8, device=X.device)
-        step = torch.empty(rows, dtype=torch.float32, device=X.device)
+        q = X.new_empty((rows, d_in), dtype=torch.int8)
+        step = X.new_empty(rows, dtype=torch.float32)
     else:
         q, step = outputs
-        _req_here(q, torch.int8, (rows, d_in), "q")
-        _req_here(step, torch.float32, (rows,), "step")
-    _check(lib().awq_quantize_int8(X.data_ptr(), dt, X.stride(0) if rows > 1 else max(d_in, 8), _ptr(s), mode, rows,
-                                   d_in, q.data_ptr(), step.data_ptr(), _stream()), "awq_quantize_int8")
+        _req_here(q, torch.int8, (rows, d_in), dev, "q")
+        _req_here(step, torch.float32, (rows,), dev, "step")
+    st = lib().awq_quantize_int8(X.data_ptr(), dt, X.stride(0) if rows > 1 else max(d_in, 8),
+                                 None if s is None else s.data_ptr(), mode, rows, d_in, q.data_ptr(), step.data_ptr(),
+                                 stream)
+    _check(st, "awq_quantize_int8")
     return q, step
 
 
+@functools.lru_cache(maxsize=4096)
 def w8a8_workspace_size(N, d_out, d_in) -> int:
     return int(lib().awq_w8a8_workspace_size(N, d_out, d_in))
 
@@ -493,35 +538,43 @@ def w8a8_gemm(xq, x_step, wq, w_step, dtype=None, bias=None, ws=None, out=None):
     * w_step (+ bias, float32 [d_out]), the integer sum exact; xq int8 [N, d_in]
     and wq int8 [d_out, d_in] with their steps from quantize_int8."""
     torch = _torch()
-    _req_here(xq, torch.int8, None, "xq")
-    _req_here(wq, torch.int8, None, "wq")
+    dev, stream, codes = _here(xq, "xq")
+    _req_here(xq, torch.int8, None, dev, "xq")
+    _req_here(wq, torch.int8, None, dev, "wq")
     if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
         raise ValueError("xq must be [N, d_in] and wq [d_out, d_in]")
     N, d_in = xq.shape
     d_out = wq.shape[0]
-    _req_here(x_step, torch.float32, (N,), "x_step")
-    _req_here(w_step, torch.float32, (d_out,), "w_step")
+    _req_here(x_step, torch.float32, (N,), dev, "x_step")
+    _req_here(w_step, torch.float32, (d_out,), dev, "w_step")
     if bias is not None:
-        _req_here(bias, torch.float32, (d_out,), "bias")
+        _req_here(bias, torch.float32, (d_out,), dev, "bias")
     if out is None:
-        out = torch.empty((N, d_out), dtype=dtype or torch.bfloat16, device=xq.device)
+        dt = _code(dtype or torch.bfloat16, codes, "out")
+        out = xq.new_empty((N, d_out), dtype=dtype or torch.bfloat16)
     else:
-        _req_here(out, dtype or out.dtype, (N, d_out), "out")
-    dt = _dtype_code(out, "out")
+        _req_here(out, dtype or out.dtype, (N, d_out), dev, "out")
+        dt = _code(out.dtype, codes, "out")
     if ws is None:
-        ws = workspace(w8a8_workspace_size(N, d_out, d_in))
+        ws = _scratch(xq, w8a8_workspace_size(N, d_out, d_in))
     else:
-        _same_device(ws, "ws")
-    _check(lib().awq_w8a8_gemm(xq.data_ptr(), x_step.data_ptr(), wq.data_ptr(), w_step.data_ptr(), _ptr(bias), dt, N,
-                               d_out, d_in, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream()),
-           "awq_w8a8_gemm")
+        _same_device(ws, dev, "ws")
+    st = lib().awq_w8a8_gemm(xq.data_ptr(), x_step.data_ptr(), wq.data_ptr(), w_step.data_ptr(),
+                             None if bias is None else bias.data_ptr(), dt, N, d_out, d_in, out.data_ptr(),
+                             ws.data_ptr(), ws.numel() * ws.element_size(), stream)
+    _check(st, "awq_w8a8_gemm")
     return out
 
 
 # --------------------------------------------------------------------------- 4-bit key/value cache
 def kv4_page_bytes(cfg: Kv4Cfg) -> int:
     """Bytes of one (page, kv head) of a cache (0: invalid cfg)."""
-    return int(lib().awq_kv4_page_bytes(ctypes.byref(cfg)))
+    return _kv4_page_bytes(cfg.n_kv_heads, cfg.head_dim, cfg.page_size, cfg.group)
+
+
+@functools.lru_cache(maxsize=256)
+def _kv4_page_bytes(*cfg) -> int:
+    return int(lib().awq_kv4_page_bytes(ctypes.byref(Kv4Cfg(*cfg))))
 
 
 def kv4_new_cache(n_pages, cfg: Kv4Cfg):
@@ -532,11 +585,10 @@ def kv4_new_cache(n_pages, cfg: Kv4Cfg):
     return _torch().zeros((n_pages, cfg.n_kv_heads, nbytes // 4), dtype=_torch().int32, device="cuda")
 
 
-def _req_cache(cache, cfg):
-    torch = _torch()
-    _req_here(cache, torch.int32, None, "cache")
+def _req_cache(cache, cfg, dev):
+    _req_here(cache, _torch().int32, None, dev, "cache")
     words = kv4_page_bytes(cfg) // 4
-    if cache.dim() != 3 or (words and tuple(cache.shape[1:]) != (cfg.n_kv_heads, words)):
+    if cache.dim() != 3 or (words and cache.shape[1:] != (cfg.n_kv_heads, words)):
         raise ValueError(f"cache must be [n_pages, {cfg.n_kv_heads}, {words}], got {tuple(cache.shape)}")
 
 
@@ -544,43 +596,55 @@ def kv4_append(k, v, slots, cache, cfg: Kv4Cfg):
     """Write the keys and values k, v (bf16 or fp16 [T, n_kv_heads, head_dim],
     tokens and heads may be strided) of T tokens to their slots (int32 [T]: page
     * page_size + position; outside the cache: skipped) of the cache, in place."""
-    torch = _torch()
-    dt = _dtype_code(k, "k")
+    dev, stream, codes = _here(k, "k")
+    dt = _code(k.dtype, codes, "k")
     T = k.shape[0] if k.dim() else 0
-    for t, name in ((k, "k"), (v, "v")):
-        _req_rows(t, (T, cfg.n_kv_heads, cfg.head_dim), name)
-    if v.dtype != k.dtype:
+    shape = (T, cfg.n_kv_heads, cfg.head_dim)
+    _req_rows(k, k.dtype, shape, dev, "k")
+    if isinstance(v, _torch().Tensor) and v.dtype is not k.dtype:
         raise ValueError("k and v must have one dtype")
-    _req_here(slots, torch.int32, (T,), "slots")
-    _req_cache(cache, cfg)
-    _check(lib().awq_kv4_append(k.data_ptr(), v.data_ptr(), dt, T, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                                slots.data_ptr(), cache.data_ptr(), cache.shape[0], ctypes.byref(cfg), _stream()),
-           "awq_kv4_append")
+    _req_rows(v, k.dtype, shape, dev, "v")
+    _req_here(slots, _torch().int32, (T,), dev, "slots")
+    _req_cache(cache, cfg, dev)
+    k0, k1, _ = k.stride()
+    v0, v1, _ = v.stride()
+    st = lib().awq_kv4_append(k.data_ptr(), v.data_ptr(), dt, T, k0, k1, v0, v1, slots.data_ptr(), cache.data_ptr(),
+                              cache.shape[0], ctypes.byref(cfg), stream)
+    _check(st, "awq_kv4_append")
     return cache
 
 
 def kv4_gather(cache, slots, cfg: Kv4Cfg, dtype=None, outputs=None):
     """Keys and values [T, n_kv_heads, head_dim] (bf16 by default, or fp16) that
     the cache holds for the T slots; a slot outside the cache reads as zeros."""
-    torch = _torch()
-    _req_cache(cache, cfg)
-    _req_here(slots, torch.int32, None, "slots")
+    dev, stream, codes = _here(cache, "cache")
+    _req_cache(cache, cfg, dev)
+    _req_here(slots, _torch().int32, None, dev, "slots")
     if slots.dim() != 1:
         raise ValueError("slots must be [T]")
     shape = (slots.shape[0], cfg.n_kv_heads, cfg.head_dim)
     if outputs is None:
-        outputs = tuple(torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.device) for _ in range(2))
+        dtype = dtype or _torch().bfloat16
+        dt = _code(dtype, codes, "k")
+        k, v = cache.new_empty(shape, dtype=dtype), cache.new_empty(shape, dtype=dtype)
     else:
-        for t, name in zip(outputs, ("k", "v")):
-            _req_here(t, dtype or outputs[0].dtype, shape, name)
-    k, v = outputs
-    _check(lib().awq_kv4_gather(cache.data_ptr(), cache.shape[0], slots.data_ptr(), shape[0], ctypes.byref(cfg),
-                                k.data_ptr(), v.data_ptr(), _dtype_code(k, "k"), _stream()), "awq_kv4_gather")
+        k, v = outputs
+        dt = _code(dtype or k.dtype, codes, "k")
+        for t, name in ((k, "k"), (v, "v")):
+            _req_here(t, dtype or k.dtype, shape, dev, name)
+    st = lib().awq_kv4_gather(cache.data_ptr(), cache.shape[0], slots.data_ptr(), shape[0], ctypes.byref(cfg),
+                              k.data_ptr(), v.data_ptr(), dt, stream)
+    _check(st, "awq_kv4_gather")
     return k, v
 
 
 def kv4_attention_workspace_size(batch, n_q_heads, max_q, cfg: Kv4Cfg) -> int:
-    return int(lib().awq_kv4_attention_workspace_size(batch, n_q_heads, max_q, ctypes.byref(cfg)))
+    return _kv4_attention_workspace_size(batch, n_q_heads, max_q, cfg.n_kv_heads, cfg.head_dim, cfg.page_size, cfg.group)
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv4_attention_workspace_size(batch, n_q_heads, max_q, *cfg) -> int:
+    return int(lib().awq_kv4_attention_workspace_size(batch, n_q_heads, max_q, ctypes.byref(Kv4Cfg(*cfg))))
 
 
 def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, scale=None, lse=False, ws=None,
@@ -594,37 +658,39 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
     head_dim], or (out, lse float32 [T, n_q_heads]) with lse=True. Rows of no
     sequence are left as they were (unset in a fresh output)."""
     torch = _torch()
-    dt = _dtype_code(q, "q")
-    _req_rows(q, (None, None, cfg.head_dim), "q")
+    dev, stream, codes = _here(q, "q")
+    dt = _code(q.dtype, codes, "q")
+    _req_rows(q, q.dtype, (None, None, cfg.head_dim), dev, "q")
     T, n_q_heads, D = q.shape
-    _req_cache(cache, cfg)
-    _req_here(lens, torch.int32, None, "lens")
-    _req_here(table, torch.int32, None, "table")
+    _req_cache(cache, cfg, dev)
+    _req_here(lens, torch.int32, None, dev, "lens")
+    _req_here(table, torch.int32, None, dev, "table")
     batch = lens.shape[0] if lens.dim() == 1 else -1
     if batch < 0 or table.dim() != 2 or table.shape[0] != batch:
         raise ValueError("lens must be [batch] and table [batch, table_pages]")
     if q_start is not None:
-        _req_here(q_start, torch.int32, (batch + 1,), "q_start")
+        _req_here(q_start, torch.int32, (batch + 1,), dev, "q_start")
         if max_q is None:
             raise ValueError("q_start needs max_q, the most rows of a sequence")
     elif T != batch:
         raise ValueError("without q_start, q must have one row a sequence")
     max_q = 1 if max_q is None else int(max_q)
     if out is None:
-        out = torch.empty((T, n_q_heads, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty((T, n_q_heads, D))
     else:
-        _req_here(out, q.dtype, (T, n_q_heads, D), "out")
-    lse_t = torch.empty((T, n_q_heads), dtype=torch.float32, device=q.device) if lse else None
+        _req_here(out, q.dtype, (T, n_q_heads, D), dev, "out")
+    lse_t = q.new_empty((T, n_q_heads), dtype=torch.float32) if lse else None
     if ws is None:
-        ws = workspace(kv4_attention_workspace_size(batch, n_q_heads, max_q, cfg))
+        ws = _scratch(q, kv4_attention_workspace_size(batch, n_q_heads, max_q, cfg))
     else:
-        _same_device(ws, "ws")
-    if scale is None:
-        scale = D ** -0.5
-    _check(lib().awq_kv4_attention(q.data_ptr(), dt, q.stride(0), q.stride(1), T, n_q_heads, _ptr(q_start), max_q,
-                                   cache.data_ptr(), cache.shape[0], table.data_ptr(), table.shape[1], lens.data_ptr(),
-                                   batch, float(scale), ctypes.byref(cfg), out.data_ptr(), _ptr(lse_t), ws.data_ptr(),
-                                   ws.numel() * ws.element_size(), _stream()), "awq_kv4_attention")
+        _same_device(ws, dev, "ws")
+    q0, q1, _ = q.stride()
+    st = lib().awq_kv4_attention(q.data_ptr(), dt, q0, q1, T, n_q_heads, None if q_start is None else q_start.data_ptr(),
+                                 max_q, cache.data_ptr(), cache.shape[0], table.data_ptr(), table.shape[1],
+                                 lens.data_ptr(), batch, D ** -0.5 if scale is None else float(scale),
+                                 ctypes.byref(cfg), out.data_ptr(), lse_t.data_ptr() if lse else None, ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), stream)
+    _check(st, "awq_kv4_attention")
     return (out, lse_t) if lse else out
 
 

@@ -304,17 +304,17 @@ struct Kv4Warp {
   float m[NT][2], l[NT][2];    // reference exponent (the same in all lanes of a column), sum of p over this lane's tokens
 
   // Rows [r0, r0 + 8 NT) of the sequence's n * share query rows (row = token * share + head in the group).
-  __device__ __forceinline__ void load_queries(const Kv4AttnArgs& a, const Kv4Seq& s, int head, long long r0, int lane) {
+  __device__ __forceinline__ void load_queries(const Kv4AttnArgs& a, const Kv4Seq& s, int head, int r0, int lane) {
     const int g = lane >> 2, q = lane & 3;
-    const long long rows = (long long)s.n * a.share;
+    const int rows = s.n * a.share;
     vis_min = 0x7fffffff;
     vis_max = 0;
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       // this lane loads column g: 8 channels of each 32
-      const long long r = r0 + 8 * u + g;
+      const int r = r0 + 8 * u + g;
       const bool in = r < rows;
-      const int tok = in ? (int)(r / a.share) : 0, e = in ? (int)(r - (long long)tok * a.share) : 0;
+      const int tok = in ? (int)((unsigned)r / (unsigned)a.share) : 0, e = in ? r - tok * a.share : 0;
       const long long off = (s.row0 + tok) * a.q_tok + (long long)(head * a.share + e) * a.q_head;
       const uint16_t* src = a.q + off;
       float x[NJ][8];
@@ -338,28 +338,23 @@ struct Kv4Warp {
       // [2^10, 2^11): fp16 then holds every entry down to 2^-20 of it to 11
       // bits, also the odd channels' 2^-4. Exact back through the scale.
       const int ex = top > 0.0f ? min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -110), 127) : 0;
-      const float f1 = __uint_as_float((uint32_t)(127 + (10 - ex) / 2) << 23);
-      const float f2 = __uint_as_float((uint32_t)(127 + (10 - ex) - (10 - ex) / 2) << 23);
+      const float even = __uint_as_float((uint32_t)(137 - ex) << 23), odd = even * 0.0625f;
       float part[NG];
 #pragma unroll
       for (int gi = 0; gi < NG; ++gi) part[gi] = 0.0f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        __half h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[i] = __float2half_rn(x[j][i] * f1 * f2 * ((i & 1) ? 0.0625f : 1.0f));
-          part[j / JG] += __half2float(h[i]) * ((i & 1) ? 16.0f : 1.0f);
-        }
-        auto two = [&](int lo, int hi) {
-          return (uint32_t)__half_as_ushort(h[lo]) | (uint32_t)__half_as_ushort(h[hi]) << 16;
-        };
-        qf[u][j][0] = two(0, 4);
-        qf[u][j][1] = two(2, 6);
-        qf[u][j][2] = two(1, 5);
-        qf[u][j][3] = two(3, 7);
+        const float(&y)[8] = x[j];
+        part[j / JG] += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+        qf[u][j][0] = pack2<true>(y[0] * even, y[4] * even);
+        qf[u][j][1] = pack2<true>(y[2] * even, y[6] * even);
+        qf[u][j][2] = pack2<true>(y[1] * odd, y[5] * odd);
+        qf[u][j][3] = pack2<true>(y[3] * odd, y[7] * odd);
       }
-      const float unit = exp2f((float)(ex - 10 + 24)) * a.scale_log2;
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) part[gi] *= even;
+      // 2^(ex + 14): through two factors, as 2^14 more than a float's largest may be meant
+      const float unit = __uint_as_float((uint32_t)(117 + ex) << 23) * (16777216.0f * a.scale_log2);
       const int see = in ? s.L - s.n + tok + 1 : 0;
 #pragma unroll
       for (int gi = 0; gi < NG; ++gi) {
@@ -684,27 +679,31 @@ struct Kv4Warp {
 // unit, two with pages of 16, on across tiles); no working warp waits for
 // another until its range is done. A tile that lies in one warp's range is
 // written out by it; the at most two that it shares (its first and its last) go
-// to the workspace as (unnormalised output, m, l), are joined within the block,
-// and where they cross blocks by kv4_attention_join. All joins run in the order
+// to shared memory as (unnormalised output, m, l), are joined within the block,
+// and where they cross blocks, through the workspace, by kv4_attention_join. All joins run in the order
 // of the ranges, so the result is the same every time.
+// A tile's queries, its first reference and its end cost a warp about as much
+// as KV4_EDGE units, so the ranges are cut in a count that has that many more
+// at the front of each tile.
+// With short contexts (the page tables bound them) the blocks' ranges begin and
+// end with tiles instead (`solo`): some blocks then have more to do, but there
+// is nothing to join between blocks and the second launch falls away.
+constexpr int KV4_EDGE = 2;
 constexpr int KV4_MAX_BATCH = 512;  // sequences of a launch: what the block needs of them sits in shared memory
 constexpr int KV4_CTAS = 148;       // blocks of the grid, one per SM
 // Working warps of a block: as many as their state leaves registers for.
 constexpr int kv4_warps(int dim, int group, int nt) {
   return dim * nt > 128 ? 7 : dim / group * nt == 1 || (dim == 64 && nt == 1) ? 15 : 11;
 }
-// units in a warp's ring: three, or two where shared memory holds no more
-constexpr int kv4_stages(int dim, int group, int warps) {
-  return 3 * warps * 2 * kv4_strip_bytes(dim, group) + 17 * 1024 <= 227 * 1024 ? 3 : 2;
-}
+constexpr int KV4_STAGES = 2;       // units in a warp's ring
 
 struct Kv4SplitArgs {
   Kv4AttnArgs a;
   int tile_rows;    // 8 NT
-  float* warp_part; // [working warps of the grid][2][8 NT][D + 4]
   float* cta_part;  // [KV4_CTAS][2][8 NT][D + 4]
   long long* cta_seg;  // [KV4_CTAS][2] tile of a block partial (-1: none)
   int* cta_bad;     // [KV4_CTAS]
+  int solo;         // blocks take whole tiles
   int clear_err;    // the first launch of a call sets the error word, later ones add to it
 };
 
@@ -727,10 +726,10 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Units of the batch: prefix[b] = units before sequence b, units of a tile
-// (span) and tiles of a head of each, and its rows and context.
+// The batch: count[b] = counted units before sequence b, real[b] = units before
+// it; units of a tile (span) and tiles of a head of each, its rows and context.
 struct Kv4Plan {
-  long long prefix[KV4_MAX_BATCH + 1];
+  long long count[KV4_MAX_BATCH + 1], real[KV4_MAX_BATCH + 1];
   int span[KV4_MAX_BATCH], tiles[KV4_MAX_BATCH], row0[KV4_MAX_BATCH], n[KV4_MAX_BATCH], len[KV4_MAX_BATCH];
   int bad;
   __device__ __forceinline__ Kv4Seq seq(int b) const {
@@ -744,73 +743,90 @@ struct Kv4Plan {
 };
 
 // Filled by the whole block.
-__device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, long long* warp_sums) {
+__device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, longlong2* warp_sums) {
   const Kv4AttnArgs& a = s.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (threadIdx.x == 0) {
-    p.prefix[0] = 0;
+    p.count[0] = p.real[0] = 0;
     p.bad = 0;
   }
   __syncthreads();
-  long long before = 0;
+  long long count0 = 0, real0 = 0;
   for (int b0 = 0; b0 < a.batch; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
-    long long n = 0;
+    long long count = 0, real = 0;
     if (b < a.batch) {
       const Kv4Seq q = kv4_seq(a, b);
       if (q.bad) p.bad = 1;
-      const long long rows = (long long)q.n * a.share;
+      const int rows = q.n * a.share;
       // a sequence without context still has its rows to write: one unit, which reads nothing
       const int span = q.n > 0 ? max(1, (int)(((long long)q.L + KV4_UNIT - 1) / KV4_UNIT)) : 0;
-      const int tiles = (int)((rows + s.tile_rows - 1) / s.tile_rows);
+      const int tiles = (rows + s.tile_rows - 1) / s.tile_rows;
       p.span[b] = span;
       p.tiles[b] = tiles;
       p.row0[b] = (int)q.row0;
       p.n[b] = q.n;
       p.len[b] = q.L;
-      n = (long long)span * tiles * a.c.heads;
+      const long long all = (long long)tiles * a.c.heads;
+      real = all * span;
+      count = real + all * (span ? KV4_EDGE : 0);
     }
-    long long inc = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += t;
+      const long long x = __shfl_up_sync(0xffffffffu, count, d), y = __shfl_up_sync(0xffffffffu, real, d);
+      if (lane >= d) {
+        count += x;
+        real += y;
+      }
     }
-    if (lane == 31) warp_sums[warp] = inc;
+    if (lane == 31) warp_sums[warp] = make_longlong2(count, real);
     __syncthreads();
-    for (int w = 0; w < warp; ++w) inc += warp_sums[w];
-    if (b < a.batch) p.prefix[b + 1] = before + inc;
+    for (int w = 0; w < warp; ++w) {
+      count += warp_sums[w].x;
+      real += warp_sums[w].y;
+    }
+    if (b < a.batch) {
+      p.count[b + 1] = count0 + count;
+      p.real[b + 1] = real0 + real;
+    }
     if (b0 + (int)blockDim.x < a.batch) {
-      for (int w = 0; w < warps; ++w) before += warp_sums[w];
+      for (int w = 0; w < warps; ++w) {
+        count0 += warp_sums[w].x;
+        real0 += warp_sums[w].y;
+      }
       __syncthreads();
     }
   }
   __syncthreads();
 }
 
-// First unit of worker w: one unit each at least.
-__device__ __forceinline__ long long kv4_begin(long long w, long long most, long long units) {
-  const long long workers = units < most ? units : most;
-  return w < workers ? w * units / workers : units;
-}
-
 // A place in the order of units.
 struct Kv4Cursor {
   int b, at, span, tile, tiles, head;  // unit `at` of `span` of a tile
-  __device__ __forceinline__ void seek(const Kv4Plan& p, int batch, long long u) {
-    int lo = 0, hi = batch;  // prefix[lo] <= u < prefix[hi]
+  // Counted place u (inside the batch): the unit there, or the tile's first
+  // where u counts its edge. Returns how far u lies behind the tile's begin.
+  __device__ __forceinline__ int seek(const Kv4Plan& p, int batch, long long u) {
+    int lo = 0, hi = batch;  // count[lo] <= u < count[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.prefix[mid] <= u) lo = mid;
+      if (p.count[mid] <= u) lo = mid;
       else hi = mid;
     }
     b = lo;
     span = p.span[b];
     tiles = p.tiles[b];
-    const long long in = u - p.prefix[b], seg = in / span;
-    at = (int)(in - seg * span);
-    head = (int)(seg / tiles);
-    tile = (int)(seg - (long long)head * tiles);
+    const long long in = u - p.count[b];
+    const int wide = span + KV4_EDGE;
+    const int seg = in >> 32 ? (int)(in / wide) : (int)((unsigned)in / (unsigned)wide);
+    const int off = (int)(in - (long long)seg * wide);
+    at = max(0, off - KV4_EDGE);
+    head = (int)((unsigned)seg / (unsigned)tiles);
+    tile = seg - head * tiles;
+    return off;
+  }
+  // units before this place
+  __device__ __forceinline__ long long index(const Kv4Plan& p) const {
+    return p.real[b] + (long long)(head * tiles + tile) * span + at;
   }
   // to the next unit; true if it begins another tile
   __device__ __forceinline__ bool step(const Kv4Plan& p, const Kv4AttnArgs& a) {
@@ -835,12 +851,40 @@ struct Kv4Cursor {
   }
 };
 
+// The range of working warp w (of W) of this block: its first unit in cur, returns their number.
+__device__ __forceinline__ int kv4_range(const Kv4SplitArgs& s, const Kv4Plan& p, int w, int W, Kv4Cursor& cur) {
+  const int batch = s.a.batch;
+  // Where there are fewer counted units than takers, the last takers get none,
+  // so that the parts of a tile always are with neighbours.
+  const long long all = p.count[batch], blocks = min((long long)gridDim.x, all), c = blockIdx.x;
+  if (c >= blocks) return 0;
+  long long c0 = all * c / blocks, c1 = all * (c + 1) / blocks;
+  if (s.solo) {  // up to the begin of a tile
+    Kv4Cursor e;
+    if (c0 < all)
+      if (const int off = e.seek(p, batch, c0)) c0 += e.span + KV4_EDGE - off;
+    if (c1 < all)
+      if (const int off = e.seek(p, batch, c1)) c1 += e.span + KV4_EDGE - off;
+  }
+  const long long warps = min((long long)W, c1 - c0);
+  if (w >= warps) return 0;
+  const long long u0 = c0 + (c1 - c0) * w / warps, u1 = c0 + (c1 - c0) * (w + 1) / warps;
+  long long end = p.real[batch];
+  if (u1 < all) {
+    cur.seek(p, batch, u1);
+    end = cur.index(p);
+  }
+  cur.seek(p, batch, u0);
+  return (int)(end - cur.index(p));
+}
+
 // Query row r (in the sequence's n * share) of a kv head: its row in out and lse; -1 if there is none.
-__device__ __forceinline__ long long kv4_out_row(const Kv4AttnArgs& a, const Kv4Seq& s, int head, long long r) {
-  if (r >= (long long)s.n * a.share) return -1;
-  const long long tok = s.row0 + r / a.share;
+__device__ __forceinline__ long long kv4_out_row(const Kv4AttnArgs& a, const Kv4Seq& s, int head, int r) {
+  if (r >= s.n * a.share) return -1;
+  const int t = (int)((unsigned)r / (unsigned)a.share);
+  const long long tok = s.row0 + t;
   if (!AWQ_IDX_OK(tok, a.T, BS_KV4_O)) return -1;
-  return tok * a.q_heads + head * a.share + (int)(r % a.share);
+  return tok * a.q_heads + head * a.share + (r - t * a.share);
 }
 
 // Row `row` of a tile joined by one warp out of n parts part(0), part(1), ...:
@@ -894,11 +938,13 @@ struct Kv4Joined {
       }
     }
   }
-  __device__ __forceinline__ void store(float* r, int lane) const {
+  // behind m and l: the row of out that this becomes
+  __device__ __forceinline__ void store(float* r, long long at, int lane) const {
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (4 * lane + 128 * k < D) *reinterpret_cast<float4*>(r + 4 * lane + 128 * k) = v[k];
-    if (lane == 0) *reinterpret_cast<float2*>(r + D) = make_float2(m, l);
+    if (lane == 0)
+      *reinterpret_cast<float4*>(r + D) = make_float4(m, l, __int_as_float((int)(at & 0xffffffff)), __int_as_float((int)(at >> 32)));
   }
   __device__ __forceinline__ void write(const Kv4AttnArgs& a, long long at, int lane) const {
     if (at < 0) return;
@@ -919,12 +965,15 @@ template <int D, int G, int NT>
 struct Kv4SplitSmem {
   static constexpr int W = kv4_warps(D, G, NT);
   static constexpr int STRIP = kv4_strip_bytes(D, G);
-  static constexpr int STAGES = kv4_stages(D, G, W);
+  static constexpr int STAGES = KV4_STAGES;
+  static constexpr int PART = 8 * NT * (D + 4);
+  static_assert(PART * (int)sizeof(float) <= STAGES * 2 * STRIP, "a warp's last part lies in its ring");
   alignas(128) uint8_t ring[W][STAGES][2 * STRIP];
+  float part[W][PART];   // a warp's first part
   alignas(8) uint64_t full[W][STAGES];
   uint64_t empty[W][STAGES];
   Kv4Plan plan;
-  long long sums[W + 1];
+  longlong2 sums[W + 1];
   long long seg[W][2];   // tile of a warp's first and last part (-1: none)
   int flags[W][2];       // bit 0: the part begins its tile, bit 1: it ends it
   uint8_t lost[W][4];    // strips of a stage's unit that are not there to be read (by bit)
@@ -934,16 +983,14 @@ struct Kv4SplitSmem {
 
 // Lane i of the producer warp: the units of working warp i.
 template <int D, int G, int NT>
-__device__ __forceinline__ void kv4_produce(const Kv4SplitArgs& s, Kv4SplitSmem<D, G, NT>& sm, long long units, int lane) {
+__device__ __forceinline__ void kv4_produce(const Kv4SplitArgs& s, Kv4SplitSmem<D, G, NT>& sm, int lane) {
   using Sm = Kv4SplitSmem<D, G, NT>;
   constexpr int W = Sm::W, STAGES = Sm::STAGES, STRIP = Sm::STRIP;
   const Kv4AttnArgs& a = s.a;
-  const long long me = (long long)blockIdx.x * W + lane, most = (long long)gridDim.x * W;
-  const long long u0 = kv4_begin(me, most, units), u1 = kv4_begin(me + 1, most, units);
-  int left = lane < W ? (int)(u1 - u0) : 0;
+  Kv4Cursor cur{};
+  int left = lane < W ? kv4_range(s, sm.plan, lane, W, cur) : 0;
   int stage = 0, sent = 0;
   uint32_t phase = 1;  // a fresh ring is empty
-  Kv4Cursor cur;
   int page[2] = {-1, -1};
   // pages of 16 tokens hold one strip of the unit each, larger ones both, one behind the other
   const bool two = a.c.page_shift == 4;
@@ -953,10 +1000,7 @@ __device__ __forceinline__ void kv4_produce(const Kv4SplitArgs& s, Kv4SplitSmem<
     page[0] = p < a.table_pages ? __ldg(row + p) : -1;
     if (two) page[1] = p + 1 < a.table_pages ? __ldg(row + p + 1) : -1;
   };
-  if (left > 0) {
-    cur.seek(sm.plan, a.batch, u0);
-    look();
-  }
+  if (left > 0) look();
   uint64_t idle_since = 0;
   while (__any_sync(0xffffffffu, left > 0)) {
     bool moved = false;
@@ -1020,7 +1064,7 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
     kv4_attention_split(const __grid_constant__ Kv4SplitArgs s) {
   using Sm = Kv4SplitSmem<D, G, NT>;
   using St = Kv4Warp<D, G, NT>;
-  constexpr int W = Sm::W, STAGES = Sm::STAGES, PART = 8 * NT * (D + 4);
+  constexpr int W = Sm::W, STAGES = Sm::STAGES, PART = Sm::PART;
   extern __shared__ uint8_t smem_raw[];
   // (offset, not address, arithmetic keeps the accesses shared-memory ones)
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u));
@@ -1040,33 +1084,40 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
     sm.abort = 0;
   }
   kv4_plan(s, sm.plan, sm.sums);
-  const long long units = sm.plan.prefix[a.batch];
   if (warp == W) {
-    kv4_produce<D, G, NT>(s, sm, units, lane);
-  } else {
-    const long long me = (long long)blockIdx.x * W + warp, most = (long long)gridDim.x * W;
-    const long long u0 = kv4_begin(me, most, units), u1 = kv4_begin(me + 1, most, units);
-    float* my_part = s.warp_part + me * 2 * PART;
-    Kv4Cursor cur;
-    int left = (int)(u1 - u0), stage = 0;
-    uint32_t phase = 0;
-    bool fresh_tile = true, first = true, begins = false;
-    if (left > 0) {
-      cur.seek(sm.plan, a.batch, u0);
-      begins = cur.at == 0;
+    kv4_produce<D, G, NT>(s, sm, lane);
+    if (s.solo && blockIdx.x == 0) {
+      // no second kernel gathers what the blocks found: this warp looks at all
+      // pages of the batch (few, or the call would not be solo)
+      int bad = sm.plan.bad ? ERR_KV4_PAGE : 0;
+      for (int i = lane; i < a.batch * a.table_pages; i += 32) {
+        const int b = i / a.table_pages, p = i - b * a.table_pages, page = __ldg(a.table + i);
+        if (sm.plan.n[b] > 0 && (long long)p << a.c.page_shift < sm.plan.len[b] && (page < 0 || page >= a.c.n_pages))
+          bad = ERR_KV4_PAGE;
+      }
+      bad = __reduce_max_sync(0xffffffffu, bad);
+      if (lane == 0 && (s.clear_err || bad)) *a.err = bad;
     }
+  } else {
+    Kv4Cursor cur;
+    int left = kv4_range(s, sm.plan, warp, W, cur), stage = 0;
+    uint32_t phase = 0;
+    bool fresh_tile = true, first = true, begins = cur.at == 0;
     St w;
     int done = 0;
     while (left > 0) {
       if (fresh_tile) {
-        w.load_queries(a, sm.plan.seq(cur.b), cur.head, (long long)cur.tile * s.tile_rows, lane);
+        w.load_queries(a, sm.plan.seq(cur.b), cur.head, cur.tile * s.tile_rows, lane);
         fresh_tile = false;
         done = 0;
       }
       const bool here = mbar_wait(smem_u32(&sm.full[warp][stage]), phase, &sm.abort, nullptr, 0);
       if (!__all_sync(0xffffffffu, here)) {
-        // a copy that never came: report, write nothing
-        if (lane == 0) sm.bad = ERR_KV4_COPY;
+        // a copy that never came (the wait took two seconds): report, write nothing
+        if (lane == 0) {
+          sm.bad = ERR_KV4_COPY;
+          if (s.solo) *a.err = ERR_KV4_COPY;
+        }
         break;
       }
       const unsigned lost = sm.lost[warp][stage];
@@ -1092,7 +1143,7 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
           for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const long long at = kv4_out_row(a, seq, cur.head, (long long)cur.tile * s.tile_rows + 8 * u + 2 * q + c);
+              const long long at = kv4_out_row(a, seq, cur.head, cur.tile * s.tile_rows + 8 * u + 2 * q + c);
               if (at < 0) continue;
               const float inv = w.l[u][c] == 0.0f ? 0.0f : __fdividef(1.0f, w.l[u][c]);
               uint16_t* o = static_cast<uint16_t*>(a.out) + at * D + g;
@@ -1107,8 +1158,10 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
             }
           __syncwarp();
         } else {
+          // (a last part that is not the first follows the warp's last unit: its ring is free)
           const int k = first ? 0 : 1;
-          w.store(my_part + k * PART, lane);
+          __syncwarp();
+          w.store(k ? reinterpret_cast<float*>(sm.ring[warp][0]) : sm.part[warp], lane);
           if (lane == 0) {
             sm.seg[warp][k] = cur.id(a);
             sm.flags[warp][k] = (begins ? 1 : 0) | (ends ? 2 : 0);
@@ -1126,51 +1179,58 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __threadfence_block();
   __syncthreads();
   // ---------------- join the warps' parts: chains of consecutive parts of one tile
   // lane e of every warp looks at part e (2 W <= 32): which parts begin a chain
   static_assert(2 * W <= 32, "parts of a block");
   const long long my_seg = lane < 2 * W ? sm.seg[lane >> 1][lane & 1] : -1;
+  const int my_flags = lane < 2 * W ? sm.flags[lane >> 1][lane & 1] : 0;
   const unsigned valid = __ballot_sync(0xffffffffu, my_seg >= 0);
   const unsigned below = valid & ((1u << lane) - 1u);
   const long long prev = __shfl_sync(0xffffffffu, my_seg, below ? 31 - __clz(below) : 0);
-  const unsigned heads = __ballot_sync(0xffffffffu, my_seg >= 0 && (!below || prev != my_seg));
-  const int chains = __popc(heads);
-  const int my_flags = lane < 2 * W ? sm.flags[lane >> 1][lane & 1] : 0;
+  unsigned heads = __ballot_sync(0xffffffffu, my_seg >= 0 && (!below || prev != my_seg));
   if (threadIdx.x == 0) {
-    s.cta_bad[blockIdx.x] = sm.bad ? sm.bad : sm.plan.bad ? ERR_KV4_PAGE : 0;
+    if (!s.solo) s.cta_bad[blockIdx.x] = sm.bad ? sm.bad : sm.plan.bad ? ERR_KV4_PAGE : 0;
     // slot 0: a tile that an earlier block began, slot 1: one that a later block ends
-    s.cta_seg[2 * blockIdx.x] = s.cta_seg[2 * blockIdx.x + 1] = -1;
+    if (!s.solo) s.cta_seg[2 * blockIdx.x] = s.cta_seg[2 * blockIdx.x + 1] = -1;
   }
   __syncthreads();
-  const float* base = s.warp_part + (long long)blockIdx.x * W * 2 * PART;
-  for (int it = warp; it < chains * 8 * NT; it += W + 1) {
-    const int ch = it / (8 * NT), row = it - ch * 8 * NT;
-    const int e0 = __fns(heads, 0, ch + 1);
+  for (int turn = 0; heads; ++turn) {
+    const int e0 = __ffs(heads) - 1;
+    heads &= heads - 1;
     const long long seg = __shfl_sync(0xffffffffu, my_seg, e0);
     const unsigned mine = __ballot_sync(0xffffffffu, my_seg == seg);
     const int flags = __reduce_or_sync(0xffffffffu, (unsigned)(my_seg == seg ? my_flags : 0));
-    Kv4Joined<D> j;
-    // the i-th part of the chain: e0, then slot 0 of the warps behind
-    j.join([&](int i) { return base + (long long)(i == 0 ? e0 : 2 * ((e0 >> 1) + i)) * PART; }, __popc(mine), row, lane);
-    if (flags == 3) {
-      const int head_b = (int)(seg >> 32), b = head_b / a.c.heads, head = head_b - b * a.c.heads;
-      j.write(a, kv4_out_row(a, sm.plan.seq(b), head, (long long)(int)(seg & 0xffffffff) * s.tile_rows + row), lane);
-    } else {
-      // shared with other blocks: slot 1 if it begins here, else 0
-      const int k = flags & 1;
-      j.store(s.cta_part + ((long long)blockIdx.x * 2 + k) * PART + row * (D + 4), lane);
-      if (row == 0 && lane == 0) s.cta_seg[2 * blockIdx.x + k] = seg;
+    const int b = (int)(seg >> 32) / a.c.heads, head = (int)(seg >> 32) - b * a.c.heads;
+    // rows go round the warps, on from where the last chain's stopped
+    for (int row = (warp + (W + 1) * 8 * NT - turn * 8 * NT % (W + 1)) % (W + 1); row < 8 * NT; row += W + 1) {
+      const long long at = kv4_out_row(a, sm.plan.seq(b), head, (int)(seg & 0xffffffff) * s.tile_rows + row);
+      Kv4Joined<D> j;
+      // the i-th part of the chain: e0, then the first parts of the warps behind
+      j.join(
+          [&](int i) -> const float* {
+            return i == 0 && (e0 & 1) ? reinterpret_cast<const float*>(sm.ring[e0 >> 1][0]) : sm.part[(e0 >> 1) + i];
+          },
+          __popc(mine), row, lane);
+      if (flags == 3) {
+        j.write(a, at, lane);
+      } else if (!s.solo) {
+        // shared with other blocks: slot 1 if it begins here, else 0
+        const int k = flags & 1;
+        j.store(s.cta_part + ((long long)blockIdx.x * 2 + k) * PART + row * (D + 4), at, lane);
+        if (row == 0 && lane == 0) s.cta_seg[2 * blockIdx.x + k] = seg;
+      }
     }
   }
 }
+
+constexpr int KV4_JOIN_WARPS = 16;
 
 // Block c joins the tile that block c of the split began and did not end:
 // its slot 1, then slot 0 of the following blocks while they hold that tile.
 // Block 0 sets the call's error word. Launched to overlap the split's end.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) kv4_attention_join(const __grid_constant__ Kv4SplitArgs s, int ctas) {
+__global__ void __launch_bounds__(32 * KV4_JOIN_WARPS) kv4_attention_join(const __grid_constant__ Kv4SplitArgs s, int ctas) {
   constexpr int PART = 8 * NT * (D + 4);
   const Kv4AttnArgs& a = s.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
@@ -1182,7 +1242,6 @@ __global__ void __launch_bounds__(256) kv4_attention_join(const __grid_constant_
     if (lane == 0 && (s.clear_err || bad)) *a.err = bad;
   }
   const long long seg = s.cta_seg[2 * c + 1];
-  if (seg < 0) return;
   int n = 1;
   for (int i = c + 1; i < ctas; i += 32) {  // how many blocks behind hold the tile
     const bool same = i + lane < ctas && s.cta_seg[2 * (i + lane)] == seg;
@@ -1191,13 +1250,12 @@ __global__ void __launch_bounds__(256) kv4_attention_join(const __grid_constant_
     n += k;
     if (k < 32) break;
   }
-  const int head_b = (int)(seg >> 32), b = head_b / a.c.heads, head = head_b - b * a.c.heads;
-  const Kv4Seq seq = kv4_seq(a, b);
-  for (int row = warp; row < 8 * NT; row += 8) {
-    const long long at = kv4_out_row(a, seq, head, (long long)(int)(seg & 0xffffffff) * s.tile_rows + row);
-    if (at < 0) continue;
+  if (seg < 0) return;
+  for (int row = warp; row < 8 * NT; row += KV4_JOIN_WARPS) {
+    const float* first = s.cta_part + ((long long)c * 2 + 1) * PART + row * (D + 4) + D;
+    const long long at = (long long)__float_as_int(first[3]) << 32 | (unsigned)__float_as_int(first[2]);
     Kv4Joined<D> j;
-    j.join([&](int i) { return s.cta_part + ((long long)(c + i) * 2 + (i == 0)) * PART; }, n, row, lane);
+    j.join([&](int i) -> const float* { return s.cta_part + ((long long)(c + i) * 2 + (i == 0)) * PART; }, n, row, lane);
     j.write(a, at, lane);
   }
 }

@@ -2,17 +2,27 @@
 // 4-bit key/value cache with its attention (declared in include/awq.h).
 // Included after awq_api.cu, whose host helpers it uses.
 #pragma once
+#include <atomic>
+
 #include "kv4_sm100.cuh"
 #include "w8a8_sm100.cuh"
 
 namespace {
 
-// A kernel launched behind another that uses most of shared memory asks for the
-// same split of L1, so that the SMs are not reconfigured between the two.
+// Shared memory of a kernel, set once a context (an attribute call costs about
+// a microsecond, as much as a small launch's share of it). All kernels of a
+// chain ask for the largest split of L1, so that the SMs are not reconfigured
+// between them. `once` belongs to the one kernel.
 template <typename K>
-bool big_carveout(K kernel) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
-         cudaSuccess;
+bool kernel_smem(K kernel, int smem, std::atomic<unsigned long long>& once) {
+  const unsigned long long ctx = current_context_id();
+  if (ctx != 0 && once.load(std::memory_order_relaxed) == ctx) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+          cudaSuccess)
+    return false;
+  once.store(current_context_id(), std::memory_order_relaxed);
+  return true;
 }
 
 // Launch that may start while the kernel before it on the stream ends
@@ -164,28 +174,33 @@ awq_status check_kv4_attention(int64_t batch, int64_t n_q_heads, int64_t max_q, 
   if (st != AWQ_OK) return st;
   if (batch < 1 || batch > 65535 || n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c->n_kv_heads != 0)
     return AWQ_ERR_SHAPE;
-  if (max_q < 1 || max_q > (1 << 24)) return AWQ_ERR_SHAPE;
+  if (max_q < 1 || max_q > (1 << 24) || max_q * (n_q_heads / c->n_kv_heads) > (1 << 30)) return AWQ_ERR_SHAPE;
   return AWQ_OK;
 }
 
+// Contexts of at most this many tokens (as the page tables bound them) are not
+// split between blocks, if the tables are small enough for one warp to check.
+#ifndef KV4_SOLO
+#define KV4_SOLO 2048
+#endif
+constexpr int64_t KV4_SOLO_TOKENS = KV4_SOLO, KV4_SOLO_PAGES = 4096;
+
 // Workspace of the attention: [0, kAlign) error word, then the block flags and
-// tiles and the partial outputs of blocks and warps.
+// tiles and the blocks' partial outputs.
 struct Kv4Layout {
-  int nt, warps;
-  size_t off_bad, off_seg, off_cta, off_warp, total;
+  int nt;
+  size_t off_bad, off_seg, off_cta, total;
 };
 
 Kv4Layout kv4_layout(int64_t n_q_heads, int64_t max_q, const awq_kv4cfg* c) {
   Kv4Layout L{};
   const long long rows = max_q * (n_q_heads / c->n_kv_heads);
   L.nt = rows > 8 && c->head_dim <= 128 ? 2 : 1;
-  L.warps = kv4_warps(c->head_dim, c->group, L.nt);
   const size_t part = (size_t)8 * L.nt * (c->head_dim + 4) * sizeof(float);
   size_t off = kAlign;
   L.off_bad = off;   off += align_up(KV4_CTAS * sizeof(int));
   L.off_seg = off;   off += align_up(KV4_CTAS * 2 * sizeof(long long));
   L.off_cta = off;   off += align_up(KV4_CTAS * 2 * part);
-  L.off_warp = off;  off += align_up((size_t)KV4_CTAS * L.warps * 2 * part);
   L.total = off;
   return L;
 }
@@ -264,9 +279,9 @@ extern "C" awq_status awq_w8a8_gemm(const int8_t* xq, const float* x_step, const
   CUtensorMap tw, tx;
   if (!make_map_u8(&tw, wq, d_out, d_in, W8_BM) || !make_map_u8(&tx, xq, N, d_in, p.b_rows)) return AWQ_ERR_CUDA;
   const bool f16 = dtype == AWQ_DTYPE_F16;
+  static std::atomic<unsigned long long> once[4];
   auto launch = [&](auto kernel) -> awq_status {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem) != cudaSuccess)
-      return AWQ_ERR_CUDA;
+    if (!kernel_smem(kernel, W8_SMEM_LIMIT, once[(p.pair ? 2 : 0) + (f16 ? 1 : 0)])) return AWQ_ERR_CUDA;
     kernel<<<p.pair ? 2 * p.workers : p.workers, W8_THREADS, p.smem, cs>>>(tw, tx, a);
     return launch_status();
   };
@@ -387,7 +402,6 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   a.err = at<int>(ws, 0);
   Kv4SplitArgs sa{};
   sa.tile_rows = 8 * L.nt;
-  sa.warp_part = at<float>(ws, L.off_warp);
   sa.cta_part = at<float>(ws, L.off_cta);
   sa.cta_seg = at<long long>(ws, L.off_seg);
   sa.cta_bad = at<int>(ws, L.off_bad);
@@ -399,6 +413,7 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
     if (q_start) sa.a.q_start += first;
     sa.a.row_first = (int)first;
     sa.clear_err = first == 0;
+    sa.solo = table_pages * cfg->page_size <= KV4_SOLO_TOKENS && sa.a.batch * table_pages <= KV4_SOLO_PAGES;
     st = kv4_shapes(cfg->head_dim, cfg->group, [&](auto d, auto g) -> awq_status {
       constexpr int D = decltype(d)::value, G = decltype(g)::value;
       auto launch = [&](auto nt) -> awq_status {
@@ -407,11 +422,11 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
         static_assert(smem <= 232448, "shared memory of the split attention");
         auto k = kv4_attention_split<D, G, NT>;
         auto j = kv4_attention_join<D, NT>;
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess || !big_carveout(j))
-          return AWQ_ERR_CUDA;
+        static std::atomic<unsigned long long> once_k{0}, once_j{0};
+        if (!kernel_smem(k, smem, once_k) || !kernel_smem(j, 0, once_j)) return AWQ_ERR_CUDA;
         k<<<KV4_CTAS, 32 * (kv4_warps(D, G, NT) + 1), smem, cs>>>(sa);
-        if ((st = launch_status()) != AWQ_OK) return st;
-        return launch_behind(j, dim3(KV4_CTAS), dim3(256), 0, cs, sa, KV4_CTAS);
+        if ((st = launch_status()) != AWQ_OK || sa.solo) return st;
+        return launch_behind(j, dim3(KV4_CTAS), dim3(32 * KV4_JOIN_WARPS), 0, cs, sa, KV4_CTAS);
       };
       return L.nt == 2 ? launch(std::integral_constant<int, D <= 128 ? 2 : 1>{}) : launch(std::integral_constant<int, 1>{});
     });
