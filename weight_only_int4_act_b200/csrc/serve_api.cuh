@@ -235,12 +235,29 @@ extern "C" awq_status awq_quantize_int8(const void* x, awq_dtype dtype, int64_t 
     return AWQ_ERR_INVALID_ARG;
   if (rows < 1 || rows > INT32_MAX / 2 || d_in < 16 || d_in % 16 != 0 || d_in > W8_MAX_K) return AWQ_ERR_SHAPE;
   if (ldx < d_in || ldx % 8 != 0) return AWQ_ERR_SHAPE;
-  awq_status st = check_device(nullptr);
+  int sms = 0;
+  awq_status st = check_device(&sms);
   if (st != AWQ_OK) return st;
   cudaStream_t cs = as_stream(stream);
+  // Few rows: as many threads as a row has chunks of 8 channels, for its
+  // latency. Many: up to four chunks a thread, so that several blocks fit an SM
+  // and one row's reduction hides under another's loads.
+  const int64_t n8 = d_in / 8;
+  const int ch = rows <= 2 * sms ? (n8 <= 1024 ? 1 : 2) : n8 <= 256 ? 1 : n8 <= 512 ? 2 : 4;
+  const unsigned threads = (unsigned)(cdiv(cdiv(n8, ch), 32) * 32);
+  const int64_t resident = (int64_t)sms * (threads <= 64 ? 16 : threads <= 128 ? 8 : threads <= 256 ? 3 : 1);
+  const unsigned grid = (unsigned)(rows < resident ? rows : resident);
   auto launch = [&](auto f16, auto m) {
-    quantize_int8_rows<decltype(f16)::value, decltype(m)::value>
-        <<<(unsigned)rows, 256, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
+    constexpr bool F = decltype(f16)::value;
+    constexpr int M = decltype(m)::value;
+    if (threads > (ch == 4 ? 512u : 1024u))
+      quantize_int8_long<F, M><<<(unsigned)(rows < 2 * sms ? rows : 2 * sms), 1024, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
+    else if (ch == 1)
+      quantize_int8_rows<F, M, 1><<<grid, threads, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
+    else if (ch == 2)
+      quantize_int8_rows<F, M, 2><<<grid, threads, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
+    else
+      quantize_int8_rows<F, M, 4><<<grid, threads, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
     return launch_status();
   };
   auto modes = [&](auto f16) {

@@ -38,72 +38,135 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
 // leaves a unit in the last place of 1, and the low byte is the integer's.
 __device__ __forceinline__ uint32_t round_bits(float x) { return __float_as_uint(__fadd_rn(x, 12582912.0f)); }
 
-// One block per row; 16 channels (32 bytes in, 16 bytes out) per thread and turn.
+// The row's largest |v| as bits: for floats without their sign the order of the
+// bits is the order of the values, infinity and NaN above all finite ones.
+constexpr uint32_t Q8_INF = 0x7f800000u, Q8_FLOOR = 0x322bcc77u;  // infinity, 1e-8f
+
+// 8 channels of a row: v = x, x s or x (1 / s).
 template <bool F16, int MODE>
-__global__ void __launch_bounds__(256)
-    quantize_int8_rows(const void* __restrict__ xv, long long ldx, const float* __restrict__ s, long long rows, int d_in,
+__device__ __forceinline__ void q8_values(const uint4& raw, const float (&f)[8], float (&v)[8]) {
+  const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = widen2<F16>(u[i]);
+    v[2 * i] = MODE == Q8_PLAIN ? p.x : __fmul_rn(p.x, f[2 * i]);
+    v[2 * i + 1] = MODE == Q8_PLAIN ? p.y : __fmul_rn(p.y, f[2 * i + 1]);
+  }
+}
+template <int MODE>
+__device__ __forceinline__ void q8_factors(const float* __restrict__ s, int c, float (&f)[8]) {
+  if constexpr (MODE != Q8_PLAIN) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(s) + 2 * c), b = __ldg(reinterpret_cast<const float4*>(s) + 2 * c + 1);
+    const float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = MODE == Q8_MUL ? g[i] : __frcp_rn(g[i]);
+  }
+}
+__device__ __forceinline__ uint32_t q8_top(const float (&v)[8], uint32_t top) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  return top;
+}
+// 8 codes; a row that is not finite gets zeros.
+__device__ __forceinline__ uint2 q8_codes(const float (&v)[8], float inv, bool finite) {
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = round_bits(__fmul_rn(v[i], inv));
+  const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  return finite ? make_uint2(lo, hi) : make_uint2(0, 0);
+}
+// The maximum over the block; red: 32 words, not in use by the call before.
+__device__ __forceinline__ uint32_t q8_block_max(uint32_t top, uint32_t* red) {
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+  __syncthreads();
+  return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : 0u);
+}
+
+// A block takes rows blockIdx.x, + gridDim.x, ...; a thread keeps CH fixed
+// chunks of 8 channels (tid + k blockDim), so 1 / s is taken once a launch and
+// a row is read once: it stays in registers between its maximum and its codes,
+// and the next row's loads are under way meanwhile. Bound by HBM (3 bytes a
+// channel); 16384 x 8192 bf16 with 1 / s: see the design document's table.
+template <bool F16, int MODE, int CH>
+__global__ void quantize_int8_rows(const void* __restrict__ xv, long long ldx, const float* __restrict__ s, long long rows,
+                                   int d_in, int8_t* __restrict__ q, float* __restrict__ step) {
+  const uint16_t* x = static_cast<const uint16_t*>(xv);
+  __shared__ uint32_t red[2][32];
+  const int n8 = d_in / 8, tid = threadIdx.x, T = blockDim.x;
+  float f[CH][8];
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+    if (tid + k * T < n8) q8_factors<MODE>(s, tid + k * T, f[k]);
+  uint4 next[CH];
+  auto load = [&](long long r) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+      next[k] = r < rows && tid + k * T < n8 && AWQ_SPAN_OK(r * ldx + 8 * (tid + k * T), 8, (rows - 1) * ldx + d_in, BS_Q8_IN)
+                    ? __ldcs(reinterpret_cast<const uint4*>(x + r * ldx) + tid + k * T)
+                    : make_uint4(0, 0, 0, 0);
+  };
+  load(blockIdx.x);
+  int turn = 0;
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
+    uint4 raw[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) raw[k] = next[k];
+    load(r + gridDim.x);
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+      if (tid + k * T < n8) {
+        float v[8];
+        q8_values<F16, MODE>(raw[k], f[k], v);
+        top = q8_top(v, top);
+      }
+    top = q8_block_max(top, red[turn]);
+    const bool finite = top < Q8_INF;
+    const float most = __uint_as_float(max(top, Q8_FLOOR)), inv = __fdiv_rn(127.0f, most);
+    if (tid == 0 && AWQ_IDX_OK(r, rows, BS_Q8_STEP)) step[r] = finite ? __fdiv_rn(most, 127.0f) : __int_as_float(0x7fffffff);
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+      if (tid + k * T < n8) {
+        float v[8];
+        q8_values<F16, MODE>(raw[k], f[k], v);
+        const int c = tid + k * T;
+        if (AWQ_SPAN_OK(r * d_in + 8 * c, 8, rows * d_in, BS_Q8_CODES))
+          *reinterpret_cast<uint2*>(q + r * d_in + 8 * c) = q8_codes(v, inv, finite);
+      }
+  }
+}
+
+// Rows too long for registers: read twice (the second time mostly out of L2).
+template <bool F16, int MODE>
+__global__ void __launch_bounds__(1024)
+    quantize_int8_long(const void* __restrict__ xv, long long ldx, const float* __restrict__ s, long long rows, int d_in,
                        int8_t* __restrict__ q, float* __restrict__ step) {
   const uint16_t* x = static_cast<const uint16_t*>(xv);
-  __shared__ float red[8];
-  const int n16 = d_in / 16;
-  for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+  __shared__ uint32_t red[2][32];
+  const int n8 = d_in / 8;
+  int turn = 0;
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
     const uint4* row = reinterpret_cast<const uint4*>(x + r * ldx);
-    auto load = [&](int c, float (&v)[16]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 w = __ldg(row + 2 * c + h);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = widen2<F16>(u[i]);
-          v[8 * h + 2 * i] = f.x;
-          v[8 * h + 2 * i + 1] = f.y;
-        }
-      }
-      if constexpr (MODE != Q8_PLAIN) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float si = __ldg(s + 16 * c + i);
-          v[i] = __fmul_rn(v[i], MODE == Q8_MUL ? si : __frcp_rn(si));
-        }
-      }
-    };
-    float top = 0.0f;
-    bool bad = false;
-    for (int c = threadIdx.x; c < n16; c += blockDim.x) {
-      float v[16];
-      load(c, v);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        top = fmaxf(top, fabsf(v[i]));
-        bad |= !(fabsf(v[i]) <= 3.402823466e38f);
-      }
+    uint32_t top = 0;
+    for (int c = threadIdx.x; c < n8; c += blockDim.x) {
+      float f[8], v[8];
+      q8_factors<MODE>(s, c, f);
+      q8_values<F16, MODE>(__ldg(row + c), f, v);
+      top = q8_top(v, top);
     }
-    if (bad) top = __int_as_float(0x7f800000);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-    __syncthreads();
-    top = red[0];
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) top = fmaxf(top, red[w]);
-    const bool finite = top <= 3.402823466e38f;
-    top = fmaxf(top, 1e-8f);
-    const float inv = __fdiv_rn(127.0f, top);
+    top = q8_block_max(top, red[turn]);
+    const bool finite = top < Q8_INF;
+    const float most = __uint_as_float(max(top, Q8_FLOOR)), inv = __fdiv_rn(127.0f, most);
     if (threadIdx.x == 0 && AWQ_IDX_OK(r, rows, BS_Q8_STEP))
-      step[r] = finite ? __fdiv_rn(top, 127.0f) : __int_as_float(0x7fffffff);
-    for (int c = threadIdx.x; c < n16; c += blockDim.x) {
-      float v[16];
-      load(c, v);
-      uint32_t out[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a = round_bits(__fmul_rn(v[4 * i], inv)), b = round_bits(__fmul_rn(v[4 * i + 1], inv));
-        const uint32_t e = round_bits(__fmul_rn(v[4 * i + 2], inv)), f = round_bits(__fmul_rn(v[4 * i + 3], inv));
-        out[i] = finite ? __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(e, f, 0x0040), 0x5410) : 0u;
-      }
-      if (AWQ_SPAN_OK(r * d_in + 16 * c, 16, rows * d_in, BS_Q8_CODES))
-        *reinterpret_cast<uint4*>(q + r * d_in + 16 * c) = make_uint4(out[0], out[1], out[2], out[3]);
+      step[r] = finite ? __fdiv_rn(most, 127.0f) : __int_as_float(0x7fffffff);
+    for (int c = threadIdx.x; c < n8; c += blockDim.x) {
+      float f[8], v[8];
+      q8_factors<MODE>(s, c, f);
+      q8_values<F16, MODE>(__ldg(row + c), f, v);
+      if (AWQ_SPAN_OK(r * d_in + 8 * c, 8, rows * d_in, BS_Q8_CODES))
+        *reinterpret_cast<uint2*>(q + r * d_in + 8 * c) = q8_codes(v, inv, finite);
     }
   }
 }
