@@ -46,73 +46,69 @@ awq_status launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
 bool dtype_ok(awq_dtype d) { return d == AWQ_DTYPE_BF16 || d == AWQ_DTYPE_F16; }
 
 // ------------------------------------------------------------------ 8-bit integer linear layer
+constexpr double W8_EPILOGUE_BYTES = 80.0 * 10;  // a token's part of an epilogue: about 10 ns, at 80 bytes a ns
+
 awq_status check_w8(int64_t N, int64_t d_out, int64_t d_in) {
   if (N < 1 || d_out < 1 || d_in < 16 || d_in % 16 != 0 || d_in > W8_MAX_K) return AWQ_ERR_SHAPE;
   if (d_out > (1 << 24) || N > (1 << 24)) return AWQ_ERR_SHAPE;
-  if (N * d_out > (int64_t)INT32_MAX * 8) return AWQ_ERR_SHAPE;
   return AWQ_OK;
 }
 
 struct W8Plan {
-  bool pair;
-  int bm, bn, b_rows, workers, slots, smem;
-  long long tiles;
+  bool small, pair;
+  int b_rows, ctas, smem;
   W8Args a;
-  size_t ws;
 };
 
 W8Plan w8_plan(int64_t N, int64_t d_out, int64_t d_in) {
   W8Plan p{};
-  p.pair = N > 64;
-  p.bm = p.pair ? 2 * W8_BM : W8_BM;
-  const int step = p.pair ? 32 : 16;
-  const long long nb = cdiv(N, 256);
-  p.bn = (int)(cdiv(cdiv(N, nb), step) * step);
-  p.b_rows = p.pair ? p.bn / 2 : p.bn;
   W8Args& a = p.a;
   a.N = (int)N;
   a.d_out = (int)d_out;
-  a.bn = p.bn;
-  a.n_mb = (int)cdiv(d_out, p.bm);
-  a.n_nb = (int)cdiv(N, p.bn);
   a.n_kb = (int)cdiv(d_in, W8_BK);
+  p.small = N <= W8_SMALL_N;
+  if (p.small) {
+    a.bn = (int)(cdiv(N, 16) * 16);
+    p.b_rows = a.bn;
+    a.n_mb = (int)cdiv(d_out, W8_BM);
+    a.n_nb = 1;
+    a.cols = a.bn <= 32 ? 32 : a.bn <= 64 ? 64 : 128;
+    // three CTAs to an SM (two of the widest tiles): the ring covers the loads'
+    // latency together with the neighbours', and holds [bn][128] int32
+    const int per_sm = a.bn <= 64 ? 3 : 2;
+    a.stages = (W8_SMEM_LIMIT / per_sm - 1024 - w8_small_smem(0, a.bn)) / w8_stage_bytes(a.bn);
+    p.smem = w8_small_smem(a.stages, a.bn);
+    // as many CTAs share a tile as fill the SMs once, at least four K steps each
+    a.split = 1;
+    while (a.split < 8 && (int64_t)a.n_mb * a.split * 2 <= (int64_t)W8_SMS * per_sm && a.n_kb / (a.split * 2) >= 4) a.split *= 2;
+    p.ctas = a.n_mb * a.split;
+    return p;
+  }
+  // The tile shape whose workers have the fewest bytes to fetch into an SM: the
+  // waves of tiles times a tile's K steps, and an epilogue in plain sight at
+  // the end, about as long as one byte a ns and token.
+  double best = 0.0;
+  for (int pair = 0; pair < 2; ++pair)
+    for (int bn = 64; bn <= 256; bn += 32) {
+      const int bm = pair ? 2 * W8_BM : W8_BM, rows = pair ? bn / 2 : bn, G = pair ? W8_SMS / 2 : W8_SMS;
+      const double waves = (double)cdiv(cdiv(d_out, bm) * cdiv(N, bn), G);
+      const double cost = waves * a.n_kb * w8_stage_bytes(rows) + W8_EPILOGUE_BYTES * bn;
+      if (best == 0.0 || cost < best) {
+        best = cost;
+        p.pair = pair != 0;
+        a.bn = bn;
+      }
+    }
+  p.b_rows = p.pair ? a.bn / 2 : a.bn;
+  a.n_mb = (int)cdiv(d_out, p.pair ? 2 * W8_BM : W8_BM);
+  a.n_nb = (int)cdiv(N, a.bn);
   a.group_nb = a.n_nb < 8 ? a.n_nb : 8;
-  int st = (W8_SMEM_LIMIT - w8_smem_bytes(0, p.b_rows)) / w8_stage_bytes(p.b_rows);
+  const int st = (W8_SMEM_LIMIT - w8_smem_bytes(0, p.b_rows)) / w8_stage_bytes(p.b_rows);
   a.stages = st < W8_MAX_STAGES ? st : W8_MAX_STAGES;
   p.smem = w8_smem_bytes(a.stages, p.b_rows);
-  p.tiles = (long long)a.n_mb * a.n_nb;
-  const int G = p.pair ? W8_SMS / 2 : W8_SMS;
-  // whole waves first; what is left (one to two waves, or all tiles where
-  // there are fewer) in equal ranges, unless it is whole waves as well or the
-  // uneven last wave is a small part of the whole
-  const long long waves = p.tiles / G;
-  const bool even = p.tiles % G == 0 || waves >= 4 || a.n_kb < 2;
-  const long long split = even ? 0 : p.tiles - (waves > 1 ? (waves - 1) * G : 0);
-  a.whole = (int)(p.tiles - split);
-  a.units = split * a.n_kb;
-  // at least 4 K steps a worker
-  p.workers = split == 0 ? (int)(p.tiles < G ? p.tiles : G) : a.whole ? G : (int)(a.units / 4 < G ? (a.units / 4 > 1 ? a.units / 4 : 1) : G);
-  p.slots = 1;
-  for (long long t = 0; t < split; ++t) {
-    const long long n = w4_sk_cta(t * a.n_kb + a.n_kb - 1, p.workers, a.units) - w4_sk_cta(t * a.n_kb, p.workers, a.units) + 1;
-    if (n > p.slots) p.slots = (int)n;
-  }
-  a.p_stride = (N * d_out + 3) / 4 * 4;
-  p.ws = kAlign + (p.slots > 1 ? align_up((size_t)p.slots * a.p_stride * sizeof(int)) : 0);
+  const int64_t tiles = (int64_t)a.n_mb * a.n_nb, G = p.pair ? W8_SMS / 2 : W8_SMS;
+  p.ctas = (int)(tiles < G ? tiles : G) * (p.pair ? 2 : 1);
   return p;
-}
-
-// The split tiles of a plan (each found at its first inner range boundary), with their slab counts.
-void w8_fixups(const W8Plan& p, W8Fixups& fx) {
-  fx.n = 0;
-  const long long U = p.a.units, k = p.a.n_kb;
-  for (long long c = 1; c < p.workers && U > 0; ++c) {
-    const long long b = w4_sk_begin(c, p.workers, U), tile = b / k, t0 = tile * k;
-    if (b == t0 || w4_sk_cta(t0, p.workers, U) != c - 1) continue;
-    fx.tile[fx.n] = (int)(p.a.whole + tile);
-    fx.ns[fx.n] = (short)(w4_sk_cta(t0 + k - 1, p.workers, U) - (c - 1) + 1);
-    ++fx.n;
-  }
 }
 
 // 2-D map of bytes over a row-major [rows, cols] matrix, box of 128 columns (one swizzled row) x box_rows.
@@ -270,7 +266,7 @@ extern "C" awq_status awq_quantize_int8(const void* x, awq_dtype dtype, int64_t 
 
 extern "C" size_t awq_w8a8_workspace_size(int64_t N, int64_t d_out, int64_t d_in) {
   if (check_w8(N, d_out, d_in) != AWQ_OK) return 0;
-  return w8_plan(N, d_out, d_in).ws;
+  return kAlign;
 }
 
 extern "C" awq_status awq_w8a8_gemm(const int8_t* xq, const float* x_step, const int8_t* wq, const float* w_step,
@@ -282,38 +278,45 @@ extern "C" awq_status awq_w8a8_gemm(const int8_t* xq, const float* x_step, const
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(Y, 16) || !aligned(x_step, 4) || !aligned(w_step, 4) ||
       !aligned(bias, 4) || !aligned(ws, 256))
     return AWQ_ERR_INVALID_ARG;
-  W8Plan p = w8_plan(N, d_out, d_in);
-  if (ws_bytes < p.ws) return AWQ_ERR_WORKSPACE;
+  if (ws_bytes < kAlign) return AWQ_ERR_WORKSPACE;
   if ((st = check_device(nullptr)) != AWQ_OK) return st;
+  W8Plan p = w8_plan(N, d_out, d_in);
   cudaStream_t cs = as_stream(stream);
   W8Args& a = p.a;
   a.dx = x_step;
   a.dw = w_step;
   a.bias = bias;
   a.Y = Y;
-  a.P = at<int>(ws, kAlign);
   a.err = at<int>(ws, 0);
   CUtensorMap tw, tx;
   if (!make_map_u8(&tw, wq, d_out, d_in, W8_BM) || !make_map_u8(&tx, xq, N, d_in, p.b_rows)) return AWQ_ERR_CUDA;
   const bool f16 = dtype == AWQ_DTYPE_F16;
-  static std::atomic<unsigned long long> once[4];
+  static std::atomic<unsigned long long> once[6];
+  if (p.small) {
+    auto launch = [&](auto kernel) -> awq_status {
+      if (!kernel_smem(kernel, W8_SMEM_LIMIT / 2, once[f16 ? 1 : 0])) return AWQ_ERR_CUDA;
+      cudaLaunchConfig_t c{};
+      c.gridDim = dim3((unsigned)p.ctas);
+      c.blockDim = dim3(W8_SMALL_THREADS);
+      c.dynamicSmemBytes = p.smem;
+      c.stream = cs;
+      cudaLaunchAttribute at{};
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = (unsigned)a.split;
+      at.val.clusterDim.y = at.val.clusterDim.z = 1;
+      c.attrs = &at;
+      c.numAttrs = 1;
+      return cudaLaunchKernelEx(&c, kernel, tw, tx, a) == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+    };
+    return f16 ? launch(w8a8_small_tcgen05<true>) : launch(w8a8_small_tcgen05<false>);
+  }
   auto launch = [&](auto kernel) -> awq_status {
-    if (!kernel_smem(kernel, W8_SMEM_LIMIT, once[(p.pair ? 2 : 0) + (f16 ? 1 : 0)])) return AWQ_ERR_CUDA;
-    kernel<<<p.pair ? 2 * p.workers : p.workers, W8_THREADS, p.smem, cs>>>(tw, tx, a);
+    if (!kernel_smem(kernel, W8_SMEM_LIMIT, once[(p.pair ? 4 : 2) + (f16 ? 1 : 0)])) return AWQ_ERR_CUDA;
+    kernel<<<p.ctas, W8_THREADS, p.smem, cs>>>(tw, tx, a);
     return launch_status();
   };
-  st = p.pair ? (f16 ? launch(w8a8_gemm_pair_tcgen05<true>) : launch(w8a8_gemm_pair_tcgen05<false>))
-              : (f16 ? launch(w8a8_gemm_tcgen05<true>) : launch(w8a8_gemm_tcgen05<false>));
-  if (st != AWQ_OK || p.slots == 1) return st;
-  W8Fixups fx;
-  w8_fixups(p, fx);
-  if (fx.n == 0) return AWQ_OK;
-  const dim3 rgrid((unsigned)fx.n, (unsigned)cdiv((long long)p.bm * p.bn, 1024));
-  if (f16)
-    w8a8_reduce<true><<<rgrid, 256, 0, cs>>>(a, p.bm, fx);
-  else
-    w8a8_reduce<false><<<rgrid, 256, 0, cs>>>(a, p.bm, fx);
-  return launch_status();
+  return p.pair ? (f16 ? launch(w8a8_gemm_pair_tcgen05<true>) : launch(w8a8_gemm_pair_tcgen05<false>))
+                : (f16 ? launch(w8a8_gemm_tcgen05<true>) : launch(w8a8_gemm_tcgen05<false>));
 }
 
 extern "C" size_t awq_kv4_page_bytes(const awq_kv4cfg* cfg) {

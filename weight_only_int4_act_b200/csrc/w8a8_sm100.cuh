@@ -177,27 +177,38 @@ __global__ void __launch_bounds__(1024)
 // a pair), so a few tokens still fill an instruction and a TMEM lane is an
 // output channel: an epilogue warp stores 32 consecutive channels of a token.
 // One K step is 128 channels (128 bytes, one swizzled row; 4 MMAs of K = 32).
-// Roles (192 threads, one CTA per SM): warp 0 TMA, warp 1 TMEM and MMAs, warps
-// 2..5 epilogue out of two accumulators, so that it runs under the next tile.
 //
-// Work: G workers (CTAs, or pairs) first take whole tiles c, c + G, ...; the
-// last one to two waves (all tiles, where there are fewer) are cut into G equal
-// contiguous ranges of (tile, K step) units. A tile that several workers touch
-// leaves int32 partials in slabs which w8a8_reduce adds: the sum is exact, so
-// the split changes no bit.
-constexpr int W8_THREADS = 192;
+// w8a8_gemm_tcgen05 (many tokens): G workers (CTAs, or CTA pairs) take whole
+// tiles c, c + G, ... The accumulators are double, so that an epilogue runs
+// under the next tile. Roles (320 threads, one CTA per SM): warp 0 TMA, warp 1
+// TMEM and MMAs, warps 2..9 epilogue (two on each quarter of the TMEM lanes:
+// with one a 256-token tile's epilogue took 10 us, as long as 28 K steps).
+// Bound by what an SM can fetch from L2: about 80 bytes a ns were measured, so
+// the plan takes the tile shape with the fewest bytes an SM.
+//
+// w8a8_small_tcgen05 (few tokens): the weights' bytes are the bound, and 128 of
+// its channels a CTA are too few CTAs. So a cluster of S CTAs shares a tile,
+// each over its S-th of K, several CTAs to an SM; at the end they add their
+// int32 accumulators through distributed shared memory (exact in any order).
 constexpr int W8_BM = 128;
 constexpr int W8_BK = 128;
 constexpr int W8_A_STAGE = W8_BM * W8_BK;
 constexpr int W8_MAX_STAGES = 12;
 constexpr int W8_NBARS = 2 * W8_MAX_STAGES + 5;
-constexpr int W8_TMEM_COLS = 512;
 constexpr int W8_SMEM_LIMIT = 232448;
-constexpr int W8_SMS = 148;  // workers of the plan: one CTA per SM
+constexpr int W8_SMS = 148;      // CTAs of the plan: one per SM
+constexpr int W8_EPI = 8;        // epilogue warps
+constexpr int W8_THREADS = 64 + 32 * W8_EPI;
+constexpr int W8_SMALL_THREADS = 192;
+constexpr int W8_SMALL_N = 128;  // tokens up to which the small kernel runs
 
 __host__ __device__ constexpr int w8_stage_bytes(int b_rows) { return W8_A_STAGE + b_rows * W8_BK; }
 __host__ __device__ constexpr int w8_smem_bytes(int stages, int b_rows) {
-  return 1024 + stages * w8_stage_bytes(b_rows) + W8_NBARS * 8 + 64 + 4 * 256 * 4;
+  return 1024 + stages * w8_stage_bytes(b_rows) + W8_NBARS * 8 + 64 + W8_EPI * 128 * 4;
+}
+
+__host__ __device__ constexpr int w8_small_smem(int stages, int bn) {
+  return 1024 + stages * w8_stage_bytes(bn) + W8_NBARS * 8 + 64 + W8_SMALL_N * 4;
 }
 
 constexpr int ERR_W8_EMPTY = 0x501, ERR_W8_FULL = 0x502, ERR_W8_TFULL = 0x503, ERR_W8_TEMPTY = 0x504;
@@ -208,12 +219,10 @@ struct W8Args {
   int n_mb, n_nb, n_kb;  // tiles of channels and tokens, K steps
   int group_nb;          // token tiles that neighbouring workers share a weight tile over
   int stages;
-  int whole;             // tiles [0, whole) are taken whole, strided by the workers
-  long long units;       // (tiles - whole) * n_kb, cut into ranges
+  int cols;              // small kernel: TMEM columns
+  int split;             // small kernel: CTAs of a cluster
   const float *dx, *dw, *bias;
   void* Y;
-  int* P;                // [slots][N, d_out] partials
-  long long p_stride;
   int* err;
 };
 
@@ -224,44 +233,6 @@ __host__ __device__ inline void w8_tile(const W8Args& a, long long t, int& mb, i
   nb = first + (int)(in % width);
   mb = (int)(in / width);
 }
-
-struct W8Seg {
-  int mb, nb, kb0, kb1, slot;
-  bool whole;  // no other worker touches the tile
-};
-
-// The segments of worker c of G, in order; every role walks the same sequence.
-struct W8Sched {
-  long long t, u, u1;
-  int c, G;
-  __device__ W8Sched(const W8Args& a, int c_, int G_) : t(c_), c(c_), G(G_) {
-    u = w4_sk_begin(c, G, a.units);
-    u1 = w4_sk_begin(c + 1, G, a.units);
-  }
-  __device__ bool next(const W8Args& a, W8Seg& g) {
-    long long tile;
-    g.kb0 = 0;
-    g.kb1 = a.n_kb;
-    g.slot = 0;
-    g.whole = true;
-    if (t < a.whole) {
-      tile = t;
-      t += G;
-    } else {
-      if (u >= u1) return false;
-      const long long k = u / a.n_kb, t0 = k * a.n_kb;
-      tile = a.whole + k;
-      g.kb0 = (int)(u - t0);
-      g.kb1 = (int)min((long long)a.n_kb, (long long)g.kb0 + (u1 - u));
-      const long long first = w4_sk_cta(t0, G, a.units);
-      g.whole = w4_sk_cta(t0 + a.n_kb - 1, G, a.units) == first;
-      g.slot = (int)(c - first);
-      u += g.kb1 - g.kb0;
-    }
-    w8_tile(a, tile, g.mb, g.nb);
-    return true;
-  }
-};
 
 // Instruction descriptor, kind::i8: signed 8-bit A and B (K-major), int32 D.
 __host__ __device__ constexpr uint32_t idesc_i8_s32(int M, int N) {
@@ -283,27 +254,53 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t
         : "memory");
 }
 
-template <bool F16>
 __device__ __forceinline__ float w8_scale(int acc, float dx, float dw) {
   return __fmul_rn(__fmul_rn(__int2float_rn(acc), dx), dw);
+}
+
+// One channel's sums of tokens 32 c .. of a tile (jn of them, at most 32) to Y: y is the first's place.
+template <bool F16>
+__device__ __forceinline__ void w8_store32(const W8Args& a, const uint32_t (&v)[32], const float* dx, float dw, float bias,
+                                           bool biased, long long e0, int jn) {
+  uint16_t* y = static_cast<uint16_t*>(a.Y) + e0;
+  const long long ld = a.d_out, all = (long long)a.N * a.d_out;
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const float4 d4 = *reinterpret_cast<const float4*>(dx + j);
+    float r[4] = {w8_scale((int)v[j], d4.x, dw), w8_scale((int)v[j + 1], d4.y, dw), w8_scale((int)v[j + 2], d4.z, dw),
+                  w8_scale((int)v[j + 3], d4.w, dw)};
+    if (biased) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = __fadd_rn(r[i], bias);
+    }
+    const uint32_t p0 = pack2<F16>(r[0], r[1]), p1 = pack2<F16>(r[2], r[3]);
+    if (j < jn && AWQ_IDX_OK(e0 + j * ld, all, BS_W8_Y)) y[0] = (uint16_t)p0;
+    if (j + 1 < jn && AWQ_IDX_OK(e0 + (j + 1) * ld, all, BS_W8_Y)) y[ld] = (uint16_t)(p0 >> 16);
+    if (j + 2 < jn && AWQ_IDX_OK(e0 + (j + 2) * ld, all, BS_W8_Y)) y[2 * ld] = (uint16_t)p1;
+    if (j + 3 < jn && AWQ_IDX_OK(e0 + (j + 3) * ld, all, BS_W8_Y)) y[3 * ld] = (uint16_t)(p1 >> 16);
+    y += 4 * ld;
+  }
 }
 
 template <bool PAIR, bool F16>
 __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensorMap& tmX, const W8Args& args) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int bn = args.bn, stages = args.stages;
   const int b_rows = PAIR ? bn / 2 : bn;  // token rows this CTA loads
   const uint32_t b_stage = (uint32_t)b_rows * W8_BK, stage_bytes = W8_A_STAGE + b_stage;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + stages * stage_bytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + W8_NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* sdx = reinterpret_cast<float*>(tmem_slot + 16);  // [4 epilogue warps][256]
+  // [epilogue warps][128] steps of the tokens; 16-byte aligned (29 barriers and 64 bytes behind a 1024-byte boundary)
+  float* sdx = reinterpret_cast<float*>(tmem_slot + 14);
+  static_assert((W8_NBARS * 8 + 14 * 4) % 16 == 0, "sdx is read 16 bytes at a time");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? (cluster_ctarank() & 1u) : 0u;
   const bool lead = rank == 0;
   const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, G = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const long long tiles = (long long)args.n_mb * args.n_nb;
   auto full = [&](int s) { return smem_u32(bars + s); };
   auto empty = [&](int s) { return smem_u32(bars + W8_MAX_STAGES + s); };
   auto tfull = [&](int a) { return smem_u32(bars + 2 * W8_MAX_STAGES + a); };
@@ -317,7 +314,7 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull(a), 1);
-      mbar_init(tempty(a), PAIR ? 8 : 4);
+      mbar_init(tempty(a), PAIR ? 2 * W8_EPI : W8_EPI);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -331,10 +328,10 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
   }
   if (warp == 1) {
     if constexpr (PAIR) {
-      tmem_alloc_pair(smem_u32(tmem_slot), W8_TMEM_COLS);
+      tmem_alloc_pair(smem_u32(tmem_slot), 512);
       tmem_relinquish_pair();
     } else {
-      tmem_alloc(smem_u32(tmem_slot), W8_TMEM_COLS);
+      tmem_alloc(smem_u32(tmem_slot), 512);
       tmem_relinquish();
     }
   }
@@ -343,7 +340,7 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
   if constexpr (PAIR) cluster_sync();  // barriers of both CTAs initialised before any remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int acc_stride = 256;
+  constexpr int acc_stride = 256;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -351,16 +348,16 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
       Ring ring;
       uint32_t issued = 0, last_parity = 0;
       bool ok = true;
-      W8Sched sched(args, worker, G);
-      W8Seg g;
-      while (ok && sched.next(args, g)) {
-        for (int kb = g.kb0; kb < g.kb1; ++kb) {
+      for (long long t = worker; ok && t < tiles; t += G) {
+        int mb, nb;
+        w8_tile(args, t, mb, nb);
+        const int wrow = (mb * (PAIR ? 2 : 1) + (int)rank) * W8_BM, xrow = nb * bn + (int)rank * b_rows;
+        for (int kb = 0; kb < args.n_kb; ++kb) {
           if (!mbar_wait(empty(ring.stage), ring.phase ^ 1u, abort_flag, args.err, ERR_W8_EMPTY)) {
             ok = false;
             break;
           }
           const uint32_t sa = smem_u32(smem + ring.stage * stage_bytes), sb = sa + W8_A_STAGE;
-          const int wrow = (g.mb * (PAIR ? 2 : 1) + (int)rank) * W8_BM, xrow = g.nb * bn + (int)rank * b_rows;
           if constexpr (PAIR) {
             const uint32_t bar = mapa_shared(full(ring.stage), 0);
             if (lead) mbar_arrive_expect_tx(full(ring.stage), 2 * stage_bytes);
@@ -393,14 +390,13 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
       const uint64_t d0 = desc_kmajor_sw128(smem_u32(smem));
       Ring ring;
       bool ok = true;
-      W8Sched sched(args, worker, G);
-      W8Seg g;
-      for (int local = 0; ok && sched.next(args, g); ++local) {
+      int local = 0;
+      for (long long t = worker; ok && t < tiles; t += G, ++local) {
         const int acc = local & 1;
         if (!mbar_wait(tempty(acc), ((local >> 1) & 1) ^ 1u, abort_flag, args.err, ERR_W8_TEMPTY)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * acc_stride;
-        for (int kb = g.kb0; kb < g.kb1; ++kb) {
+        for (int kb = 0; kb < args.n_kb; ++kb) {
           if (!mbar_wait(full(ring.stage), ring.phase, abort_flag, args.err, ERR_W8_FULL)) {
             ok = false;
             break;
@@ -408,7 +404,7 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
           tc_fence_after();
           const uint64_t da = d0 + ((uint64_t)(ring.stage * stage_bytes) >> 4), db = da + (W8_A_STAGE >> 4);
 #pragma unroll
-          for (int k = 0; k < W8_BK / 32; ++k) mma_i8<PAIR>(d_tmem, da + 2 * k, db + 2 * k, idesc, (kb != g.kb0) || k);
+          for (int k = 0; k < W8_BK / 32; ++k) mma_i8<PAIR>(d_tmem, da + 2 * k, db + 2 * k, idesc, kb != 0 || k);
           if constexpr (PAIR)
             mma_commit_pair(empty(ring.stage), 0x3);
           else
@@ -429,48 +425,36 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
       mbar_wait_drain(drain_bar, 0);
     }
   } else {
-    // ---------------- epilogue (warp w reads TMEM lanes 32 (w % 4) ..)
-    using Ty = W4Type<F16>;
-    const int quad = warp & 3;
-    float* dxs = sdx + (warp - 2) * 256;
-    W8Sched sched(args, worker, G);
-    W8Seg g;
-    for (int local = 0; sched.next(args, g); ++local) {
+    // ---------------- epilogue: warp w reads TMEM lanes 32 (w % 4) .., every other 32 tokens
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    float* dxs = sdx + (warp - 2) * 128;
+    int local = 0;
+    for (long long t = worker; t < tiles; t += G, ++local) {
+      int mb, nb;
+      w8_tile(args, t, mb, nb);
       const int acc = local & 1;
-      const int t0 = g.nb * bn, toks = min(bn, args.N - t0);
-      const int o = (g.mb * (PAIR ? 2 : 1) + (int)rank) * W8_BM + quad * 32 + lane;
+      const int t0 = nb * bn, toks = min(bn, args.N - t0);
+      const int o = (mb * (PAIR ? 2 : 1) + (int)rank) * W8_BM + quad * 32 + lane;
       const bool in = o < args.d_out;
-      if (g.whole)
-        for (int j = lane; j < toks; j += 32) dxs[j] = __ldg(args.dx + t0 + j);
-      const float dw = g.whole && in ? __ldg(args.dw + o) : 0.0f;
-      const float bias = g.whole && in && args.bias ? __ldg(args.bias + o) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int tok = 64 * c + 32 * half + lane;
+        if (tok < toks) dxs[32 * c + lane] = __ldg(args.dx + t0 + tok);
+      }
+      const float dw = in ? __ldg(args.dw + o) : 0.0f;
+      const float bias = in && args.bias ? __ldg(args.bias + o) : 0.0f;
       __syncwarp();
       const bool ready = mbar_wait_sleep(tfull(acc), (local >> 1) & 1u, abort_flag, args.err, ERR_W8_TFULL, 64);
       if (!__all_sync(0xffffffffu, ready)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * acc_stride;
-      for (int c = 0; c * 32 < toks; ++c) {
+      for (int c = half; c * 32 < toks; c += 2) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(taddr + c * 32, v);
         tmem_ld_wait();
-        const int jn = min(32, toks - c * 32);
-        const long long e0 = (long long)(t0 + c * 32) * args.d_out + o;
-        if (in && g.whole) {
-          typename Ty::T* y = static_cast<typename Ty::T*>(args.Y) + e0;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float r = w8_scale<F16>((int)v[j], dxs[c * 32 + j], dw);
-            if (args.bias) r = __fadd_rn(r, bias);
-            if (j < jn && AWQ_IDX_OK(e0 + (long long)j * args.d_out, (long long)args.N * args.d_out, BS_W8_Y))
-              y[(long long)j * args.d_out] = Ty::from_float(r);
-          }
-        } else if (in) {
-          int* P = args.P + (long long)g.slot * args.p_stride + e0;
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < jn && AWQ_IDX_OK(e0 + (long long)j * args.d_out, (long long)args.N * args.d_out, BS_W8_P))
-              P[(long long)j * args.d_out] = (int)v[j];
-        }
+        if (in)
+          w8_store32<F16>(args, v, dxs + 32 * (c >> 1), dw, bias, args.bias != nullptr,
+                          (long long)(t0 + c * 32) * args.d_out + o, min(32, toks - c * 32));
         __syncwarp();
       }
       tc_fence_before();
@@ -490,9 +474,9 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR)
-      tmem_dealloc_pair(tmem_base, W8_TMEM_COLS);
+      tmem_dealloc_pair(tmem_base, 512);
     else
-      tmem_dealloc(tmem_base, W8_TMEM_COLS);
+      tmem_dealloc(tmem_base, 512);
   }
 }
 
@@ -509,50 +493,144 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W8_THREADS, 1)
   w8a8_body<true, F16>(tmW, tmX, args);
 }
 
-// Tiles that two or more workers touch, found on the host from the shapes.
-struct W8Fixups {
-  int n;
-  int tile[W8_SMS];
-  short ns[W8_SMS];
-};
+__device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
 
-// Block (b, y) adds the partials of split tile fx.tile[b] for 1024 of its
-// elements (channel fastest) and writes them scaled and rounded.
+// One tile of 128 channels x bn tokens (bn <= 128, all of them) and one S-th of
+// K per CTA; blockIdx.x = tile * S + rank in the cluster.
 template <bool F16>
-__global__ void __launch_bounds__(256) w8a8_reduce(const W8Args a, int bm, const __grid_constant__ W8Fixups fx) {
-  using Ty = W4Type<F16>;
-  if (!AWQ_IDX_OK(blockIdx.x, fx.n, BS_W8_P)) return;
-  int mb, nb;
-  w8_tile(a, fx.tile[blockIdx.x], mb, nb);
-  const int ns = fx.ns[blockIdx.x];
-  const int o0 = mb * bm, t0 = nb * a.bn;
-  const int rows = min(bm, a.d_out - o0), toks = min(a.bn, a.N - t0);
-  long long idx[4];
-  bool in[4];
-  int acc[4], oo[4], tt[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int e = blockIdx.y * 1024 + k * 256 + threadIdx.x;
-    const int j = e / rows, r = e - j * rows;
-    tt[k] = t0 + j;
-    oo[k] = o0 + r;
-    idx[k] = (long long)tt[k] * a.d_out + oo[k];
-    in[k] = e < rows * toks && AWQ_IDX_OK(idx[k], (long long)a.N * a.d_out, BS_W8_P);
-    acc[k] = 0;
-  }
-  for (int s = 0; s < ns; ++s) {
-    const int* P = a.P + (long long)s * a.p_stride;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (in[k]) acc[k] += P[idx[k]];
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (in[k]) {
-      float y = w8_scale<F16>(acc[k], __ldg(a.dx + tt[k]), __ldg(a.dw + oo[k]));
-      if (a.bias) y = __fadd_rn(y, __ldg(a.bias + oo[k]));
-      static_cast<typename Ty::T*>(a.Y)[idx[k]] = Ty::from_float(y);
+__global__ void __launch_bounds__(W8_SMALL_THREADS)
+    w8a8_small_tcgen05(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                       const __grid_constant__ W8Args args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int bn = args.bn, stages = args.stages, S = args.split;
+  const uint32_t stage_bytes = w8_stage_bytes(bn);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + stages * stage_bytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + W8_NBARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sdx = reinterpret_cast<float*>(tmem_slot + 14);  // [128] steps of the tokens
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mb = blockIdx.x / S, rank = blockIdx.x - mb * S;
+  const int kb0 = (int)((long long)args.n_kb * rank / S), kb1 = (int)((long long)args.n_kb * (rank + 1) / S);
+  auto full = [&](int s) { return smem_u32(bars + s); };
+  auto empty = [&](int s) { return smem_u32(bars + W8_MAX_STAGES + s); };
+  const uint32_t tfull = smem_u32(bars + 2 * W8_MAX_STAGES);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
     }
+    mbar_init(tfull, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    if (blockIdx.x == 0) *args.err = 0;
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), args.cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring ring;
+      uint32_t issued = 0, last_parity = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(empty(ring.stage), ring.phase ^ 1u, abort_flag, args.err, ERR_W8_EMPTY)) break;
+        const uint32_t sa = smem_u32(smem + ring.stage * stage_bytes);
+        mbar_arrive_expect_tx(full(ring.stage), stage_bytes);
+        tma_load_2d(sa, &tmW, full(ring.stage), kb * W8_BK, mb * W8_BM);
+        tma_load_2d(sa + W8_A_STAGE, &tmX, full(ring.stage), kb * W8_BK, 0);
+        issued |= 1u << ring.stage;
+        last_parity = (last_parity & ~(1u << ring.stage)) | (ring.phase << ring.stage);
+        ring.next(stages);
+      }
+      for (int s = 0; s < stages; ++s)
+        if (issued & (1u << s)) mbar_wait_drain(full(s), (last_parity >> s) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_i8_s32(W8_BM, bn);
+      const uint64_t d0 = desc_kmajor_sw128(smem_u32(smem));
+      Ring ring;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(full(ring.stage), ring.phase, abort_flag, args.err, ERR_W8_FULL)) break;
+        tc_fence_after();
+        const uint64_t da = d0 + ((uint64_t)(ring.stage * stage_bytes) >> 4), db = da + (W8_A_STAGE >> 4);
+#pragma unroll
+        for (int k = 0; k < W8_BK / 32; ++k) mma_i8<false>(tmem_base, da + 2 * k, db + 2 * k, idesc, kb != kb0 || k);
+        mma_commit(empty(ring.stage));
+        ring.next(stages);
+      }
+      // (on a wait that gave up too: what was issued ends before the block does)
+      mma_commit(tfull);
+      mbar_wait_drain(tfull, 0);
+    }
+  }
+  __syncwarp();
+  // ---------------- epilogue (warps 2..5; warp w reads TMEM lanes 32 (w % 4) ..)
+  const int quad = warp & 3, o = mb * W8_BM + quad * 32 + lane;
+  const bool in = o < args.d_out, biased = args.bias != nullptr;
+  int* part = reinterpret_cast<int*>(smem);  // [bn][128] int32, over the ring
+  bool ready = true;
+  if (warp >= 2) {
+    const int tok = threadIdx.x - 64;
+    if (tok < args.N) sdx[tok] = __ldg(args.dx + tok);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    const float dw = in ? __ldg(args.dw + o) : 0.0f, bias = in && biased ? __ldg(args.bias + o) : 0.0f;
+    ready = __all_sync(0xffffffffu, mbar_wait_sleep(tfull, 0, abort_flag, args.err, ERR_W8_TFULL, 32)) && !*abort_flag;
+    tc_fence_after();
+    for (int c = 0; c * 32 < args.N && ready; ++c) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quad * 32) << 16) + c * 32, v);
+      tmem_ld_wait();
+      const int jn = min(32, args.N - c * 32);
+      if (S == 1) {
+        if (in) w8_store32<F16>(args, v, sdx + 32 * c, dw, bias, biased, (long long)(c * 32) * args.d_out + o, jn);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < jn) part[(c * 32 + j) * 128 + quad * 32 + lane] = (int)v[j];
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+  }
+  if (S > 1) {
+    cluster_sync();  // every CTA's accumulators are in its shared memory
+    if (warp >= 2 && ready) {
+      const float dw = in ? __ldg(args.dw + o) : 0.0f, bias = in && biased ? __ldg(args.bias + o) : 0.0f;
+      const uint32_t mine = smem_u32(part + quad * 32 + lane);
+      for (int j = rank; j < args.N; j += S) {  // tokens go round the cluster
+        int sum = 0;
+        for (int r = 0; r < S; ++r) sum += ld_cluster_s32(mapa_shared(mine + j * 512, (uint32_t)r));
+        float y = w8_scale(sum, sdx[j], dw);
+        if (biased) y = __fadd_rn(y, bias);
+        const long long e = (long long)j * args.d_out + o;
+        if (in && AWQ_IDX_OK(e, (long long)args.N * args.d_out, BS_W8_Y))
+          static_cast<typename W4Type<F16>::T*>(args.Y)[e] = W4Type<F16>::from_float(y);
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, args.cols);
+  }
 }
 
 }  // namespace awq
