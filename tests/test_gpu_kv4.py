@@ -224,6 +224,77 @@ def test_attention_prompt_chunk(dtype):
     _run([700, 260], [300, 260], 2, 4, 128, 128, 64, dtype, 77)
 
 
+# the batches below give enough blocks of 256 query rows for the tensor-memory kernel (one group a head, head_dim <= 128)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 256])
+def test_prompt_pages_and_mixed_rows(dim, page, dtype):
+    """Chunks behind older contexts, a whole prompt, single tokens and a sequence without rows in one batch."""
+    _run([700, 260, 90, 333, 64, 129, 40], [300, 260, 1, 70, 0, 129, 3], 8, 2, dim, dim, page, dtype, 7 * page + dim)
+
+
+@pytest.mark.parametrize("share,heads,new", [(1, 16, 700), (3, 7, 201), (8, 5, 260), (16, 40, 5), (71, 10, 15)])
+def test_prompt_shared_heads(share, heads, new):
+    """Row tiles that cut a token's heads anywhere; few and many rows a token."""
+    _run([new + 77, new], [new, new], heads, share, 64, 64, 64, "bf16", share)
+
+
+def test_prompt_more_rows_than_context():
+    """Rows that see nothing: zeros and -inf."""
+    _run([100, 40, 0], [300, 129, 70], 16, 2, 128, 128, 16, "f16", 3)
+
+
+def test_prompt_large_values_and_steps():
+    loud = torch.ones(128, device="cuda")
+    loud[3], loud[77] = 40.0, 25.0
+    _run([500, 390], [300, 290], 10, 4, 128, 128, 32, "bf16", 5, kscale=2.0, vscale=100.0, scale_k=loud)
+    _run([500, 390], [300, 290], 10, 4, 128, 128, 32, "f16", 6, kscale=0.01, vscale=1e-3)
+
+
+def test_prompt_long_context():
+    _run([6000, 5001], [260, 130], 10, 2, 128, 128, 64, "bf16", 8, lse=False)
+
+
+def test_prompt_masked_tokens_may_hold_anything():
+    """NaN in a token does not reach the rows before it, does reach all from it on."""
+    heads, n = 20, 300
+    cfg, cache, table, lens, slots = _fill([400, 350], heads, 128, 128, 32, "bf16", 60)
+    q = _rand((2 * n, 2 * heads, 128), "bf16", 61)
+    start = torch.tensor([0, n, 2 * n], dtype=torch.int32).cuda()
+    good = awq.kv4_attention(q, cache, table, lens, cfg, q_start=start, max_q=n)
+    bad = torch.full((1, heads, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    awq.kv4_append(bad, bad, torch.tensor([slots[290]], dtype=torch.int32).cuda(), cache, cfg)
+    out = awq.kv4_attention(q, cache, table, lens, cfg, q_start=start, max_q=n)
+    first = 290 - (400 - n)  # the first row that sees token 290
+    assert torch.equal(out[:first], good[:first]) and torch.equal(out[n:], good[n:])
+    assert torch.isnan(out[first:n]).all()
+    work = awq.workspace(awq.kv4_attention_workspace_size(2, 2 * heads, n, cfg))
+    table[1, 3] = cache.shape[0]  # a page outside the cache: left out of the second sequence, and reported
+    out, lse = awq.kv4_attention(q, cache, table, lens, cfg, q_start=start, max_q=n, ws=work, lse=True)
+    with pytest.raises(awq.AwqError, match="DEVICE"):
+        awq.workspace_error(work)
+    assert torch.equal(out[:first], good[:first])
+    assert torch.equal(out[n:n + 96 - 50], good[n:n + 96 - 50])  # rows that see only the first three pages
+    keep = np.concatenate([slots[400:400 + 96], slots[400 + 128:]])
+    (kc, ks, kz), (vc, vs, vz) = _read(cache, cfg, keep)
+    k, v = S.four_bit_values(kc, ks, kz), S.four_bit_values(vc, vs, vz)
+    ref, ref_lse, _ = S.attention(_f64(q[2 * n - 1:]), k, v, 2, 128 ** -0.5, 318)
+    assert np.abs(_f64(out[2 * n - 1:]) - ref).max() <= 2.0 ** -7 * np.abs(v).max()
+    assert np.abs(_f64(lse[2 * n - 1:]) - ref_lse).max() <= 2.0 ** -10
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_scale_zero_and_negative(n):
+    """scale 0: the mean of the visible values; scale below 0: the softmax turned round."""
+    cfg, cache, table, lens, slots = _fill([200, 170], 20, 64, 64, 16, "f16", 33)
+    q = _rand((2 * n, 40, 64), "f16", 34, 2.0)
+    start = torch.tensor([0, n, 2 * n], dtype=torch.int32).cuda()
+    parts = _read(cache, cfg, slots)
+    for scale in (0.0, -0.2):
+        out, lse = awq.kv4_attention(q, cache, table, lens, cfg, q_start=start, max_q=n, scale=scale, lse=True)
+        _check(out, lse, q if scale >= 0 else -q, cfg, parts, [200, 170], [0, n, 2 * n], 2, abs(scale), "f16")
+
+
 def test_attention_large_values_and_steps():
     """Peaked softmax, values of very different sizes, loud key channels, large queries."""
     loud = torch.ones(128, device="cuda")

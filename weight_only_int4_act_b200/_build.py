@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(LIB_DIR, VARIANTS["release"][0])
 SOURCES = [os.path.join(PKG, "csrc", "awq_lib.cu")]
 DEPS = SOURCES + [os.path.join(PKG, "csrc", f) for f in (
     "ptx.cuh", "fq.cuh", "check.cuh", "gemm_sm100.cuh", "gemm_pair_sm100.cuh", "awq_kernels.cuh",
-    "w4a16_sm100.cuh", "awq_api.cu", "serve_api.cuh", "w8a8_sm100.cuh", "kv4_sm100.cuh")] + [os.path.join(ROOT, "include", "awq.h")]
+    "w4a16_sm100.cuh", "awq_api.cu", "serve_api.cuh", "w8a8_sm100.cuh", "kv4_sm100.cuh",
+    "kv4_prompt_sm100.cuh")] + [os.path.join(ROOT, "include", "awq.h")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",

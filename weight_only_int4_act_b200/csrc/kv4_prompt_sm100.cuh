@@ -1,0 +1,564 @@
+// Attention of many query rows a sequence (prompts and their chunks) over the
+// 4-bit cache, on tcgen05. A block takes 256 rows (token x head of the group)
+// of one kv head in two tiles of 128, and walks the context in tiles of 64
+// tokens:
+//   S_q = Q_q C_k^T       M = 128 rows, N = 64 tokens, K = D; codes less zeros
+//   O_q += W_q C_v        M = 128 rows, N = D channels, K = 64 tokens
+// with fp16 operands and fp32 accumulators in tensor memory (S_q twice, so that
+// the next tile's scores are there when a softmax ends; W_q takes the place of
+// its S_q). With one group a head the codes less zeros (-15 .. 15) are exact in
+// fp16 and the steps enter in fp32: the score's as s = dk_t (q . c_t), the
+// value's in the weight w_t = p_t dv_t, which is rounded to fp16 (2^-11) once,
+// as in the split kernel. With several groups a head each code is also
+// multiplied by its group's step over the power of two of the token's largest
+// (one more rounding, 2^-11, of keys and values).
+//
+// Warps (14): 0 loads packed strips (cp.async.bulk), 1 issues the MMAs, 2..5
+// unpack them into the operand tiles, 6..9 and 10..13 are the softmax of the
+// two row tiles, a thread a row. The running maximum may lag by 2^8 before the
+// output is rescaled, which is rare after the first tiles.
+#pragma once
+#include <type_traits>
+
+#include "kv4_sm100.cuh"
+
+namespace awq {
+
+constexpr int KVP_ROWS = 256, KVP_TOK = 64, KVP_THREADS = 448, KVP_STAGES = 3, KVP_RAW = 2;
+constexpr int KVP_MIN_ROWS = 64;  // sequences of at most so many rows are the split kernel's
+constexpr int ERR_KVP_RAW = 0x601, ERR_KVP_FREE = 0x602, ERR_KVP_SCORE = 0x603, ERR_KVP_WEIGHT = 0x604, ERR_KVP_OUT = 0x605,
+              ERR_KVP_TILE = 0x606;
+
+struct KvpArgs {
+  Kv4AttnArgs a;
+  int tiles;  // row tiles of the longest sequence: gridDim.x
+};
+
+template <int D, int G>
+struct KvpSmem {
+  static constexpr int SUB = (D + 63) / 64;                 // 64-channel sub-tiles of 128-byte rows
+  static constexpr int STRIP = kv4_strip_bytes(D, G);
+  alignas(1024) uint8_t q[2][SUB][128 * 128];
+  alignas(1024) uint8_t k[KVP_STAGES][SUB][KVP_TOK * 128];
+  alignas(1024) uint8_t v[KVP_STAGES][D * 128];
+  alignas(128) uint8_t raw[KVP_RAW][4 * STRIP];
+  float2 step[KVP_STAGES][KVP_TOK];  // (key, value) step of a token
+  int exponent[KVP_STAGES][4];       // largest value step's, by strip
+  int lost_raw[KVP_RAW], lost[KVP_STAGES];  // strips (by bit) in pages outside the cache
+  uint64_t raw_full[KVP_RAW], raw_empty[KVP_RAW], tile_full[KVP_STAGES], tile_empty[KVP_STAGES];
+  uint64_t q_full, score[2][2], weight[2][2], out_done[2][2], drain;  // [row tile][context tile & 1]
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// Codes less zero of the four pairs of a word, exact in fp16: low nibbles as
+// (1024 + c) - (1024 + z), high ones as (1024 + 16 c) / 16 - (64 + z).
+// lo: bytes 0 and 2, bytes 1 and 3; hi: the same of the high nibbles.
+struct KvpPairs {
+  __half2 lo0, lo1, hi0, hi1;
+};
+__device__ __forceinline__ KvpPairs kvp_unpack(uint32_t w, __half2 z0, __half2 z1) {
+  // z0: the zeros of lo0 and hi0, z1: of lo1 and hi1
+  const uint32_t x = w >> 8;
+  const __half2 k1024 = __float2half2_rn(1024.0f), k64 = __float2half2_rn(64.0f), k16 = __float2half2_rn(0.0625f);
+  auto h2 = [](uint32_t u) { return *reinterpret_cast<const __half2*>(&u); };
+  KvpPairs p;
+  p.lo0 = __hsub2(h2((w & 0x000F000Fu) | 0x64006400u), __hadd2(k1024, z0));
+  p.lo1 = __hsub2(h2((x & 0x000F000Fu) | 0x64006400u), __hadd2(k1024, z1));
+  p.hi0 = __hfma2(h2((w & 0x00F000F0u) | 0x64006400u), k16, __hneg2(__hadd2(k64, z0)));
+  p.hi1 = __hfma2(h2((x & 0x00F000F0u) | 0x64006400u), k16, __hneg2(__hadd2(k64, z1)));
+  return p;
+}
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// The head-wide power of two of a token's steps and a group's step over it.
+__device__ __forceinline__ float kvp_pow2(float x) { return __uint_as_float(__float_as_uint(x) & 0x7F800000u); }
+
+template <int D, int G>
+__global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __grid_constant__ KvpArgs args) {
+  using Sm = KvpSmem<D, G>;
+  constexpr int SUB = Sm::SUB, NJ = D / 32, NG = D / G, STRIP = kv4_strip_bytes(D, G);
+  constexpr bool FOLD = NG > 1;
+  extern __shared__ uint8_t smem_raw[];
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const Kv4AttnArgs& a = args.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.y, b = blockIdx.z;
+  const Kv4Seq seq = kv4_seq(a, b);
+  const int rows = seq.n * a.share;
+  if (threadIdx.x == 0 && seq.bad) atomicMax(a.err, ERR_KV4_PAGE);
+  // the longest tiles first
+  const int n_tiles = (rows + KVP_ROWS - 1) / KVP_ROWS, tile = n_tiles - 1 - (int)blockIdx.x;
+  if (rows <= KVP_MIN_ROWS || tile < 0) return;
+  const int r0 = tile * KVP_ROWS;
+  // context tiles of the two row tiles (their last rows see the most)
+  int n_ctx[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int last = min(r0 + 128 * (q + 1), rows) - 1;
+    const int see = last >= r0 + 128 * q ? seq.L - seq.n + (int)((unsigned)last / (unsigned)a.share) + 1 : 0;
+    n_ctx[q] = see > 0 ? (see + KVP_TOK - 1) / KVP_TOK : 0;
+  }
+  const int n = max(n_ctx[0], n_ctx[1]);  // (the second's, unless it is empty)
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < KVP_RAW; ++s) {
+      mbar_init(smem_u32(&sm.raw_full[s]), 1);
+      mbar_init(smem_u32(&sm.raw_empty[s]), 4);
+    }
+    for (int s = 0; s < KVP_STAGES; ++s) {
+      mbar_init(smem_u32(&sm.tile_full[s]), 4);
+      mbar_init(smem_u32(&sm.tile_empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sm.q_full), 8);
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(smem_u32(&sm.score[q][0]), 1);
+      mbar_init(smem_u32(&sm.score[q][1]), 1);
+      mbar_init(smem_u32(&sm.weight[q][0]), 4);
+      mbar_init(smem_u32(&sm.weight[q][1]), 4);
+      mbar_init(smem_u32(&sm.out_done[q][0]), 1);
+      mbar_init(smem_u32(&sm.out_done[q][1]), 1);
+    }
+    mbar_init(smem_u32(&sm.drain), 1);
+    sm.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sm.tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  volatile int* abort_flag = &sm.abort;
+  auto score_col = [&](int q, int buf) { return tmem + (uint32_t)(128 * q + 64 * buf); };
+  auto out_col = [&](int q) { return tmem + (uint32_t)(256 + 128 * q); };
+
+  if (warp == 0) {
+    // ---------------- packed strips
+    Ring ring;
+    bool ok = true;
+    for (int j = 0; j < n && ok; ++j) {
+      ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sm.raw_empty[ring.stage]), ring.phase ^ 1u, abort_flag, a.err,
+                                                   ERR_KVP_RAW, 32));
+      if (!ok) break;
+      const uint32_t bar = smem_u32(&sm.raw_full[ring.stage]);
+      // lane i < 4: strip i of the tile (pages of 16 .. 64 tokens and more hold 1, 2 or 4 of them in a row)
+      const int per = min(4, 1 << (a.c.page_shift - 4)), t0 = KVP_TOK * j + 16 * lane, p = t0 >> a.c.page_shift;
+      const bool in = lane < 4 && t0 < seq.L;
+      const int page = in && p < a.table_pages ? __ldg(a.table + (long long)b * a.table_pages + p) : -1;
+      bool good = in && page >= 0 && page < a.c.n_pages;
+      if (in && !good) atomicMax(a.err, ERR_KV4_PAGE);
+      if (good && lane % per == 0) {
+        // (a run's later strips lie in the same page: inside the cache too)
+        const long long off = a.c.strip(page, head, t0 & ((1 << a.c.page_shift) - 1));
+        good = AWQ_SPAN_OK(off, (long long)per * STRIP, a.c.bytes(), BS_KV4_STRIP);
+        if (good) {
+          mbar_expect_tx(bar, per * STRIP);
+          bulk_load(smem_u32(sm.raw[ring.stage]) + lane * STRIP, a.c.base + off, per * STRIP, bar);
+        }
+      }
+      const unsigned lost = __ballot_sync(0xffffffffu, in && !good);
+      __syncwarp();
+      if (lane == 0) {
+        sm.lost_raw[ring.stage] = (int)lost;
+        mbar_arrive(bar);
+      }
+      ring.next(KVP_RAW);
+    }
+    if (!ok) {  // copies in flight end before the block does
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 200000ull) {
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && n > 0) {
+      // ---------------- MMAs
+      constexpr uint32_t F16_F32 = 1u << 4, M128 = (128u >> 4) << 24;
+      constexpr uint32_t S_DESC = F16_F32 | ((KVP_TOK >> 3) << 17) | M128, O_DESC = F16_F32 | ((D >> 3) << 17) | M128;
+      auto scores = [&](int q, int j, int st) {
+        const uint64_t dq = desc_kmajor_sw128(smem_u32(sm.q[q][0])), dk = desc_kmajor_sw128(smem_u32(sm.k[st][0]));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_bf16(score_col(q, j & 1), dq + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4),
+                   dk + (((k >> 2) * KVP_TOK * 128 + (k & 3) * 32) >> 4), S_DESC, k != 0);
+        mma_commit(smem_u32(&sm.score[q][j & 1]));
+      };
+      Ring now, next;  // the stages of tiles j and j + 1
+      bool ok = mbar_wait(smem_u32(&sm.q_full), 0, abort_flag, a.err, ERR_KVP_TILE) &&
+                mbar_wait(smem_u32(&sm.tile_full[0]), 0, abort_flag, a.err, ERR_KVP_TILE);
+      if (ok) {
+        tc_fence_after();
+        for (int q = 0; q < 2; ++q)
+          if (n_ctx[q] > 0) scores(q, 0, 0);
+      }
+      next.next(KVP_STAGES);
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n) {
+          ok = mbar_wait(smem_u32(&sm.tile_full[next.stage]), next.phase, abort_flag, a.err, ERR_KVP_TILE);
+          if (!ok) break;
+          tc_fence_after();
+          for (int q = 0; q < 2 && ok; ++q)
+            if (j + 1 < n_ctx[q]) {
+              // the buffer of scores j + 1 held the weights of j - 1: their product is done
+              if (j > 0) ok = mbar_wait(smem_u32(&sm.out_done[q][(j - 1) & 1]), ((j - 1) >> 1) & 1, abort_flag, a.err, ERR_KVP_OUT);
+              if (ok) scores(q, j + 1, next.stage);
+            }
+        }
+        for (int q = 0; q < 2 && ok; ++q)
+          if (j < n_ctx[q]) {
+            ok = mbar_wait(smem_u32(&sm.weight[q][j & 1]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_WEIGHT);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dv = desc_kmajor_sw128(smem_u32(sm.v[now.stage]));
+#pragma unroll
+            for (int k = 0; k < KVP_TOK / 16; ++k)
+              mma_f16_tmem_a(out_col(q), score_col(q, j & 1) + 8 * k, dv + ((k * 32) >> 4), O_DESC, j > 0 || k > 0);
+            mma_commit(smem_u32(&sm.out_done[q][j & 1]));
+          }
+        if (ok) mma_commit(smem_u32(&sm.tile_empty[now.stage]));
+        now.next(KVP_STAGES);
+        next.next(KVP_STAGES);
+      }
+      // what was issued ends before the block does
+      mma_commit(smem_u32(&sm.drain));
+      mbar_wait_drain(smem_u32(&sm.drain), 0);
+      if (!ok) *abort_flag = 1;
+    }
+  } else if (warp < 6) {
+    // ---------------- unpack: warp u takes strip u's values and steps, and keys of 16 tokens
+    const int u = warp - 2, r = lane >> 2, q4 = lane & 3;
+    Ring ring, raw;
+    for (int j = 0; j < n; ++j) {
+      bool ok = mbar_wait_sleep(smem_u32(&sm.raw_full[raw.stage]), raw.phase, abort_flag, a.err, ERR_KVP_RAW, 32) &&
+                mbar_wait_sleep(smem_u32(&sm.tile_empty[ring.stage]), ring.phase ^ 1u, abort_flag, a.err, ERR_KVP_FREE, 32);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint8_t* s = sm.raw[raw.stage] + u * STRIP;
+      const bool lost = sm.lost_raw[raw.stage] >> u & 1;
+      const int t0 = KVP_TOK * j + 16 * u;
+      const uint32_t* kpar = reinterpret_cast<const uint32_t*>(s + 16 * D);
+      const uint32_t* vpar = kpar + 16 * NG;
+      // a token whose bytes may hold anything counts as zero 0, step 0
+      auto param = [&](const uint32_t* par, int gi, int t) -> float2 {
+        return !lost && t0 + t < seq.L ? widen2<true>(par[16 * gi + t]) : make_float2(0.0f, 0.0f);
+      };
+      // one factor a token: its step, or with several groups the power of two of its largest one
+      auto factor = [&](const uint32_t* par, int t) {
+        float f = param(par, 0, t).x;
+        bool nan = f != f;
+#pragma unroll
+        for (int gi = 1; gi < NG; ++gi) {
+          const float x = param(par, gi, t).x;
+          nan |= x != x;
+          f = fmaxf(f, x);
+        }
+        return nan ? __int_as_float(0x7fffffff) : FOLD ? kvp_pow2(f) : f;
+      };
+      // a group's step over the factor, in fp16 (exact), and the zero
+      auto ratio = [&](const uint32_t* par, int gi, int t, float f) {
+        const float2 p = param(par, gi, t);
+        return make_float2(f > 0.0f ? __fdividef(p.x, f) : 0.0f, p.y);  // (f: a power of two; NaN gives 0)
+      };
+      if (lane < 16) {
+        const float fk = factor(kpar, lane), fv = factor(vpar, lane);
+        sm.step[ring.stage][16 * u + lane] = make_float2(fk, fv);
+        const int e = fv > 0.0f ? (int)(__float_as_uint(fv) >> 23) - 127 : -200;
+        const int top = __reduce_max_sync(0x0000ffffu, e);
+        if (lane == 0) sm.exponent[ring.stage][u] = top;
+      }
+      if (u == 0 && lane == 0) sm.lost[ring.stage] = sm.lost_raw[raw.stage];
+      // keys: a lane takes the words of (token, q): chunk 4 j + q of the token's row holds channels 8 (4 j + q) + {0 4 2 6 1 5 3 7}
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int t = 8 * half + r, row = 16 * u + t;
+        uint32_t w[NJ];
+        load_words<NJ>(s + t * (D / 2) + 4 * q4 * NJ, w);
+        const float f = FOLD ? factor(kpar, t) : 1.0f;
+#pragma unroll
+        for (int jj = 0; jj < NJ; ++jj) {
+          const float2 p = FOLD ? ratio(kpar, jj * 32 / G, t, f) : param(kpar, 0, t);
+          const __half2 z = __float2half2_rn(p.y);
+          KvpPairs c = kvp_unpack(w[jj], z, z);
+          if (FOLD) {
+            const __half2 m = __float2half2_rn(p.x);
+            c.lo0 = __hmul2(c.lo0, m);
+            c.lo1 = __hmul2(c.lo1, m);
+            c.hi0 = __hmul2(c.hi0, m);
+            c.hi1 = __hmul2(c.hi1, m);
+          }
+          const int chunk = 4 * jj + q4;
+          *reinterpret_cast<uint4*>(sm.k[ring.stage][chunk >> 3] + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
+              make_uint4(bits(c.lo0), bits(c.lo1), bits(c.hi0), bits(c.hi1));
+        }
+      }
+      // values: rows are channels, 64 tokens of 2 bytes; a lane writes pairs of tokens
+      {
+        const int ta = 2 * q4, tb = ta + 8;
+        float f[4];
+        if (FOLD) {
+          f[0] = factor(vpar, ta), f[1] = factor(vpar, ta + 1), f[2] = factor(vpar, tb), f[3] = factor(vpar, tb + 1);
+        }
+        const uint2* vw = reinterpret_cast<const uint2*>(s + 8 * D) + lane;
+#pragma unroll
+        for (int p = 0; p < NJ; ++p) {
+          const int gi = p * 32 / G;
+          float2 x[4];
+          const int tk[4] = {ta, ta + 1, tb, tb + 1};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = FOLD ? ratio(vpar, gi, tk[i], f[i]) : param(vpar, 0, tk[i]);
+          const __half2 z0 = __floats2half2_rn(x[0].y, x[1].y), z1 = __floats2half2_rn(x[2].y, x[3].y);
+          const __half2 m0 = __floats2half2_rn(x[0].x, x[1].x), m1 = __floats2half2_rn(x[2].x, x[3].x);
+          const uint2 w2 = vw[32 * p];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            KvpPairs c = kvp_unpack(h ? w2.y : w2.x, z0, z1);
+            if (FOLD) {
+              c.lo0 = __hmul2(c.lo0, m0);
+              c.hi0 = __hmul2(c.hi0, m0);
+              c.lo1 = __hmul2(c.lo1, m1);
+              c.hi1 = __hmul2(c.hi1, m1);
+            }
+            const int ch = 32 * p + 8 * h + r;  // (its low three bits are r's)
+            uint8_t* row = sm.v[ring.stage] + ch * 128 + 4 * q4;
+            const int c0 = ((2 * u) ^ r) << 4, c1 = ((2 * u + 1) ^ r) << 4;
+            *reinterpret_cast<uint32_t*>(row + c0) = bits(c.lo0);
+            *reinterpret_cast<uint32_t*>(row + c1) = bits(c.lo1);
+            *reinterpret_cast<uint32_t*>(row + 16 * 128 + c0) = bits(c.hi0);
+            *reinterpret_cast<uint32_t*>(row + 16 * 128 + c1) = bits(c.hi1);
+          }
+        }
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&sm.tile_full[ring.stage]));
+        mbar_arrive(smem_u32(&sm.raw_empty[raw.stage]));
+      }
+      ring.next(KVP_STAGES);
+      raw.next(KVP_RAW);
+    }
+  } else {
+    // ---------------- softmax: a thread a row
+    const int q = (warp - 6) >> 2, quad = warp & 3, row = quad * 32 + lane, r = r0 + 128 * q + row;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const bool in = r < rows;
+    const int tok = in ? (int)((unsigned)r / (unsigned)a.share) : 0, e = in ? r - tok * a.share : 0;
+    const int vis = in ? seq.L - seq.n + tok + 1 : 0;
+    float top = 0.0f;
+    {
+      const long long off = (seq.row0 + tok) * a.q_tok + (long long)(head * a.share + e) * a.q_head;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + off);
+      const bool ok = in && AWQ_IDX_OK(seq.row0 + tok, a.T, BS_KV4_Q);
+      // the row twice (the second time out of the caches): its largest entry, then scaled so that it lies in [1, 2)
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = a.f16 ? widen2<true>(ww[i]) : widen2<false>(ww[i]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      // (a row of NaN or infinity: its operands become NaN or infinity too)
+      const int ex = top > 0.0f ? min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -110), 127) : 0;
+      // (a negative scale turns the query round, so that the largest score is the largest product's)
+      const float down = copysignf(__uint_as_float((uint32_t)(137 - ex) << 23), a.scale_log2);
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        float2 f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = a.f16 ? widen2<true>(ww[i]) : widen2<false>(ww[i]);
+        // channels {0 4 2 6 1 5 3 7} of the eight, as the keys' codes come out of their words
+        const uint4 o = make_uint4(pack2<true>(f[0].x * down, f[2].x * down), pack2<true>(f[1].x * down, f[3].x * down),
+                                   pack2<true>(f[0].y * down, f[2].y * down), pack2<true>(f[1].y * down, f[3].y * down));
+        *reinterpret_cast<uint4*>(sm.q[q][c >> 3] + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = o;
+      }
+      // 2^(ex - 10) |scale|: score (log2) per unit of q . c; never 0, which would make hidden scores NaN
+      top = fmaxf(__uint_as_float((uint32_t)(117 + ex) << 23) * fabsf(a.scale_log2), 1e-37f);
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+    const float unit = top;
+    float m = KV4_LOWEST, l = 0.0f;
+    bool ok = true;
+    const int n_mine = n_ctx[q];
+    // Wait for the weights' product of tile j. (Scores j or j + 1 being there
+    // means that the one of the same barrier before, j - 2, is done.)
+    auto product_done = [&](int j) {
+      return mbar_wait(smem_u32(&sm.out_done[q][j & 1]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_OUT);
+    };
+    Ring ring;
+    for (int j = 0; j < n_mine; ++j, ring.next(KVP_STAGES)) {
+      const int st = j & 1, t0 = KVP_TOK * j;
+      ok = mbar_wait(smem_u32(&sm.score[q][st]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_SCORE) &&
+           mbar_wait(smem_u32(&sm.tile_full[ring.stage]), ring.phase, abort_flag, a.err, ERR_KVP_TILE);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const float4* step = reinterpret_cast<const float4*>(sm.step[ring.stage]);  // (key, value) steps of two tokens
+      const unsigned lost = (unsigned)sm.lost[ring.stage];
+      const int* ex = sm.exponent[ring.stage];
+      const float ev = (float)max(max(ex[0], ex[1]), max(ex[2], ex[3]));
+      const uint32_t col = score_col(q, st) + lanes;
+      float2 sum = make_float2(0.0f, 0.0f);
+      // EDGE: some row of the warp does not see all tokens of the tile. The
+      // scores are read from tensor memory twice, half a tile at a time (for
+      // the maximum, then for the weights): a row's 64 do not fit the registers.
+      auto weigh = [&](auto edge_tag) -> bool {
+        constexpr bool EDGE = decltype(edge_tag)::value;
+        auto hidden = [&](int i) { return t0 + i >= vis || (lost >> (i >> 4) & 1u); };
+        float most = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t s[32];
+          __syncwarp();  // (rows of a warp part ways where some do not see a token)
+          tmem_ld_32x32b_x32(col + 32 * half, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const int i = 32 * half + k;
+            const float4 f = step[i >> 1];
+            float2 x = mul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), make_float2(f.x, f.z));
+            if (EDGE && hidden(i)) x.x = -INFINITY;
+            if (EDGE && hidden(i + 1)) x.y = -INFINITY;
+            most = fmaxf(most, fmaxf(x.x, x.y));
+          }
+        }
+        // the tile's largest value step joins the reference, so that weights stay below 2^9
+        const float want = fmaf(most, unit, ev);
+        float scale = 1.0f;
+        if (want > m + 8.0f) {
+          scale = exp2_fast(m - want);
+          m = want;
+          l *= scale;
+        }
+        const bool moved = __any_sync(0xffffffffu, scale != 1.0f);
+        if (j > 0 && moved) {
+          // bring the output along: the product of the tile before is in it
+          if (!__all_sync(0xffffffffu, product_done(j - 1))) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            __syncwarp();
+            tmem_ld_32x32b_x32(out_col(q) + lanes + 32 * c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
+            tmem_st_32x32b_x32(out_col(q) + lanes + 32 * c, v);
+          }
+          tmem_st_wait();
+        }
+        const float2 u2 = make_float2(unit, unit), m2 = make_float2(-m, -m);
+        uint32_t wbits[32];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t s[32];
+          __syncwarp();  // (rows of a warp part ways where some do not see a token)
+          tmem_ld_32x32b_x32(col + 32 * half, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const int i = 32 * half + k;
+            const float4 f = step[i >> 1];
+            float2 x = mul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), make_float2(f.x, f.z));
+            x = fma2(x, u2, m2);
+            float2 p = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+            if (EDGE && hidden(i)) p.x = 0.0f;
+            if (EDGE && hidden(i + 1)) p.y = 0.0f;
+            sum = add2(sum, p);
+            float2 w = mul2(p, make_float2(f.y, f.w));
+            if (EDGE && hidden(i)) w.x = 0.0f;
+            if (EDGE && hidden(i + 1)) w.y = 0.0f;
+            wbits[i >> 1] = pack2<true>(w.x, w.y);
+          }
+        }
+        __syncwarp();
+        tmem_st_32x32b_x32(col, wbits);
+        tmem_st_wait();
+        return true;
+      };
+      const bool edge = __any_sync(0xffffffffu, t0 + KVP_TOK > vis) || lost;
+      ok = edge ? weigh(std::true_type{}) : weigh(std::false_type{});
+      if (!ok) break;
+      l += sum.x + sum.y;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.weight[q][st]));  // (a warp may be a tile ahead of its neighbours)
+    }
+    // ---------------- output
+    if (ok && n_mine > 0) {
+      ok = product_done(n_mine - 1);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    const long long at = in ? kv4_out_row(a, seq, head, r) : -1;
+    const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+    if (ok) {
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        __syncwarp();
+        if (n_mine > 0) {
+          tmem_ld_32x32b_x32(out_col(q) + lanes + 32 * c, v);
+          tmem_ld_wait();
+        }
+        if (at >= 0) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // a row that sees nothing gives zeros, whatever stands in tensor memory
+              const float x = l == 0.0f ? 0.0f : __uint_as_float(v[8 * k + 2 * i]) * inv;
+              const float y = l == 0.0f ? 0.0f : __uint_as_float(v[8 * k + 2 * i + 1]) * inv;
+              o[i] = a.f16 ? pack2<true>(x, y) : pack2<false>(x, y);
+            }
+            dst[k] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (at >= 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace awq

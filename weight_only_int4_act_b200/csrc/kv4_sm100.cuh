@@ -703,6 +703,7 @@ struct Kv4SplitArgs {
   float* cta_part;  // [KV4_CTAS][2][8 NT][D + 4]
   long long* cta_seg;  // [KV4_CTAS][2] tile of a block partial (-1: none)
   int* cta_bad;     // [KV4_CTAS]
+  int max_rows;     // sequences of more query rows are another kernel's
   int solo;         // blocks take whole tiles
   int clear_err;    // the first launch of a call sets the error word, later ones add to it
 };
@@ -760,7 +761,7 @@ __device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, long
       if (q.bad) p.bad = 1;
       const int rows = q.n * a.share;
       // a sequence without context still has its rows to write: one unit, which reads nothing
-      const int span = q.n > 0 ? max(1, (int)(((long long)q.L + KV4_UNIT - 1) / KV4_UNIT)) : 0;
+      const int span = q.n > 0 && rows <= s.max_rows ? max(1, (int)(((long long)q.L + KV4_UNIT - 1) / KV4_UNIT)) : 0;
       const int tiles = (rows + s.tile_rows - 1) / s.tile_rows;
       p.span[b] = span;
       p.tiles[b] = tiles;
@@ -1092,7 +1093,7 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
       int bad = sm.plan.bad ? ERR_KV4_PAGE : 0;
       for (int i = lane; i < a.batch * a.table_pages; i += 32) {
         const int b = i / a.table_pages, p = i - b * a.table_pages, page = __ldg(a.table + i);
-        if (sm.plan.n[b] > 0 && (long long)p << a.c.page_shift < sm.plan.len[b] && (page < 0 || page >= a.c.n_pages))
+        if (sm.plan.span[b] > 0 && (long long)p << a.c.page_shift < sm.plan.len[b] && (page < 0 || page >= a.c.n_pages))
           bad = ERR_KV4_PAGE;
       }
       bad = __reduce_max_sync(0xffffffffu, bad);

@@ -4,6 +4,7 @@
 #pragma once
 #include <atomic>
 
+#include "kv4_prompt_sm100.cuh"
 #include "kv4_sm100.cuh"
 #include "w8a8_sm100.cuh"
 
@@ -180,6 +181,16 @@ awq_status check_kv4_attention(int64_t batch, int64_t n_q_heads, int64_t max_q, 
 #define KV4_SOLO 2048
 #endif
 constexpr int64_t KV4_SOLO_TOKENS = KV4_SOLO, KV4_SOLO_PAGES = 4096;
+
+// The prompt kernel takes the sequences of more than KVP_MIN_ROWS rows where it
+// has blocks for a good part of the SMs; else all go to the split kernel.
+#ifndef KVP_CTAS
+#define KVP_CTAS 40
+#endif
+bool kvp_used(int64_t batch, int64_t share, int64_t max_q, const awq_kv4cfg* c) {
+  return c->head_dim == c->group && c->head_dim <= 128 && max_q * share > KVP_MIN_ROWS &&
+         batch * c->n_kv_heads * cdiv(max_q * share, KVP_ROWS) >= KVP_CTAS;
+}
 
 // Workspace of the attention: [0, kAlign) error word, then the block flags and
 // tiles and the blocks' partial outputs.
@@ -420,8 +431,10 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   a.out = out;
   a.lse = lse;
   a.err = at<int>(ws, 0);
+  const bool prompt = kvp_used(batch, a.share, max_q, cfg);
   Kv4SplitArgs sa{};
   sa.tile_rows = 8 * L.nt;
+  sa.max_rows = prompt ? KVP_MIN_ROWS : INT32_MAX;
   sa.cta_part = at<float>(ws, L.off_cta);
   sa.cta_seg = at<long long>(ws, L.off_seg);
   sa.cta_bad = at<int>(ws, L.off_bad);
@@ -452,5 +465,19 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
     });
     if (st != AWQ_OK) return st;
   }
-  return AWQ_OK;
+  if (!prompt) return AWQ_OK;
+  KvpArgs pa{};
+  pa.a = a;
+  const dim3 grid((unsigned)cdiv(max_q * a.share, KVP_ROWS), (unsigned)cfg->n_kv_heads, (unsigned)batch);
+  auto launch = [&](auto d) -> awq_status {
+    constexpr int D = decltype(d)::value;
+    constexpr int smem = (int)sizeof(KvpSmem<D, D>) + 1024;
+    static_assert(smem <= 232448, "shared memory of the prompt attention");
+    auto k = kv4_attention_prompt<D, D>;
+    static std::atomic<unsigned long long> once{0};
+    if (!kernel_smem(k, smem, once)) return AWQ_ERR_CUDA;
+    k<<<grid, KVP_THREADS, smem, cs>>>(pa);
+    return launch_status();
+  };
+  return cfg->head_dim == 64 ? launch(std::integral_constant<int, 64>{}) : launch(std::integral_constant<int, 128>{});
 }
