@@ -6,25 +6,21 @@
 //   O_q += W_q C_v        M = 128 rows, N = D channels, K = 64 tokens
 // with fp16 operands and fp32 accumulators in tensor memory (S_q twice, so that
 // the next tile's scores are there when a softmax ends; W_q takes the place of
-// its S_q). With one group a head the codes less zeros (-15 .. 15) are exact in
-// fp16 and the steps enter in fp32: the score's as s = dk_t (q . c_t), the
-// value's in the weight w_t = p_t dv_t, which is rounded to fp16 (2^-11) once,
-// as in the split kernel. With several groups a head each code is also
-// multiplied by its group's step over the power of two of the token's largest
-// (one more rounding, 2^-11, of keys and values).
+// its S_q). It serves caches with one group a head: the codes less zeros (-15 ..
+// 15) are exact in fp16 and the steps enter in fp32, the key's in the score s =
+// dk_t (q . c_t), the value's in the weight w_t = p_t dv_t, which is rounded to
+// fp16 (2^-11) once, as in the split kernel.
 //
 // Warps (14): 0 loads packed strips (cp.async.bulk), 1 issues the MMAs, 2..5
 // unpack them into the operand tiles, 6..9 and 10..13 are the softmax of the
 // two row tiles, a thread a row. The running maximum may lag by 2^8 before the
 // output is rescaled, which is rare after the first tiles.
 #pragma once
-#include <type_traits>
-
 #include "kv4_sm100.cuh"
 
 namespace awq {
 
-constexpr int KVP_ROWS = 256, KVP_TOK = 64, KVP_THREADS = 448, KVP_STAGES = 3, KVP_RAW = 2;
+constexpr int KVP_ROWS = 256, KVP_TOK = 64, KVP_THREADS = 448, KVP_STAGES = 3, KVP_RAW = 5;
 constexpr int KVP_MIN_ROWS = 64;  // sequences of at most so many rows are the split kernel's
 constexpr int ERR_KVP_RAW = 0x601, ERR_KVP_FREE = 0x602, ERR_KVP_SCORE = 0x603, ERR_KVP_WEIGHT = 0x604, ERR_KVP_OUT = 0x605,
               ERR_KVP_TILE = 0x606;
@@ -34,10 +30,10 @@ struct KvpArgs {
   int tiles;  // row tiles of the longest sequence: gridDim.x
 };
 
-template <int D, int G>
+template <int D>
 struct KvpSmem {
   static constexpr int SUB = (D + 63) / 64;                 // 64-channel sub-tiles of 128-byte rows
-  static constexpr int STRIP = kv4_strip_bytes(D, G);
+  static constexpr int STRIP = kv4_strip_bytes(D, D);
   alignas(1024) uint8_t q[2][SUB][128 * 128];
   alignas(1024) uint8_t k[KVP_STAGES][SUB][KVP_TOK * 128];
   alignas(1024) uint8_t v[KVP_STAGES][D * 128];
@@ -74,6 +70,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
+// 16 columns of a thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Codes less zero of the four pairs of a word, exact in fp16: low nibbles as
 // (1024 + c) - (1024 + z), high ones as (1024 + 16 c) / 16 - (64 + z).
 // lo: bytes 0 and 2, bytes 1 and 3; hi: the same of the high nibbles.
@@ -94,14 +106,10 @@ __device__ __forceinline__ KvpPairs kvp_unpack(uint32_t w, __half2 z0, __half2 z
 }
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// The head-wide power of two of a token's steps and a group's step over it.
-__device__ __forceinline__ float kvp_pow2(float x) { return __uint_as_float(__float_as_uint(x) & 0x7F800000u); }
-
-template <int D, int G>
+template <int D>
 __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __grid_constant__ KvpArgs args) {
-  using Sm = KvpSmem<D, G>;
-  constexpr int SUB = Sm::SUB, NJ = D / 32, NG = D / G, STRIP = kv4_strip_bytes(D, G);
-  constexpr bool FOLD = NG > 1;
+  using Sm = KvpSmem<D>;
+  constexpr int NJ = D / 32, STRIP = Sm::STRIP;
   extern __shared__ uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const Kv4AttnArgs& a = args.a;
@@ -163,8 +171,8 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
     Ring ring;
     bool ok = true;
     for (int j = 0; j < n && ok; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&sm.raw_empty[ring.stage]), ring.phase ^ 1u, abort_flag, a.err,
-                                                   ERR_KVP_RAW, 32));
+      ok = __all_sync(0xffffffffu, mbar_wait_lean(smem_u32(&sm.raw_empty[ring.stage]), ring.phase ^ 1u, abort_flag, a.err,
+                                                   ERR_KVP_RAW));
       if (!ok) break;
       const uint32_t bar = smem_u32(&sm.raw_full[ring.stage]);
       // lane i < 4: strip i of the tile (pages of 16 .. 64 tokens and more hold 1, 2 or 4 of them in a row)
@@ -209,8 +217,8 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
         mma_commit(smem_u32(&sm.score[q][j & 1]));
       };
       Ring now, next;  // the stages of tiles j and j + 1
-      bool ok = mbar_wait(smem_u32(&sm.q_full), 0, abort_flag, a.err, ERR_KVP_TILE) &&
-                mbar_wait(smem_u32(&sm.tile_full[0]), 0, abort_flag, a.err, ERR_KVP_TILE);
+      bool ok = mbar_wait_lean(smem_u32(&sm.q_full), 0, abort_flag, a.err, ERR_KVP_TILE) &&
+                mbar_wait_lean(smem_u32(&sm.tile_full[0]), 0, abort_flag, a.err, ERR_KVP_TILE);
       if (ok) {
         tc_fence_after();
         for (int q = 0; q < 2; ++q)
@@ -219,19 +227,19 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       next.next(KVP_STAGES);
       for (int j = 0; ok && j < n; ++j) {
         if (j + 1 < n) {
-          ok = mbar_wait(smem_u32(&sm.tile_full[next.stage]), next.phase, abort_flag, a.err, ERR_KVP_TILE);
+          ok = mbar_wait_lean(smem_u32(&sm.tile_full[next.stage]), next.phase, abort_flag, a.err, ERR_KVP_TILE);
           if (!ok) break;
           tc_fence_after();
           for (int q = 0; q < 2 && ok; ++q)
             if (j + 1 < n_ctx[q]) {
               // the buffer of scores j + 1 held the weights of j - 1: their product is done
-              if (j > 0) ok = mbar_wait(smem_u32(&sm.out_done[q][(j - 1) & 1]), ((j - 1) >> 1) & 1, abort_flag, a.err, ERR_KVP_OUT);
+              if (j > 0) ok = mbar_wait_lean(smem_u32(&sm.out_done[q][(j - 1) & 1]), ((j - 1) >> 1) & 1, abort_flag, a.err, ERR_KVP_OUT);
               if (ok) scores(q, j + 1, next.stage);
             }
         }
         for (int q = 0; q < 2 && ok; ++q)
           if (j < n_ctx[q]) {
-            ok = mbar_wait(smem_u32(&sm.weight[q][j & 1]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_WEIGHT);
+            ok = mbar_wait_lean(smem_u32(&sm.weight[q][j & 1]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_WEIGHT);
             if (!ok) break;
             tc_fence_after();
             const uint64_t dv = desc_kmajor_sw128(smem_u32(sm.v[now.stage]));
@@ -254,39 +262,26 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
     const int u = warp - 2, r = lane >> 2, q4 = lane & 3;
     Ring ring, raw;
     for (int j = 0; j < n; ++j) {
-      bool ok = mbar_wait_sleep(smem_u32(&sm.raw_full[raw.stage]), raw.phase, abort_flag, a.err, ERR_KVP_RAW, 32) &&
-                mbar_wait_sleep(smem_u32(&sm.tile_empty[ring.stage]), ring.phase ^ 1u, abort_flag, a.err, ERR_KVP_FREE, 32);
+      bool ok = mbar_wait_lean(smem_u32(&sm.raw_full[raw.stage]), raw.phase, abort_flag, a.err, ERR_KVP_RAW) &&
+                mbar_wait_lean(smem_u32(&sm.tile_empty[ring.stage]), ring.phase ^ 1u, abort_flag, a.err, ERR_KVP_FREE);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint8_t* s = sm.raw[raw.stage] + u * STRIP;
       const bool lost = sm.lost_raw[raw.stage] >> u & 1;
       const int t0 = KVP_TOK * j + 16 * u;
       const uint32_t* kpar = reinterpret_cast<const uint32_t*>(s + 16 * D);
-      const uint32_t* vpar = kpar + 16 * NG;
+      const uint32_t* vpar = kpar + 16;
       // a token whose bytes may hold anything counts as zero 0, step 0
-      auto param = [&](const uint32_t* par, int gi, int t) -> float2 {
-        return !lost && t0 + t < seq.L ? widen2<true>(par[16 * gi + t]) : make_float2(0.0f, 0.0f);
+      auto param = [&](const uint32_t* par, int t) -> float2 {
+        return !lost && t0 + t < seq.L ? widen2<true>(par[t]) : make_float2(0.0f, 0.0f);
       };
-      // one factor a token: its step, or with several groups the power of two of its largest one
-      auto factor = [&](const uint32_t* par, int t) {
-        float f = param(par, 0, t).x;
-        bool nan = f != f;
-#pragma unroll
-        for (int gi = 1; gi < NG; ++gi) {
-          const float x = param(par, gi, t).x;
-          nan |= x != x;
-          f = fmaxf(f, x);
-        }
-        return nan ? __int_as_float(0x7fffffff) : FOLD ? kvp_pow2(f) : f;
-      };
-      // a group's step over the factor, in fp16 (exact), and the zero
-      auto ratio = [&](const uint32_t* par, int gi, int t, float f) {
-        const float2 p = param(par, gi, t);
-        return make_float2(f > 0.0f ? __fdividef(p.x, f) : 0.0f, p.y);  // (f: a power of two; NaN gives 0)
-      };
+      const int ta = 2 * q4, tb = ta + 8;
+      const __half2 kz[2] = {__float2half2_rn(param(kpar, r).y), __float2half2_rn(param(kpar, r + 8).y)};
+      const __half2 vz0 = __floats2half2_rn(param(vpar, ta).y, param(vpar, ta + 1).y),
+                    vz1 = __floats2half2_rn(param(vpar, tb).y, param(vpar, tb + 1).y);
       if (lane < 16) {
-        const float fk = factor(kpar, lane), fv = factor(vpar, lane);
-        sm.step[ring.stage][16 * u + lane] = make_float2(fk, fv);
+        const float fv = param(vpar, lane).x;
+        sm.step[ring.stage][16 * u + lane] = make_float2(param(kpar, lane).x, fv);
         const int e = fv > 0.0f ? (int)(__float_as_uint(fv) >> 23) - 127 : -200;
         const int top = __reduce_max_sync(0x0000ffffu, e);
         if (lane == 0) sm.exponent[ring.stage][u] = top;
@@ -298,61 +293,32 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
         const int t = 8 * half + r, row = 16 * u + t;
         uint32_t w[NJ];
         load_words<NJ>(s + t * (D / 2) + 4 * q4 * NJ, w);
-        const float f = FOLD ? factor(kpar, t) : 1.0f;
 #pragma unroll
         for (int jj = 0; jj < NJ; ++jj) {
-          const float2 p = FOLD ? ratio(kpar, jj * 32 / G, t, f) : param(kpar, 0, t);
-          const __half2 z = __float2half2_rn(p.y);
-          KvpPairs c = kvp_unpack(w[jj], z, z);
-          if (FOLD) {
-            const __half2 m = __float2half2_rn(p.x);
-            c.lo0 = __hmul2(c.lo0, m);
-            c.lo1 = __hmul2(c.lo1, m);
-            c.hi0 = __hmul2(c.hi0, m);
-            c.hi1 = __hmul2(c.hi1, m);
-          }
+          const KvpPairs c = kvp_unpack(w[jj], kz[half], kz[half]);
           const int chunk = 4 * jj + q4;
           *reinterpret_cast<uint4*>(sm.k[ring.stage][chunk >> 3] + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
               make_uint4(bits(c.lo0), bits(c.lo1), bits(c.hi0), bits(c.hi1));
         }
       }
       // values: rows are channels, 64 tokens of 2 bytes; a lane writes pairs of tokens
-      {
-        const int ta = 2 * q4, tb = ta + 8;
-        float f[4];
-        if (FOLD) {
-          f[0] = factor(vpar, ta), f[1] = factor(vpar, ta + 1), f[2] = factor(vpar, tb), f[3] = factor(vpar, tb + 1);
+      const uint2* vw = reinterpret_cast<const uint2*>(s + 8 * D) + lane;
+      uint2 w2[NJ];
+#pragma unroll
+      for (int p = 0; p < NJ; ++p) w2[p] = vw[32 * p];
+#pragma unroll
+      for (int p = 0; p < NJ; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const KvpPairs c = kvp_unpack(h ? w2[p].y : w2[p].x, vz0, vz1);
+          const int ch = 32 * p + 8 * h + r;  // (its low three bits are r's)
+          uint8_t* row = sm.v[ring.stage] + ch * 128 + 4 * q4;
+          const int c0 = ((2 * u) ^ r) << 4, c1 = ((2 * u + 1) ^ r) << 4;
+          *reinterpret_cast<uint32_t*>(row + c0) = bits(c.lo0);
+          *reinterpret_cast<uint32_t*>(row + c1) = bits(c.lo1);
+          *reinterpret_cast<uint32_t*>(row + 16 * 128 + c0) = bits(c.hi0);
+          *reinterpret_cast<uint32_t*>(row + 16 * 128 + c1) = bits(c.hi1);
         }
-        const uint2* vw = reinterpret_cast<const uint2*>(s + 8 * D) + lane;
-#pragma unroll
-        for (int p = 0; p < NJ; ++p) {
-          const int gi = p * 32 / G;
-          float2 x[4];
-          const int tk[4] = {ta, ta + 1, tb, tb + 1};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = FOLD ? ratio(vpar, gi, tk[i], f[i]) : param(vpar, 0, tk[i]);
-          const __half2 z0 = __floats2half2_rn(x[0].y, x[1].y), z1 = __floats2half2_rn(x[2].y, x[3].y);
-          const __half2 m0 = __floats2half2_rn(x[0].x, x[1].x), m1 = __floats2half2_rn(x[2].x, x[3].x);
-          const uint2 w2 = vw[32 * p];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            KvpPairs c = kvp_unpack(h ? w2.y : w2.x, z0, z1);
-            if (FOLD) {
-              c.lo0 = __hmul2(c.lo0, m0);
-              c.hi0 = __hmul2(c.hi0, m0);
-              c.lo1 = __hmul2(c.lo1, m1);
-              c.hi1 = __hmul2(c.hi1, m1);
-            }
-            const int ch = 32 * p + 8 * h + r;  // (its low three bits are r's)
-            uint8_t* row = sm.v[ring.stage] + ch * 128 + 4 * q4;
-            const int c0 = ((2 * u) ^ r) << 4, c1 = ((2 * u + 1) ^ r) << 4;
-            *reinterpret_cast<uint32_t*>(row + c0) = bits(c.lo0);
-            *reinterpret_cast<uint32_t*>(row + c1) = bits(c.lo1);
-            *reinterpret_cast<uint32_t*>(row + 16 * 128 + c0) = bits(c.hi0);
-            *reinterpret_cast<uint32_t*>(row + 16 * 128 + c1) = bits(c.hi1);
-          }
-        }
-      }
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
@@ -414,13 +380,13 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
     // Wait for the weights' product of tile j. (Scores j or j + 1 being there
     // means that the one of the same barrier before, j - 2, is done.)
     auto product_done = [&](int j) {
-      return mbar_wait(smem_u32(&sm.out_done[q][j & 1]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_OUT);
+      return mbar_wait_lean(smem_u32(&sm.out_done[q][j & 1]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_OUT);
     };
     Ring ring;
     for (int j = 0; j < n_mine; ++j, ring.next(KVP_STAGES)) {
       const int st = j & 1, t0 = KVP_TOK * j;
-      ok = mbar_wait(smem_u32(&sm.score[q][st]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_SCORE) &&
-           mbar_wait(smem_u32(&sm.tile_full[ring.stage]), ring.phase, abort_flag, a.err, ERR_KVP_TILE);
+      ok = mbar_wait_lean(smem_u32(&sm.score[q][st]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_SCORE) &&
+           mbar_wait_lean(smem_u32(&sm.tile_full[ring.stage]), ring.phase, abort_flag, a.err, ERR_KVP_TILE);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -430,27 +396,55 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       const float ev = (float)max(max(ex[0], ex[1]), max(ex[2], ex[3]));
       const uint32_t col = score_col(q, st) + lanes;
       float2 sum = make_float2(0.0f, 0.0f);
-      // EDGE: some row of the warp does not see all tokens of the tile. The
-      // scores are read from tensor memory twice, half a tile at a time (for
-      // the maximum, then for the weights): a row's 64 do not fit the registers.
-      auto weigh = [&](auto edge_tag) -> bool {
-        constexpr bool EDGE = decltype(edge_tag)::value;
+      const bool edge = __any_sync(0xffffffffu, t0 + KVP_TOK > vis) || lost;
+      bool done = false;
+      if (j > 0 && !edge) {
+        // The usual tile: weights under the reference as it stands, kept back
+        // until all of them turned out below 2^9.
+        const float2 u2 = make_float2(unit, unit), m2 = make_float2(-m, -m);
+        uint32_t s0[32], s1[32], wbits[32];
+        tmem_ld_32x32b_x32(col, s0);
+        tmem_ld_wait();
+        tmem_ld_32x32b_x32(col + 32, s1);
+        float big = 0.0f;
+        auto two = [&](uint32_t a0, uint32_t a1, int i) {
+          const float4 f = step[i];
+          const float2 x = fma2(mul2(make_float2(__uint_as_float(a0), __uint_as_float(a1)), make_float2(f.x, f.z)), u2, m2);
+          const float2 p = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+          sum = add2(sum, p);
+          const float2 w = mul2(p, make_float2(f.y, f.w));
+          big = fmaxf(big, fmaxf(w.x, w.y));
+          wbits[i] = pack2<true>(w.x, w.y);
+        };
+#pragma unroll
+        for (int k = 0; k < 16; ++k) two(s0[2 * k], s0[2 * k + 1], k);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) two(s1[2 * k], s1[2 * k + 1], 16 + k);
+        if (!__any_sync(0xffffffffu, big > 512.0f)) {
+          tmem_st_32x32b_x32(col, wbits);
+          done = true;
+        } else {
+          sum = make_float2(0.0f, 0.0f);
+        }
+      }
+      if (!done) {
+        // The first tile, one that some row does not see all of, and one whose
+        // scores outgrow the reference: first the row's largest score, then the
+        // weights, 16 tokens at a time (short code: it runs seldom).
         auto hidden = [&](int i) { return t0 + i >= vis || (lost >> (i >> 4) & 1u); };
         float most = -INFINITY;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t s[32];
-          __syncwarp();  // (rows of a warp part ways where some do not see a token)
-          tmem_ld_32x32b_x32(col + 32 * half, s);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[16];
+          __syncwarp();
+          tmem_ld_32x32b_x16(col + 16 * c, s);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const int i = 32 * half + k;
-            const float4 f = step[i >> 1];
-            float2 x = mul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), make_float2(f.x, f.z));
-            if (EDGE && hidden(i)) x.x = -INFINITY;
-            if (EDGE && hidden(i + 1)) x.y = -INFINITY;
-            most = fmaxf(most, fmaxf(x.x, x.y));
+          for (int k = 0; k < 16; k += 2) {
+            const float4 f = step[8 * c + (k >> 1)];
+            if (!hidden(16 * c + k)) most = fmaxf(most, __uint_as_float(s[k]) * f.x);
+            if (!hidden(16 * c + k + 1)) most = fmaxf(most, __uint_as_float(s[k + 1]) * f.z);
           }
         }
         // the tile's largest value step joins the reference, so that weights stay below 2^9
@@ -461,55 +455,49 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
           m = want;
           l *= scale;
         }
-        const bool moved = __any_sync(0xffffffffu, scale != 1.0f);
-        if (j > 0 && moved) {
+        if (__any_sync(0xffffffffu, scale != 1.0f) && j > 0) {
           // bring the output along: the product of the tile before is in it
-          if (!__all_sync(0xffffffffu, product_done(j - 1))) return false;
+          ok = __all_sync(0xffffffffu, product_done(j - 1));
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
             __syncwarp();
-            tmem_ld_32x32b_x32(out_col(q) + lanes + 32 * c, v);
+            tmem_ld_32x32b_x16(out_col(q) + lanes + 16 * c, v);
             tmem_ld_wait();
+            uint32_t a0[8], a1[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
-            tmem_st_32x32b_x32(out_col(q) + lanes + 32 * c, v);
+            for (int i = 0; i < 8; ++i) {
+              a0[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
+              a1[i] = __float_as_uint(__uint_as_float(v[8 + i]) * scale);
+            }
+            tmem_st_32x32b_x8(out_col(q) + lanes + 16 * c, a0);
+            tmem_st_32x32b_x8(out_col(q) + lanes + 16 * c + 8, a1);
           }
           tmem_st_wait();
         }
-        const float2 u2 = make_float2(unit, unit), m2 = make_float2(-m, -m);
-        uint32_t wbits[32];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t s[32];
-          __syncwarp();  // (rows of a warp part ways where some do not see a token)
-          tmem_ld_32x32b_x32(col + 32 * half, s);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {  // (weights of tokens 16 c .. over scores read already)
+          uint32_t s[16], wb[8];
+          __syncwarp();
+          tmem_ld_32x32b_x16(col + 16 * c, s);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const int i = 32 * half + k;
-            const float4 f = step[i >> 1];
-            float2 x = mul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), make_float2(f.x, f.z));
-            x = fma2(x, u2, m2);
-            float2 p = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-            if (EDGE && hidden(i)) p.x = 0.0f;
-            if (EDGE && hidden(i + 1)) p.y = 0.0f;
-            sum = add2(sum, p);
-            float2 w = mul2(p, make_float2(f.y, f.w));
-            if (EDGE && hidden(i)) w.x = 0.0f;
-            if (EDGE && hidden(i + 1)) w.y = 0.0f;
-            wbits[i >> 1] = pack2<true>(w.x, w.y);
+          for (int k = 0; k < 16; k += 2) {
+            const float4 f = step[8 * c + (k >> 1)];
+            const bool h0 = hidden(16 * c + k), h1 = hidden(16 * c + k + 1);
+            const float p0 = h0 ? 0.0f : exp2_fast(fmaf(__uint_as_float(s[k]) * f.x, unit, -m));
+            const float p1 = h1 ? 0.0f : exp2_fast(fmaf(__uint_as_float(s[k + 1]) * f.z, unit, -m));
+            sum.x += p0;
+            sum.y += p1;
+            wb[k >> 1] = pack2<true>(h0 ? 0.0f : p0 * f.y, h1 ? 0.0f : p1 * f.w);
           }
+          __syncwarp();
+          tmem_st_32x32b_x8(col + 8 * c, wb);
         }
-        __syncwarp();
-        tmem_st_32x32b_x32(col, wbits);
-        tmem_st_wait();
-        return true;
-      };
-      const bool edge = __any_sync(0xffffffffu, t0 + KVP_TOK > vis) || lost;
-      ok = edge ? weigh(std::true_type{}) : weigh(std::false_type{});
-      if (!ok) break;
+      }
+      tmem_st_wait();
       l += sum.x + sum.y;
       tc_fence_before();
       __syncwarp();
@@ -525,17 +513,17 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
     const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
     if (ok) {
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t v[16];
         __syncwarp();
         if (n_mine > 0) {
-          tmem_ld_32x32b_x32(out_col(q) + lanes + 32 * c, v);
+          tmem_ld_32x32b_x16(out_col(q) + lanes + 16 * c, v);
           tmem_ld_wait();
         }
         if (at >= 0) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + 32 * c);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + 16 * c);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

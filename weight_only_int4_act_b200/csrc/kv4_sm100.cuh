@@ -1112,7 +1112,7 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
         fresh_tile = false;
         done = 0;
       }
-      const bool here = mbar_wait(smem_u32(&sm.full[warp][stage]), phase, &sm.abort, nullptr, 0);
+      const bool here = mbar_wait_lean(smem_u32(&sm.full[warp][stage]), phase, &sm.abort, nullptr, 0);
       if (!__all_sync(0xffffffffu, here)) {
         // a copy that never came (the wait took two seconds): report, write nothing
         if (lane == 0) {

@@ -471,9 +471,9 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   const dim3 grid((unsigned)cdiv(max_q * a.share, KVP_ROWS), (unsigned)cfg->n_kv_heads, (unsigned)batch);
   auto launch = [&](auto d) -> awq_status {
     constexpr int D = decltype(d)::value;
-    constexpr int smem = (int)sizeof(KvpSmem<D, D>) + 1024;
+    constexpr int smem = (int)sizeof(KvpSmem<D>) + 1024;
     static_assert(smem <= 232448, "shared memory of the prompt attention");
-    auto k = kv4_attention_prompt<D, D>;
+    auto k = kv4_attention_prompt<D>;
     static std::atomic<unsigned long long> once{0};
     if (!kernel_smem(k, smem, once)) return AWQ_ERR_CUDA;
     k<<<grid, KVP_THREADS, smem, cs>>>(pa);

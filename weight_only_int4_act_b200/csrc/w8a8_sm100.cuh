@@ -171,6 +171,26 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+// mbar_wait for handshakes on the critical path: try_wait itself sleeps in
+// hardware for a while, and the clock, whose read costs about a microsecond, is
+// looked at only after many tries. Same bound and same effects when it gives up.
+__device__ __forceinline__ bool mbar_wait_lean(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > AWQ_WAIT_LIMIT_NS) {
+        *abort_flag = 1;
+        if (err) atomicCAS(err, 0, code);
+        return false;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ tensor-core product
 // Output channels are the M rows of tcgen05.mma kind::i8 (128 a CTA; 256 over a
 // CTA pair) and tokens the N columns (BN of them, a multiple of 16, or of 32 in
@@ -353,7 +373,7 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
         w8_tile(args, t, mb, nb);
         const int wrow = (mb * (PAIR ? 2 : 1) + (int)rank) * W8_BM, xrow = nb * bn + (int)rank * b_rows;
         for (int kb = 0; kb < args.n_kb; ++kb) {
-          if (!mbar_wait(empty(ring.stage), ring.phase ^ 1u, abort_flag, args.err, ERR_W8_EMPTY)) {
+          if (!mbar_wait_lean(empty(ring.stage), ring.phase ^ 1u, abort_flag, args.err, ERR_W8_EMPTY)) {
             ok = false;
             break;
           }
@@ -393,11 +413,11 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
       int local = 0;
       for (long long t = worker; ok && t < tiles; t += G, ++local) {
         const int acc = local & 1;
-        if (!mbar_wait(tempty(acc), ((local >> 1) & 1) ^ 1u, abort_flag, args.err, ERR_W8_TEMPTY)) break;
+        if (!mbar_wait_lean(tempty(acc), ((local >> 1) & 1) ^ 1u, abort_flag, args.err, ERR_W8_TEMPTY)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * acc_stride;
         for (int kb = 0; kb < args.n_kb; ++kb) {
-          if (!mbar_wait(full(ring.stage), ring.phase, abort_flag, args.err, ERR_W8_FULL)) {
+          if (!mbar_wait_lean(full(ring.stage), ring.phase, abort_flag, args.err, ERR_W8_FULL)) {
             ok = false;
             break;
           }
@@ -444,7 +464,7 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
       const float dw = in ? __ldg(args.dw + o) : 0.0f;
       const float bias = in && args.bias ? __ldg(args.bias + o) : 0.0f;
       __syncwarp();
-      const bool ready = mbar_wait_sleep(tfull(acc), (local >> 1) & 1u, abort_flag, args.err, ERR_W8_TFULL, 64);
+      const bool ready = mbar_wait_lean(tfull(acc), (local >> 1) & 1u, abort_flag, args.err, ERR_W8_TFULL);
       if (!__all_sync(0xffffffffu, ready)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + acc * acc_stride;
@@ -548,7 +568,7 @@ __global__ void __launch_bounds__(W8_SMALL_THREADS)
       Ring ring;
       uint32_t issued = 0, last_parity = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(empty(ring.stage), ring.phase ^ 1u, abort_flag, args.err, ERR_W8_EMPTY)) break;
+        if (!mbar_wait_lean(empty(ring.stage), ring.phase ^ 1u, abort_flag, args.err, ERR_W8_EMPTY)) break;
         const uint32_t sa = smem_u32(smem + ring.stage * stage_bytes);
         mbar_arrive_expect_tx(full(ring.stage), stage_bytes);
         tma_load_2d(sa, &tmW, full(ring.stage), kb * W8_BK, mb * W8_BM);
@@ -566,7 +586,7 @@ __global__ void __launch_bounds__(W8_SMALL_THREADS)
       const uint64_t d0 = desc_kmajor_sw128(smem_u32(smem));
       Ring ring;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(full(ring.stage), ring.phase, abort_flag, args.err, ERR_W8_FULL)) break;
+        if (!mbar_wait_lean(full(ring.stage), ring.phase, abort_flag, args.err, ERR_W8_FULL)) break;
         tc_fence_after();
         const uint64_t da = d0 + ((uint64_t)(ring.stage * stage_bytes) >> 4), db = da + (W8_A_STAGE >> 4);
 #pragma unroll
@@ -590,7 +610,7 @@ __global__ void __launch_bounds__(W8_SMALL_THREADS)
     if (tok < args.N) sdx[tok] = __ldg(args.dx + tok);
     asm volatile("bar.sync 1, 128;" ::: "memory");
     const float dw = in ? __ldg(args.dw + o) : 0.0f, bias = in && biased ? __ldg(args.bias + o) : 0.0f;
-    ready = __all_sync(0xffffffffu, mbar_wait_sleep(tfull, 0, abort_flag, args.err, ERR_W8_TFULL, 32)) && !*abort_flag;
+    ready = __all_sync(0xffffffffu, mbar_wait_lean(tfull, 0, abort_flag, args.err, ERR_W8_TFULL)) && !*abort_flag;
     tc_fence_after();
     for (int c = 0; c * 32 < args.N && ready; ++c) {
       uint32_t v[32];
