@@ -11,17 +11,23 @@
 // dk_t (q . c_t), the value's in the weight w_t = p_t dv_t, which is rounded to
 // fp16 (2^-11) once, as in the split kernel.
 //
-// Warps (14): 0 loads packed strips (cp.async.bulk), 1 issues the MMAs, 2..5
-// unpack them into the operand tiles, 6..9 and 10..13 are the softmax of the
-// two row tiles, a thread a row. The running maximum may lag by 2^8 before the
+// Warps (15): 0 loads packed strips (cp.async.bulk), 1 and 14 issue the MMAs of
+// the two row tiles (one thread for both spent as long on its handshakes as the
+// tensor cores on their work), 2..5 unpack strips into the operand tiles, 6..9
+// and 10..13 are the softmax of the two row tiles, a thread a row. The running maximum may lag by 2^14 before the
 // output is rescaled, which is rare after the first tiles.
 #pragma once
 #include "kv4_sm100.cuh"
 
 namespace awq {
 
-constexpr int KVP_ROWS = 256, KVP_TOK = 64, KVP_THREADS = 448, KVP_STAGES = 3, KVP_RAW = 5;
+constexpr int KVP_ROWS = 256, KVP_TOK = 64, KVP_THREADS = 480, KVP_STAGES = 3, KVP_RAW = 5;
 constexpr int KVP_MIN_ROWS = 64;  // sequences of at most so many rows are the split kernel's
+// The reference exponent may lag behind the largest score by this: weights then
+// reach 2^15, which fp16 holds, and are as exact as below 1; what falls below
+// 2^-24 of 1 does so beside a weight of at least 1. (With 8 instead, one tile in
+// eight had a warp that stopped to rescale: 587 instead of the figure below.)
+constexpr float KVP_LAG = 14.0f;
 constexpr int ERR_KVP_RAW = 0x601, ERR_KVP_FREE = 0x602, ERR_KVP_SCORE = 0x603, ERR_KVP_WEIGHT = 0x604, ERR_KVP_OUT = 0x605,
               ERR_KVP_TILE = 0x606;
 
@@ -42,7 +48,7 @@ struct KvpSmem {
   int exponent[KVP_STAGES][4];       // largest value step's, by strip
   int lost_raw[KVP_RAW], lost[KVP_STAGES];  // strips (by bit) in pages outside the cache
   uint64_t raw_full[KVP_RAW], raw_empty[KVP_RAW], tile_full[KVP_STAGES], tile_empty[KVP_STAGES];
-  uint64_t q_full, score[2][2], weight[2][2], out_done[2][2], drain;  // [row tile][context tile & 1]
+  uint64_t q_full[2], score[2][2], weight[2][2], out_done[2][2], drain[2];  // [row tile][context tile & 1]
   uint32_t tmem;
   int abort;
 };
@@ -139,9 +145,10 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
     }
     for (int s = 0; s < KVP_STAGES; ++s) {
       mbar_init(smem_u32(&sm.tile_full[s]), 4);
-      mbar_init(smem_u32(&sm.tile_empty[s]), 1);
+      mbar_init(smem_u32(&sm.tile_empty[s]), 2);
     }
-    mbar_init(smem_u32(&sm.q_full), 8);
+    mbar_init(smem_u32(&sm.q_full[0]), 4);
+    mbar_init(smem_u32(&sm.q_full[1]), 4);
     for (int q = 0; q < 2; ++q) {
       mbar_init(smem_u32(&sm.score[q][0]), 1);
       mbar_init(smem_u32(&sm.score[q][1]), 1);
@@ -150,7 +157,8 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       mbar_init(smem_u32(&sm.out_done[q][0]), 1);
       mbar_init(smem_u32(&sm.out_done[q][1]), 1);
     }
-    mbar_init(smem_u32(&sm.drain), 1);
+    mbar_init(smem_u32(&sm.drain[0]), 1);
+    mbar_init(smem_u32(&sm.drain[1]), 1);
     sm.abort = 0;
     fence_barrier_init();
   }
@@ -203,13 +211,15 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       while (globaltimer_ns() - t0 < 200000ull) {
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 14) {
     if (lane == 0 && n > 0) {
-      // ---------------- MMAs
+      // ---------------- MMAs of row tile q
+      const int q = warp == 1 ? 0 : 1;
       constexpr uint32_t F16_F32 = 1u << 4, M128 = (128u >> 4) << 24;
       constexpr uint32_t S_DESC = F16_F32 | ((KVP_TOK >> 3) << 17) | M128, O_DESC = F16_F32 | ((D >> 3) << 17) | M128;
-      auto scores = [&](int q, int j, int st) {
-        const uint64_t dq = desc_kmajor_sw128(smem_u32(sm.q[q][0])), dk = desc_kmajor_sw128(smem_u32(sm.k[st][0]));
+      const uint64_t dq = desc_kmajor_sw128(smem_u32(sm.q[q][0]));
+      auto scores = [&](int j, int st) {
+        const uint64_t dk = desc_kmajor_sw128(smem_u32(sm.k[st][0]));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           mma_bf16(score_col(q, j & 1), dq + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4),
@@ -217,44 +227,44 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
         mma_commit(smem_u32(&sm.score[q][j & 1]));
       };
       Ring now, next;  // the stages of tiles j and j + 1
-      bool ok = mbar_wait_lean(smem_u32(&sm.q_full), 0, abort_flag, a.err, ERR_KVP_TILE) &&
+      bool ok = mbar_wait_lean(smem_u32(&sm.q_full[q]), 0, abort_flag, a.err, ERR_KVP_TILE) &&
                 mbar_wait_lean(smem_u32(&sm.tile_full[0]), 0, abort_flag, a.err, ERR_KVP_TILE);
-      if (ok) {
+      if (ok && n_ctx[q] > 0) {
         tc_fence_after();
-        for (int q = 0; q < 2; ++q)
-          if (n_ctx[q] > 0) scores(q, 0, 0);
+        scores(0, 0);
       }
       next.next(KVP_STAGES);
       for (int j = 0; ok && j < n; ++j) {
-        if (j + 1 < n) {
-          ok = mbar_wait_lean(smem_u32(&sm.tile_full[next.stage]), next.phase, abort_flag, a.err, ERR_KVP_TILE);
+        if (j + 1 < n_ctx[q]) {
+          // the buffer of scores j + 1 held the weights of j - 1: their product is done
+          ok = mbar_wait_lean(smem_u32(&sm.tile_full[next.stage]), next.phase, abort_flag, a.err, ERR_KVP_TILE) &&
+               (j == 0 || mbar_wait_lean(smem_u32(&sm.out_done[q][(j - 1) & 1]), ((j - 1) >> 1) & 1, abort_flag, a.err,
+                                         ERR_KVP_OUT));
           if (!ok) break;
           tc_fence_after();
-          for (int q = 0; q < 2 && ok; ++q)
-            if (j + 1 < n_ctx[q]) {
-              // the buffer of scores j + 1 held the weights of j - 1: their product is done
-              if (j > 0) ok = mbar_wait_lean(smem_u32(&sm.out_done[q][(j - 1) & 1]), ((j - 1) >> 1) & 1, abort_flag, a.err, ERR_KVP_OUT);
-              if (ok) scores(q, j + 1, next.stage);
-            }
+          scores(j + 1, next.stage);
         }
-        for (int q = 0; q < 2 && ok; ++q)
-          if (j < n_ctx[q]) {
-            ok = mbar_wait_lean(smem_u32(&sm.weight[q][j & 1]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_WEIGHT);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t dv = desc_kmajor_sw128(smem_u32(sm.v[now.stage]));
+        if (j < n_ctx[q]) {
+          ok = mbar_wait_lean(smem_u32(&sm.weight[q][j & 1]), (j >> 1) & 1, abort_flag, a.err, ERR_KVP_WEIGHT);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dv = desc_kmajor_sw128(smem_u32(sm.v[now.stage]));
 #pragma unroll
-            for (int k = 0; k < KVP_TOK / 16; ++k)
-              mma_f16_tmem_a(out_col(q), score_col(q, j & 1) + 8 * k, dv + ((k * 32) >> 4), O_DESC, j > 0 || k > 0);
-            mma_commit(smem_u32(&sm.out_done[q][j & 1]));
-          }
-        if (ok) mma_commit(smem_u32(&sm.tile_empty[now.stage]));
+          for (int k = 0; k < KVP_TOK / 16; ++k)
+            mma_f16_tmem_a(out_col(q), score_col(q, j & 1) + 8 * k, dv + ((k * 32) >> 4), O_DESC, j > 0 || k > 0);
+          mma_commit(smem_u32(&sm.out_done[q][j & 1]));
+        } else {
+          // the other row tile's still: this one only hands the stage back once it is full
+          ok = mbar_wait_lean(smem_u32(&sm.tile_full[now.stage]), now.phase, abort_flag, a.err, ERR_KVP_TILE);
+          if (!ok) break;
+        }
+        mma_commit(smem_u32(&sm.tile_empty[now.stage]));
         now.next(KVP_STAGES);
         next.next(KVP_STAGES);
       }
       // what was issued ends before the block does
-      mma_commit(smem_u32(&sm.drain));
-      mbar_wait_drain(smem_u32(&sm.drain), 0);
+      mma_commit(smem_u32(&sm.drain[q]));
+      mbar_wait_drain(smem_u32(&sm.drain[q]), 0);
       if (!ok) *abort_flag = 1;
     }
   } else if (warp < 6) {
@@ -372,7 +382,7 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
     }
     fence_proxy_async_shared();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+    if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[q]));
     const float unit = top;
     float m = KV4_LOWEST, l = 0.0f;
     bool ok = true;
@@ -400,7 +410,7 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       bool done = false;
       if (j > 0 && !edge) {
         // The usual tile: weights under the reference as it stands, kept back
-        // until all of them turned out below 2^9.
+        // until all of them turned out to fit fp16.
         const float2 u2 = make_float2(unit, unit), m2 = make_float2(-m, -m);
         uint32_t s0[32], s1[32], wbits[32];
         tmem_ld_32x32b_x32(col, s0);
@@ -421,7 +431,7 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 16; ++k) two(s1[2 * k], s1[2 * k + 1], 16 + k);
-        if (!__any_sync(0xffffffffu, big > 512.0f)) {
+        if (!__any_sync(0xffffffffu, big > 32768.0f)) {
           tmem_st_32x32b_x32(col, wbits);
           done = true;
         } else {
@@ -447,10 +457,10 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
             if (!hidden(16 * c + k + 1)) most = fmaxf(most, __uint_as_float(s[k + 1]) * f.z);
           }
         }
-        // the tile's largest value step joins the reference, so that weights stay below 2^9
+        // the tile's largest value step joins the reference, so that weights stay below 2^(KVP_LAG + 1)
         const float want = fmaf(most, unit, ev);
         float scale = 1.0f;
-        if (want > m + 8.0f) {
+        if (want > m + KVP_LAG) {
           scale = exp2_fast(m - want);
           m = want;
           l *= scale;
