@@ -19,7 +19,10 @@ step, n the number of visible tokens:
   units, so that is at most 2^-25 max_t(p_t D_t) a token;
 - numerator and denominator are fp32 sums: (n/8 + 64) 2^-22 of the terms' sizes.
 So |O - O_ref| <= u |O| + sum_t p_t (e_t + 2^-11) (c_t + z_t) D_t + sum_t p_t e_t |O|
-  + 2^-25 max(p D) sum_t (c_t + z_t) + (n/8 + 64) 2^-22 (sum_t p_t (c_t + z_t) D_t + |O|), times 1.1."""
+  + 2^-25 max(p D) sum_t (c_t + z_t) + (n/8 + 64) 2^-22 (sum_t p_t (c_t + z_t) D_t + |O|), times 1.1.
+- The kernel for prompts holds values, and for bf16 also keys, as (code - zero) step in fp16, rounded once: 2^-11 |v| a
+  value, so sum_t p_t 2^-11 |v_t| more, and 2^-11 scale sum_i |q_i| |k_ti| more in ds_t. (Steps far below the strip's
+  largest: half of fp16's smallest subnormal, 2^-25, of 2^10 over it: 2^-35 of the largest, below the terms above.)"""
 import zlib
 
 import numpy as np
@@ -118,8 +121,10 @@ def _read(cache, cfg, slots):
     return out
 
 
-def _check(out, lse, q, cfg, parts, lens, starts, share, scale, dtype):
-    """Every row of every sequence against the oracle; parts: _read() of all tokens in order."""
+def _check(out, lse, q, cfg, parts, lens, starts, share, scale, dtype, prompt=False):
+    """Every row of every sequence against the oracle; parts: _read() of all tokens in order; prompt: the prompts' kernel
+    may have run."""
+    rk, rv = (2.0 ** -11 if dtype == "bf16" else 0.0, 2.0 ** -11) if prompt else (0.0, 0.0)
     g, D = cfg.group, cfg.head_dim
     rep = lambda a: np.repeat(a, g, axis=-1)  # noqa: E731
     (kc, ks, kz), (vc, vs, vz) = parts
@@ -141,7 +146,7 @@ def _check(out, lse, q, cfg, parts, lens, starts, share, scale, dtype):
             q_e = qq[r0:r1, e]
             s = scale * q_e @ k[:, h].T
             qa = np.abs(q_e) + 2.0 ** -8 * np.abs(q_e).max(axis=1, keepdims=True)  # 2^-8 * 2^-22: the fp16 query
-            ds = (D + 16) * 2.0 ** -22 * scale * qa @ ksize[:, h].T
+            ds = (D + 16) * 2.0 ** -22 * scale * qa @ ksize[:, h].T + rk * scale * qa @ np.abs(k[:, h]).T
             vis = p[:, e] > 0
             smax = np.where(vis, np.abs(s), 0).max(axis=1, keepdims=True) if L else np.zeros((n, 1))
             err = np.where(p[:, e] > 0, 1.01 * (ds + (np.abs(s) + smax + 40) * 2.0 ** -22) + 2.0 ** -20, 0)
@@ -152,7 +157,7 @@ def _check(out, lse, q, cfg, parts, lens, starts, share, scale, dtype):
             o = np.abs(ref[:, e])
             codes = vis.astype(np.float64) @ (vc[sl] + rep(vz[sl]))[:, h]
             tol = 1.1 * (UNIT[dtype] * o + (pe * (err + 2.0 ** -11)) @ vsize[:, h] + (pe * err).sum(1, keepdims=True) * o
-                         + 2.0 ** -25 * pd * codes + (seen / 8 + 64) * 2.0 ** -22 * (size + o)) + 2.0 ** -25
+                         + rv * pe @ np.abs(v[:, h])                         + 2.0 ** -25 * pd * codes + (seen / 8 + 64) * 2.0 ** -22 * (size + o)) + 2.0 ** -25
             d = np.abs(got[r0:r1, e] - ref[:, e])
             bad = ~(d <= tol)
             assert not bad.any(), (b, e, np.argwhere(bad)[:4], d[bad][:4], tol[bad][:4])
@@ -164,7 +169,7 @@ def _check(out, lse, q, cfg, parts, lens, starts, share, scale, dtype):
                 assert (np.abs(w[~empty] - ref_lse[~empty, e]) <= 1.1 * lt[~empty]).all()
 
 
-def _run(lens, new, heads, share, dim, group, page, dtype, seed, lse=True, **kw):
+def _run(lens, new, heads, share, dim, group, page, dtype, seed, lse=True, prompt=False, **kw):
     """Build, attend (q a strided slice, output and workspace given), check. new: rows of each sequence."""
     cfg, cache, table, lens_t, slots = _fill(lens, heads, dim, group, page, dtype, seed, **kw)
     starts = np.concatenate([[0], np.cumsum(new)])
@@ -178,7 +183,7 @@ def _run(lens, new, heads, share, dim, group, page, dtype, seed, lse=True, **kw)
     awq.workspace_error(work)
     out, l = r if lse else (r, None)
     assert (buf[0] == 9).all() and (buf[-1] == 9).all()
-    _check(out, l, q, cfg, _read(cache, cfg, slots), lens, starts, share, dim ** -0.5, dtype)
+    _check(out, l, q, cfg, _read(cache, cfg, slots), lens, starts, share, dim ** -0.5, dtype, prompt)
     again = awq.kv4_attention(q, cache, table, lens_t, cfg, ws=work, **args)
     rows = np.concatenate([np.arange(a, b) for a, b in zip(starts[:-1], starts[1:])]) if T else []
     assert torch.equal(again[rows], out[rows])  # the same bits on every call
@@ -224,35 +229,44 @@ def test_attention_prompt_chunk(dtype):
     _run([700, 260], [300, 260], 2, 4, 128, 128, 64, dtype, 77)
 
 
-# the batches below give enough blocks of 256 query rows for the tensor-memory kernel (one group a head, head_dim <= 128)
+# the batches below give enough blocks of 256 query rows for the tensor-memory kernel (head_dim <= 128; fp16: one group a head)
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("page", [16, 32, 64, 256])
 def test_prompt_pages_and_mixed_rows(dim, page, dtype):
     """Chunks behind older contexts, a whole prompt, single tokens and a sequence without rows in one batch."""
-    _run([700, 260, 90, 333, 64, 129, 40], [300, 260, 1, 70, 0, 129, 3], 8, 2, dim, dim, page, dtype, 7 * page + dim)
+    _run([700, 260, 90, 333, 64, 129, 40], [300, 260, 1, 70, 0, 129, 3], 8, 2, dim, dim, page, dtype, 7 * page + dim, prompt=True)
 
 
 @pytest.mark.parametrize("share,heads,new", [(1, 16, 700), (3, 7, 201), (8, 5, 260), (16, 40, 5), (71, 10, 15)])
 def test_prompt_shared_heads(share, heads, new):
     """Row tiles that cut a token's heads anywhere; few and many rows a token."""
-    _run([new + 77, new], [new, new], heads, share, 64, 64, 64, "bf16", share)
+    _run([new + 77, new], [new, new], heads, share, 64, 64, 64, "bf16", share, prompt=True)
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (96, 32), (128, 32), (128, 64)])
+def test_prompt_groups(dim, group):
+    """Several groups a head, of very different sizes; fp16 stays with the exact kernel."""
+    _run([400, 333], [300, 290], 8, 3, dim, group, 32, "bf16", dim + group, prompt=True)
+    loud = torch.exp(torch.arange(dim, device="cuda") // group * 2.0)
+    _run([400, 333], [300, 290], 8, 3, dim, group, 32, "bf16", dim + group, prompt=True, scale_k=loud.reciprocal())
+    _run([200, 133], [100, 90], 8, 3, dim, group, 32, "f16", dim + group)
 
 
 def test_prompt_more_rows_than_context():
     """Rows that see nothing: zeros and -inf."""
-    _run([100, 40, 0], [300, 129, 70], 16, 2, 128, 128, 16, "f16", 3)
+    _run([100, 40, 0], [300, 129, 70], 16, 2, 128, 128, 16, "f16", 3, prompt=True)
 
 
 def test_prompt_large_values_and_steps():
     loud = torch.ones(128, device="cuda")
     loud[3], loud[77] = 40.0, 25.0
-    _run([500, 390], [300, 290], 10, 4, 128, 128, 32, "bf16", 5, kscale=2.0, vscale=100.0, scale_k=loud)
-    _run([500, 390], [300, 290], 10, 4, 128, 128, 32, "f16", 6, kscale=0.01, vscale=1e-3)
+    _run([500, 390], [300, 290], 10, 4, 128, 128, 32, "bf16", 5, prompt=True, kscale=2.0, vscale=100.0, scale_k=loud)
+    _run([500, 390], [300, 290], 10, 4, 128, 128, 32, "f16", 6, prompt=True, kscale=0.01, vscale=1e-3)
 
 
 def test_prompt_long_context():
-    _run([6000, 5001], [260, 130], 10, 2, 128, 128, 64, "bf16", 8, lse=False)
+    _run([6000, 5001], [260, 130], 10, 2, 128, 128, 64, "bf16", 8, lse=False, prompt=True)
 
 
 def test_prompt_masked_tokens_may_hold_anything():
@@ -292,7 +306,7 @@ def test_scale_zero_and_negative(n):
     parts = _read(cache, cfg, slots)
     for scale in (0.0, -0.2):
         out, lse = awq.kv4_attention(q, cache, table, lens, cfg, q_start=start, max_q=n, scale=scale, lse=True)
-        _check(out, lse, q if scale >= 0 else -q, cfg, parts, [200, 170], [0, n, 2 * n], 2, abs(scale), "f16")
+        _check(out, lse, q if scale >= 0 else -q, cfg, parts, [200, 170], [0, n, 2 * n], 2, abs(scale), "f16", n > 1)
 
 
 def test_attention_large_values_and_steps():

@@ -2,20 +2,30 @@
 // 4-bit cache, on tcgen05. A block takes 256 rows (token x head of the group)
 // of one kv head in two tiles of 128, and walks the context in tiles of 64
 // tokens:
-//   S_q = Q_q C_k^T       M = 128 rows, N = 64 tokens, K = D; codes less zeros
-//   O_q += W_q C_v        M = 128 rows, N = D channels, K = 64 tokens
+//   S_q = Q_q K_t^T       M = 128 rows, N = 64 tokens, K = D
+//   O_q += W_q V_t        M = 128 rows, N = D channels, K = 64 tokens
 // with fp16 operands and fp32 accumulators in tensor memory (S_q twice, so that
 // the next tile's scores are there when a softmax ends; W_q takes the place of
-// its S_q). It serves caches with one group a head: the codes less zeros (-15 ..
-// 15) are exact in fp16 and the steps enter in fp32, the key's in the score s =
-// dk_t (q . c_t), the value's in the weight w_t = p_t dv_t, which is rounded to
-// fp16 (2^-11) once, as in the split kernel.
+// its S_q).
+//
+// Values are unpacked as (code - zero) step 2^(10 - e), e the exponent of the
+// largest step in the strip of 16 tokens: one rounding to fp16 (2^-11) of each
+// value, without overflow or underflow whatever the steps are; e joins the
+// weight's exponent, w = 2^(score + e - m), and leaves the sum of the p again, a
+// strip at a time. Keys the same, the strip's power of two going into the
+// factor of its scores; but for fp16 queries (EXACT; one group a head), whose
+// output resolves it, the codes less zeros (-15 .. 15) are the keys, exactly, and
+// each score is multiplied by its token's step in fp32. (Steps of both kinds
+// applied to scores and weights in fp32 cost a shared-memory load of 16 bytes
+// for every two tokens and thread, and shared memory, which also feeds the
+// MMAs, was what bound the kernel: 470 us at 2 x 2048 queries of 8000 tokens,
+// 32 over 8 heads of 128.)
+// A token one of whose groups holds NaN turns the rows that see it to NaN.
 //
 // Warps (15): 0 loads packed strips (cp.async.bulk), 1 and 14 issue the MMAs of
 // the two row tiles (one thread for both spent as long on its handshakes as the
 // tensor cores on their work), 2..5 unpack strips into the operand tiles, 6..9
-// and 10..13 are the softmax of the two row tiles, a thread a row. The running maximum may lag by 2^14 before the
-// output is rescaled, which is rare after the first tiles.
+// and 10..13 are the softmax of the two row tiles, a thread a row.
 #pragma once
 #include "kv4_sm100.cuh"
 
@@ -25,8 +35,8 @@ constexpr int KVP_ROWS = 256, KVP_TOK = 64, KVP_THREADS = 480, KVP_STAGES = 3, K
 constexpr int KVP_MIN_ROWS = 64;  // sequences of at most so many rows are the split kernel's
 // The reference exponent may lag behind the largest score by this: weights then
 // reach 2^15, which fp16 holds, and are as exact as below 1; what falls below
-// 2^-24 of 1 does so beside a weight of at least 1. (With 8 instead, one tile in
-// eight had a warp that stopped to rescale: 587 instead of the figure below.)
+// 2^-24 of 1 does so beside a weight of at least 1. (With 8, one tile in eight
+// had a warp that stopped to rescale.)
 constexpr float KVP_LAG = 14.0f;
 constexpr int ERR_KVP_RAW = 0x601, ERR_KVP_FREE = 0x602, ERR_KVP_SCORE = 0x603, ERR_KVP_WEIGHT = 0x604, ERR_KVP_OUT = 0x605,
               ERR_KVP_TILE = 0x606;
@@ -36,16 +46,23 @@ struct KvpArgs {
   int tiles;  // row tiles of the longest sequence: gridDim.x
 };
 
-template <int D>
+// What the softmax knows of a strip: its keys are (code - zero) step / key, its
+// values (code - zero) step 2^(10 - e), down = 2^-e; tokens (by bit) that hold NaN.
+struct KvpStrip {
+  float key, e, down;
+  unsigned nan;
+};
+
+template <int D, int G>
 struct KvpSmem {
   static constexpr int SUB = (D + 63) / 64;                 // 64-channel sub-tiles of 128-byte rows
-  static constexpr int STRIP = kv4_strip_bytes(D, D);
+  static constexpr int STRIP = kv4_strip_bytes(D, G);
   alignas(1024) uint8_t q[2][SUB][128 * 128];
   alignas(1024) uint8_t k[KVP_STAGES][SUB][KVP_TOK * 128];
   alignas(1024) uint8_t v[KVP_STAGES][D * 128];
   alignas(128) uint8_t raw[KVP_RAW][4 * STRIP];
-  float2 step[KVP_STAGES][KVP_TOK];  // (key, value) step of a token
-  int exponent[KVP_STAGES][4];       // largest value step's, by strip
+  alignas(16) KvpStrip strip[KVP_STAGES][4];
+  float step[KVP_STAGES][KVP_TOK];   // EXACT: key step of a token
   int lost_raw[KVP_RAW], lost[KVP_STAGES];  // strips (by bit) in pages outside the cache
   uint64_t raw_full[KVP_RAW], raw_empty[KVP_RAW], tile_full[KVP_STAGES], tile_empty[KVP_STAGES];
   uint64_t q_full[2], score[2][2], weight[2][2], out_done[2][2], drain[2];  // [row tile][context tile & 1]
@@ -97,6 +114,13 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
 // lo: bytes 0 and 2, bytes 1 and 3; hi: the same of the high nibbles.
 struct KvpPairs {
   __half2 lo0, lo1, hi0, hi1;
+  // times a factor each for (lo0, hi0) and (lo1, hi1), rounded once
+  __device__ __forceinline__ void scale(__half2 m0, __half2 m1) {
+    lo0 = __hmul2(lo0, m0);
+    hi0 = __hmul2(hi0, m0);
+    lo1 = __hmul2(lo1, m1);
+    hi1 = __hmul2(hi1, m1);
+  }
 };
 __device__ __forceinline__ KvpPairs kvp_unpack(uint32_t w, __half2 z0, __half2 z1) {
   // z0: the zeros of lo0 and hi0, z1: of lo1 and hi1
@@ -112,10 +136,11 @@ __device__ __forceinline__ KvpPairs kvp_unpack(uint32_t w, __half2 z0, __half2 z
 }
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-template <int D>
+template <int D, int G, bool EXACT>
 __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __grid_constant__ KvpArgs args) {
-  using Sm = KvpSmem<D>;
-  constexpr int NJ = D / 32, STRIP = Sm::STRIP;
+  using Sm = KvpSmem<D, G>;
+  constexpr int NJ = D / 32, NG = D / G, STRIP = Sm::STRIP;
+  static_assert(!EXACT || NG == 1, "one step a token");
   extern __shared__ uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const Kv4AttnArgs& a = args.a;
@@ -280,32 +305,52 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       const bool lost = sm.lost_raw[raw.stage] >> u & 1;
       const int t0 = KVP_TOK * j + 16 * u;
       const uint32_t* kpar = reinterpret_cast<const uint32_t*>(s + 16 * D);
-      const uint32_t* vpar = kpar + 16;
-      // a token whose bytes may hold anything counts as zero 0, step 0
-      auto param = [&](const uint32_t* par, int t) -> float2 {
-        return !lost && t0 + t < seq.L ? widen2<true>(par[t]) : make_float2(0.0f, 0.0f);
-      };
-      const int ta = 2 * q4, tb = ta + 8;
-      const __half2 kz[2] = {__float2half2_rn(param(kpar, r).y), __float2half2_rn(param(kpar, r + 8).y)};
-      const __half2 vz0 = __floats2half2_rn(param(vpar, ta).y, param(vpar, ta + 1).y),
-                    vz1 = __floats2half2_rn(param(vpar, tb).y, param(vpar, tb + 1).y);
-      if (lane < 16) {
-        const float fv = param(vpar, lane).x;
-        sm.step[ring.stage][16 * u + lane] = make_float2(param(kpar, lane).x, fv);
-        const int e = fv > 0.0f ? (int)(__float_as_uint(fv) >> 23) - 127 : -200;
-        const int top = __reduce_max_sync(0x0000ffffu, e);
-        if (lane == 0) sm.exponent[ring.stage][u] = top;
+      const uint32_t* vpar = kpar + 16 * NG;
+      // the strip's largest steps and its tokens that hold NaN: lane l looks at token l % 16, of the keys or the values
+      const int lt = lane & 15;
+      float most = 0.0f;
+      bool nan = false;
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) {
+        const float x = __low2float(*reinterpret_cast<const __half2*>((lane < 16 ? kpar : vpar) + 16 * gi + lt));
+        nan |= x != x;
+        most = fmaxf(most, x);
       }
+      const bool there = !lost && t0 + lt < seq.L;  // (else its bytes may hold anything)
+      int e = there && !nan ? (int)(__float_as_uint(most) >> 23) - 127 : -24;
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, d));
+      const unsigned nans = __ballot_sync(0xffffffffu, there && nan);
+      const int ek = __shfl_sync(0xffffffffu, e, 0), ev = __shfl_sync(0xffffffffu, e, 16);
+      if (EXACT && lane < 16) sm.step[ring.stage][16 * u + lane] = there ? most : 0.0f;
+      if (lane == 0)
+        sm.strip[ring.stage][u] = KvpStrip{EXACT ? 1.0f : __uint_as_float((uint32_t)(117 + ek) << 23), (float)ev,
+                                           __uint_as_float((uint32_t)(127 - ev) << 23), (nans | nans >> 16) & 0xffffu};
       if (u == 0 && lane == 0) sm.lost[ring.stage] = sm.lost_raw[raw.stage];
+      const float kup = __uint_as_float((uint32_t)(137 - ek) << 23), vup = __uint_as_float((uint32_t)(137 - ev) << 23);
+      // (step times its strip's power of two, zero) of a token's group; nothing where its bytes may hold anything or NaN
+      const unsigned dead = (nans | nans >> 16) | (lost ? 0xffffu : t0 + 16 > seq.L ? 0xffffu << max(seq.L - t0, 0) : 0u);
+      auto param = [&](const uint32_t* par, int gi, int t, float up) -> float2 {
+        const float2 p = widen2<true>(par[16 * gi + t]);
+        return dead >> t & 1u ? make_float2(0.0f, 0.0f) : make_float2(p.x * up, p.y);
+      };
       // keys: a lane takes the words of (token, q): chunk 4 j + q of the token's row holds channels 8 (4 j + q) + {0 4 2 6 1 5 3 7}
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int t = 8 * half + r, row = 16 * u + t;
         uint32_t w[NJ];
         load_words<NJ>(s + t * (D / 2) + 4 * q4 * NJ, w);
+        __half2 kz[NG], km[NG];
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+          const float2 p = param(kpar, gi, t, kup);
+          km[gi] = __float2half2_rn(p.x);
+          kz[gi] = __float2half2_rn(p.y);
+        }
 #pragma unroll
         for (int jj = 0; jj < NJ; ++jj) {
-          const KvpPairs c = kvp_unpack(w[jj], kz[half], kz[half]);
+          KvpPairs c = kvp_unpack(w[jj], kz[jj * 32 / G], kz[jj * 32 / G]);
+          if (!EXACT) c.scale(km[jj * 32 / G], km[jj * 32 / G]);
           const int chunk = 4 * jj + q4;
           *reinterpret_cast<uint4*>(sm.k[ring.stage][chunk >> 3] + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
               make_uint4(bits(c.lo0), bits(c.lo1), bits(c.hi0), bits(c.hi1));
@@ -313,14 +358,26 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       }
       // values: rows are channels, 64 tokens of 2 bytes; a lane writes pairs of tokens
       const uint2* vw = reinterpret_cast<const uint2*>(s + 8 * D) + lane;
+      const int ta = 2 * q4, tb = ta + 8;
       uint2 w2[NJ];
+      __half2 vz0[NG], vz1[NG], vm0[NG], vm1[NG];
 #pragma unroll
       for (int p = 0; p < NJ; ++p) w2[p] = vw[32 * p];
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) {
+        const float2 a0 = param(vpar, gi, ta, vup), a1 = param(vpar, gi, ta + 1, vup), b0 = param(vpar, gi, tb, vup),
+                     b1 = param(vpar, gi, tb + 1, vup);
+        vm0[gi] = __floats2half2_rn(a0.x, a1.x);
+        vz0[gi] = __floats2half2_rn(a0.y, a1.y);
+        vm1[gi] = __floats2half2_rn(b0.x, b1.x);
+        vz1[gi] = __floats2half2_rn(b0.y, b1.y);
+      }
 #pragma unroll
       for (int p = 0; p < NJ; ++p)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const KvpPairs c = kvp_unpack(h ? w2[p].y : w2[p].x, vz0, vz1);
+          KvpPairs c = kvp_unpack(h ? w2[p].y : w2[p].x, vz0[p * 32 / G], vz1[p * 32 / G]);
+          c.scale(vm0[p * 32 / G], vm1[p * 32 / G]);
           const int ch = 32 * p + 8 * h + r;  // (its low three bits are r's)
           uint8_t* row = sm.v[ring.stage] + ch * 128 + 4 * q4;
           const int c0 = ((2 * u) ^ r) << 4, c1 = ((2 * u + 1) ^ r) << 4;
@@ -400,65 +457,74 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const float4* step = reinterpret_cast<const float4*>(sm.step[ring.stage]);  // (key, value) steps of two tokens
+      const KvpStrip* strip = sm.strip[ring.stage];
+      const float4* step = reinterpret_cast<const float4*>(sm.step[ring.stage]);
       const unsigned lost = (unsigned)sm.lost[ring.stage];
-      const int* ex = sm.exponent[ring.stage];
-      const float ev = (float)max(max(ex[0], ex[1]), max(ex[2], ex[3]));
       const uint32_t col = score_col(q, st) + lanes;
-      float2 sum = make_float2(0.0f, 0.0f);
+      float sum = 0.0f;
       const bool edge = __any_sync(0xffffffffu, t0 + KVP_TOK > vis) || lost;
+      const bool nan = (strip[0].nan | strip[1].nan | strip[2].nan | strip[3].nan) != 0;
       bool done = false;
-      if (j > 0 && !edge) {
+      if (j > 0 && !edge && !nan) {
         // The usual tile: weights under the reference as it stands, kept back
         // until all of them turned out to fit fp16.
-        const float2 u2 = make_float2(unit, unit), m2 = make_float2(-m, -m);
         uint32_t s0[32], s1[32], wbits[32];
         tmem_ld_32x32b_x32(col, s0);
         tmem_ld_wait();
         tmem_ld_32x32b_x32(col + 32, s1);
-        float big = 0.0f;
-        auto two = [&](uint32_t a0, uint32_t a1, int i) {
-          const float4 f = step[i];
-          const float2 x = fma2(mul2(make_float2(__uint_as_float(a0), __uint_as_float(a1)), make_float2(f.x, f.z)), u2, m2);
-          const float2 p = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-          sum = add2(sum, p);
-          const float2 w = mul2(p, make_float2(f.y, f.w));
-          big = fmaxf(big, fmaxf(w.x, w.y));
-          wbits[i] = pack2<true>(w.x, w.y);
+        __half2 big = __float2half2_rn(0.0f);
+        auto sixteen = [&](const uint32_t* x, int c) {
+          const KvpStrip f = strip[c];
+          const float2 u2 = make_float2(unit * f.key, unit * f.key), m2 = make_float2(f.e - m, f.e - m);
+          float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float2 y = make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+            if (EXACT) {
+              const float4 d = step[4 * c + (k >> 2)];
+              y = mul2(y, k & 2 ? make_float2(d.z, d.w) : make_float2(d.x, d.y));
+            }
+            y = fma2(y, u2, m2);
+            const float2 w = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+            part = add2(part, w);
+            wbits[8 * c + (k >> 1)] = pack2<true>(w.x, w.y);
+            big = __hmax2(big, *reinterpret_cast<const __half2*>(&wbits[8 * c + (k >> 1)]));
+          }
+          sum = fmaf(part.x + part.y, f.down, sum);
         };
-#pragma unroll
-        for (int k = 0; k < 16; ++k) two(s0[2 * k], s0[2 * k + 1], k);
+        sixteen(s0, 0);
+        sixteen(s0 + 16, 1);
         tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) two(s1[2 * k], s1[2 * k + 1], 16 + k);
-        if (!__any_sync(0xffffffffu, big > 32768.0f)) {
+        sixteen(s1, 2);
+        sixteen(s1 + 16, 3);
+        const float2 top2 = __half22float2(big);
+        if (!__any_sync(0xffffffffu, fmaxf(top2.x, top2.y) > 32768.0f)) {
           tmem_st_32x32b_x32(col, wbits);
           done = true;
         } else {
-          sum = make_float2(0.0f, 0.0f);
+          sum = 0.0f;
         }
       }
       if (!done) {
-        // The first tile, one that some row does not see all of, and one whose
-        // scores outgrow the reference: first the row's largest score, then the
-        // weights, 16 tokens at a time (short code: it runs seldom).
+        // The first tile, one that some row does not see all of, one with NaN,
+        // and one whose scores outgrow the reference: first the row's largest
+        // exponent, then the weights, a strip at a time (short code: it runs seldom).
         auto hidden = [&](int i) { return t0 + i >= vis || (lost >> (i >> 4) & 1u); };
-        float most = -INFINITY;
+        float want = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t s[16];
           __syncwarp();
           tmem_ld_32x32b_x16(col + 16 * c, s);
           tmem_ld_wait();
+          float most = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const float4 f = step[8 * c + (k >> 1)];
-            if (!hidden(16 * c + k)) most = fmaxf(most, __uint_as_float(s[k]) * f.x);
-            if (!hidden(16 * c + k + 1)) most = fmaxf(most, __uint_as_float(s[k + 1]) * f.z);
+          for (int k = 0; k < 16; ++k) {
+            const float x = __uint_as_float(s[k]) * (EXACT ? sm.step[ring.stage][16 * c + k] : 1.0f);
+            if (!hidden(16 * c + k)) most = fmaxf(most, x);
           }
+          want = fmaxf(want, fmaf(most, unit * strip[c].key, strip[c].e));
         }
-        // the tile's largest value step joins the reference, so that weights stay below 2^(KVP_LAG + 1)
-        const float want = fmaf(most, unit, ev);
         float scale = 1.0f;
         if (want > m + KVP_LAG) {
           scale = exp2_fast(m - want);
@@ -493,22 +559,27 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
           __syncwarp();
           tmem_ld_32x32b_x16(col + 16 * c, s);
           tmem_ld_wait();
+          const KvpStrip f = strip[c];
+          float part = 0.0f;
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
-            const float4 f = step[8 * c + (k >> 1)];
-            const bool h0 = hidden(16 * c + k), h1 = hidden(16 * c + k + 1);
-            const float p0 = h0 ? 0.0f : exp2_fast(fmaf(__uint_as_float(s[k]) * f.x, unit, -m));
-            const float p1 = h1 ? 0.0f : exp2_fast(fmaf(__uint_as_float(s[k + 1]) * f.z, unit, -m));
-            sum.x += p0;
-            sum.y += p1;
-            wb[k >> 1] = pack2<true>(h0 ? 0.0f : p0 * f.y, h1 ? 0.0f : p1 * f.w);
+            float w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x = __uint_as_float(s[k + i]) * (EXACT ? sm.step[ring.stage][16 * c + k + i] : 1.0f);
+              w[i] = f.nan >> (k + i) & 1u ? __int_as_float(0x7fffffff) : exp2_fast(fmaf(x, unit * f.key, f.e - m));
+              if (hidden(16 * c + k + i)) w[i] = 0.0f;
+              part += w[i];
+            }
+            wb[k >> 1] = pack2<true>(w[0], w[1]);
           }
+          sum = fmaf(part, f.down, sum);
           __syncwarp();
           tmem_st_32x32b_x8(col + 8 * c, wb);
         }
       }
       tmem_st_wait();
-      l += sum.x + sum.y;
+      l += sum;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.weight[q][st]));  // (a warp may be a tile ahead of its neighbours)
@@ -520,7 +591,7 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       tc_fence_after();
     }
     const long long at = in ? kv4_out_row(a, seq, head, r) : -1;
-    const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+    const float inv = l == 0.0f ? 0.0f : __fdividef(0.0009765625f, l);  // (the values' 2^10)
     if (ok) {
 #pragma unroll 1
       for (int c = 0; c < D / 16; ++c) {

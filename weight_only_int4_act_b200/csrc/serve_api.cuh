@@ -187,8 +187,9 @@ constexpr int64_t KV4_SOLO_TOKENS = KV4_SOLO, KV4_SOLO_PAGES = 4096;
 #ifndef KVP_CTAS
 #define KVP_CTAS 40
 #endif
-bool kvp_used(int64_t batch, int64_t share, int64_t max_q, const awq_kv4cfg* c) {
-  return c->head_dim == c->group && c->head_dim <= 128 && max_q * share > KVP_MIN_ROWS &&
+bool kvp_used(int64_t batch, int64_t share, int64_t max_q, const awq_kv4cfg* c, bool f16) {
+  // (fp16 with several groups a head would be rounded more than its output resolves)
+  return c->head_dim <= 128 && (!f16 || c->head_dim == c->group) && max_q * share > KVP_MIN_ROWS &&
          batch * c->n_kv_heads * cdiv(max_q * share, KVP_ROWS) >= KVP_CTAS;
 }
 
@@ -431,7 +432,7 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   a.out = out;
   a.lse = lse;
   a.err = at<int>(ws, 0);
-  const bool prompt = kvp_used(batch, a.share, max_q, cfg);
+  const bool prompt = kvp_used(batch, a.share, max_q, cfg, a.f16);
   Kv4SplitArgs sa{};
   sa.tile_rows = 8 * L.nt;
   sa.max_rows = prompt ? KVP_MIN_ROWS : INT32_MAX;
@@ -469,15 +470,21 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   KvpArgs pa{};
   pa.a = a;
   const dim3 grid((unsigned)cdiv(max_q * a.share, KVP_ROWS), (unsigned)cfg->n_kv_heads, (unsigned)batch);
-  auto launch = [&](auto d) -> awq_status {
-    constexpr int D = decltype(d)::value;
-    constexpr int smem = (int)sizeof(KvpSmem<D>) + 1024;
-    static_assert(smem <= 232448, "shared memory of the prompt attention");
-    auto k = kv4_attention_prompt<D>;
-    static std::atomic<unsigned long long> once{0};
-    if (!kernel_smem(k, smem, once)) return AWQ_ERR_CUDA;
-    k<<<grid, KVP_THREADS, smem, cs>>>(pa);
-    return launch_status();
-  };
-  return cfg->head_dim == 64 ? launch(std::integral_constant<int, 64>{}) : launch(std::integral_constant<int, 128>{});
+  return kv4_shapes(cfg->head_dim, cfg->group, [&](auto d, auto g) -> awq_status {
+    constexpr int D = decltype(d)::value, G = decltype(g)::value;
+    if constexpr (D <= 128) {
+      constexpr int smem = (int)sizeof(KvpSmem<D, G>) + 1024;
+      static_assert(smem <= 232448, "shared memory of the prompt attention");
+      auto launch = [&](auto k, std::atomic<unsigned long long>& once) -> awq_status {
+        if (!kernel_smem(k, smem, once)) return AWQ_ERR_CUDA;
+        k<<<grid, KVP_THREADS, smem, cs>>>(pa);
+        return launch_status();
+      };
+      static std::atomic<unsigned long long> once[2];
+      if constexpr (D == G)
+        if (a.f16) return launch(kv4_attention_prompt<D, G, true>, once[1]);
+      return launch(kv4_attention_prompt<D, G, false>, once[0]);
+    }
+    return AWQ_ERR_UNSUPPORTED;  // (kvp_used keeps them with the split kernel)
+  });
 }

@@ -174,10 +174,13 @@ __global__ void __launch_bounds__(1024)
 // mbar_wait for handshakes on the critical path: try_wait itself sleeps in
 // hardware for a while, and the clock, whose read costs about a microsecond, is
 // looked at only after many tries. Same bound and same effects when it gives up.
-__device__ __forceinline__ bool mbar_wait_lean(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+// ns > 0: sleep so long between tries, where there is time, to leave the issue slots to others.
+__device__ __forceinline__ bool mbar_wait_lean(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code,
+                                               uint32_t ns = 0) {
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (ns) __nanosleep(ns);
     if ((it & 255u) == 0) {
       if (*abort_flag) return false;
       const uint64_t t = globaltimer_ns();
