@@ -63,6 +63,7 @@ struct KvpSmem {
   alignas(128) uint8_t raw[KVP_RAW][4 * STRIP];
   alignas(16) KvpStrip strip[KVP_STAGES][4];
   float step[KVP_STAGES][KVP_TOK];   // EXACT: key step of a token
+  float unit[2][128];                // score (log2) per unit of a row's product
   int lost_raw[KVP_RAW], lost[KVP_STAGES];  // strips (by bit) in pages outside the cache
   uint64_t raw_full[KVP_RAW], raw_empty[KVP_RAW], tile_full[KVP_STAGES], tile_empty[KVP_STAGES];
   uint64_t q_full[2], score[2][2], weight[2][2], out_done[2][2], drain[2];  // [row tile][context tile & 1]
@@ -103,10 +104,13 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // Codes less zero of the four pairs of a word, exact in fp16: low nibbles as
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
         return dead >> t & 1u ? make_float2(0.0f, 0.0f) : make_float2(p.x * up, p.y);
       };
       // keys: a lane takes the words of (token, q): chunk 4 j + q of the token's row holds channels 8 (4 j + q) + {0 4 2 6 1 5 3 7}
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int t = 8 * half + r, row = 16 * u + t;
         uint32_t w[NJ];
@@ -400,47 +404,61 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
     const int q = (warp - 6) >> 2, quad = warp & 3, row = quad * 32 + lane, r = r0 + 128 * q + row;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const bool in = r < rows;
-    const int tok = in ? (int)((unsigned)r / (unsigned)a.share) : 0, e = in ? r - tok * a.share : 0;
-    const int vis = in ? seq.L - seq.n + tok + 1 : 0;
-    float top = 0.0f;
+    const int vis = in ? seq.L - seq.n + (int)((unsigned)r / (unsigned)a.share) + 1 : 0;
     {
-      const long long off = (seq.row0 + tok) * a.q_tok + (long long)(head * a.share + e) * a.q_head;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + off);
-      const bool ok = in && AWQ_IDX_OK(seq.row0 + tok, a.T, BS_KV4_Q);
-      // the row twice (the second time out of the caches): its largest entry, then scaled so that it lies in [1, 2)
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      // The warp's 32 rows, a row by LANES lanes of 8 channels each: scaled by a
+      // power of two so that the largest entry lies in [2^10, 2^11) (a row of
+      // NaN or infinity: its operands become NaN or infinity too). A negative
+      // scale turns the query round, so that the largest score is the largest
+      // product's.
+      constexpr int LANES = D > 64 ? 16 : 8, PER = 32 / LANES;
+      const int chunk = lane % LANES;
+      const bool used = chunk < D / 8;
+      static_assert(32 / PER % 8 == 0, "rows in batches");
+      constexpr int BATCH = 8;  // rows' loads under way at once
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32 / PER; i0 += BATCH) {
+        uint4 ahead[BATCH];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = a.f16 ? widen2<true>(ww[i]) : widen2<false>(ww[i]);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        for (int i = 0; i < BATCH; ++i) {
+          const int gr = r0 + 128 * q + quad * 32 + PER * (i0 + i) + lane / LANES;
+          const bool have = gr < rows;
+          const int t = have ? (int)((unsigned)gr / (unsigned)a.share) : 0, he = have ? gr - t * a.share : 0;
+          const long long off = (seq.row0 + t) * a.q_tok + (long long)(head * a.share + he) * a.q_head;
+          ahead[i] = make_uint4(0, 0, 0, 0);
+          if (have && used && AWQ_IDX_OK(seq.row0 + t, a.T, BS_KV4_Q))
+            ahead[i] = __ldg(reinterpret_cast<const uint4*>(a.q + off) + chunk);
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int lr = quad * 32 + PER * (i0 + i) + lane / LANES;
+          const uint4 w = ahead[i];
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          float2 f[4];
+          float top = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[k] = a.f16 ? widen2<true>(ww[k]) : widen2<false>(ww[k]);
+            top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+          }
+#pragma unroll
+          for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const int ex = top > 0.0f ? min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -110), 127) : 0;
+          const float up = copysignf(__uint_as_float((uint32_t)(137 - ex) << 23), a.scale_log2);
+          // channels {0 4 2 6 1 5 3 7} of the eight, as the keys' codes come out of their words
+          if (used)
+            *reinterpret_cast<uint4*>(sm.q[q][chunk >> 3] + lr * 128 + (((chunk & 7) ^ (lr & 7)) << 4)) =
+                make_uint4(pack2<true>(f[0].x * up, f[2].x * up), pack2<true>(f[1].x * up, f[3].x * up),
+                           pack2<true>(f[0].y * up, f[2].y * up), pack2<true>(f[1].y * up, f[3].y * up));
+          // 2^(ex - 10) |scale|: score (log2) per unit of q . k; never 0, which would make hidden scores NaN
+          if (chunk == 0) sm.unit[q][lr] = fmaxf(__uint_as_float((uint32_t)(117 + ex) << 23) * fabsf(a.scale_log2), 1e-37f);
         }
       }
-      // (a row of NaN or infinity: its operands become NaN or infinity too)
-      const int ex = top > 0.0f ? min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -110), 127) : 0;
-      // (a negative scale turns the query round, so that the largest score is the largest product's)
-      const float down = copysignf(__uint_as_float((uint32_t)(137 - ex) << 23), a.scale_log2);
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 w = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-        float2 f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = a.f16 ? widen2<true>(ww[i]) : widen2<false>(ww[i]);
-        // channels {0 4 2 6 1 5 3 7} of the eight, as the keys' codes come out of their words
-        const uint4 o = make_uint4(pack2<true>(f[0].x * down, f[2].x * down), pack2<true>(f[1].x * down, f[3].x * down),
-                                   pack2<true>(f[0].y * down, f[2].y * down), pack2<true>(f[1].y * down, f[3].y * down));
-        *reinterpret_cast<uint4*>(sm.q[q][c >> 3] + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = o;
-      }
-      // 2^(ex - 10) |scale|: score (log2) per unit of q . c; never 0, which would make hidden scores NaN
-      top = fmaxf(__uint_as_float((uint32_t)(117 + ex) << 23) * fabsf(a.scale_log2), 1e-37f);
     }
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[q]));
-    const float unit = top;
+    const float unit = sm.unit[q][row];
     float m = KV4_LOWEST, l = 0.0f;
     bool ok = true;
     const int n_mine = n_ctx[q];
@@ -461,125 +479,112 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       const float4* step = reinterpret_cast<const float4*>(sm.step[ring.stage]);
       const unsigned lost = (unsigned)sm.lost[ring.stage];
       const uint32_t col = score_col(q, st) + lanes;
-      float sum = 0.0f;
-      const bool edge = __any_sync(0xffffffffu, t0 + KVP_TOK > vis) || lost;
-      const bool nan = (strip[0].nan | strip[1].nan | strip[2].nan | strip[3].nan) != 0;
-      bool done = false;
-      if (j > 0 && !edge && !nan) {
-        // The usual tile: weights under the reference as it stands, kept back
-        // until all of them turned out to fit fp16.
-        uint32_t s0[32], s1[32], wbits[32];
-        tmem_ld_32x32b_x32(col, s0);
+      // Half a tile at a time (short code: the warps of an SM sub-partition run
+      // four different loops, which together must stay in its instruction
+      // cache); its 16 columns of weights go over scores read already.
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        const KvpStrip f[2] = {strip[2 * c], strip[2 * c + 1]};
+        const unsigned off = lost >> (2 * c) & 3u;
+        const bool odd = __any_sync(0xffffffffu, t0 + 32 * c + 32 > vis) || off || f[0].nan || f[1].nan;
+        uint32_t s[32], wbits[16];
+        tmem_ld_32x32b_x32(col + 32 * c, s);
         tmem_ld_wait();
-        tmem_ld_32x32b_x32(col + 32, s1);
-        __half2 big = __float2half2_rn(0.0f);
-        auto sixteen = [&](const uint32_t* x, int c) {
-          const KvpStrip f = strip[c];
-          const float2 u2 = make_float2(unit * f.key, unit * f.key), m2 = make_float2(f.e - m, f.e - m);
-          float2 part = make_float2(0.0f, 0.0f);
+        float sum = 0.0f;
+        bool done = false;
+        if (!odd) {
+          // The usual case: weights under the reference as it stands, if all of them turn out to fit fp16.
+          __half2 big = __float2half2_rn(0.0f);
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float2 y = make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-            if (EXACT) {
-              const float4 d = step[4 * c + (k >> 2)];
-              y = mul2(y, k & 2 ? make_float2(d.z, d.w) : make_float2(d.x, d.y));
+          for (int h = 0; h < 2; ++h) {
+            const float2 u2 = make_float2(unit * f[h].key, unit * f[h].key), m2 = make_float2(f[h].e - m, f[h].e - m);
+            float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float2 y = make_float2(__uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]));
+              if (EXACT) {
+                const float4 d = step[8 * c + 4 * h + (k >> 2)];
+                y = mul2(y, k & 2 ? make_float2(d.z, d.w) : make_float2(d.x, d.y));
+              }
+              y = fma2(y, u2, m2);
+              const float2 w = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+              part = add2(part, w);
+              wbits[8 * h + (k >> 1)] = pack2<true>(w.x, w.y);
+              big = __hmax2(big, *reinterpret_cast<const __half2*>(&wbits[8 * h + (k >> 1)]));
             }
-            y = fma2(y, u2, m2);
-            const float2 w = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-            part = add2(part, w);
-            wbits[8 * c + (k >> 1)] = pack2<true>(w.x, w.y);
-            big = __hmax2(big, *reinterpret_cast<const __half2*>(&wbits[8 * c + (k >> 1)]));
+            sum = fmaf(part.x + part.y, f[h].down, sum);
           }
-          sum = fmaf(part.x + part.y, f.down, sum);
-        };
-        sixteen(s0, 0);
-        sixteen(s0 + 16, 1);
-        tmem_ld_wait();
-        sixteen(s1, 2);
-        sixteen(s1 + 16, 3);
-        const float2 top2 = __half22float2(big);
-        if (!__any_sync(0xffffffffu, fmaxf(top2.x, top2.y) > 32768.0f)) {
-          tmem_st_32x32b_x32(col, wbits);
-          done = true;
-        } else {
+          const float2 top2 = __half22float2(big);
+          done = !__any_sync(0xffffffffu, fmaxf(top2.x, top2.y) > 32768.0f);
+        }
+        if (!done) {
+          // The first tokens, some that a row does not see, NaN, and scores that
+          // outgrow the reference: the row's largest exponent first.
+          auto score = [&](int k) {
+            return __uint_as_float(s[k]) * (EXACT ? sm.step[ring.stage][32 * c + k] : 1.0f);
+          };
+          auto hidden = [&](int k) { return t0 + 32 * c + k >= vis || (off >> (k >> 4) & 1u); };
+          float want = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!hidden(k)) want = fmaxf(want, fmaf(score(k), unit * f[k >> 4].key, f[k >> 4].e));
+          float scale = 1.0f;
+          if (want > m + KVP_LAG) {
+            scale = exp2_fast(m - want);
+            m = want;
+            l *= scale;
+          }
+          if (__any_sync(0xffffffffu, scale != 1.0f)) {
+            // bring along the output, which the product of the tile before is in, and this tile's weights so far
+            if (j > 0) {
+              ok = __all_sync(0xffffffffu, product_done(j - 1));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < D / 16; ++i) {
+                uint32_t v[16];
+                __syncwarp();
+                tmem_ld_32x32b_x16(out_col(q) + lanes + 16 * i, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * scale);
+                tmem_st_32x32b_x16(out_col(q) + lanes + 16 * i, v);
+              }
+            }
+            if (c > 0) {
+              uint32_t v[16];
+              __syncwarp();
+              tmem_ld_32x32b_x16(col, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float2 w = widen2<true>(v[k]);
+                v[k] = pack2<true>(w.x * scale, w.y * scale);
+              }
+              tmem_st_32x32b_x16(col, v);
+            }
+            tmem_st_wait();
+          }
           sum = 0.0f;
-        }
-      }
-      if (!done) {
-        // The first tile, one that some row does not see all of, one with NaN,
-        // and one whose scores outgrow the reference: first the row's largest
-        // exponent, then the weights, a strip at a time (short code: it runs seldom).
-        auto hidden = [&](int i) { return t0 + i >= vis || (lost >> (i >> 4) & 1u); };
-        float want = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[16];
-          __syncwarp();
-          tmem_ld_32x32b_x16(col + 16 * c, s);
-          tmem_ld_wait();
-          float most = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float x = __uint_as_float(s[k]) * (EXACT ? sm.step[ring.stage][16 * c + k] : 1.0f);
-            if (!hidden(16 * c + k)) most = fmaxf(most, x);
-          }
-          want = fmaxf(want, fmaf(most, unit * strip[c].key, strip[c].e));
-        }
-        float scale = 1.0f;
-        if (want > m + KVP_LAG) {
-          scale = exp2_fast(m - want);
-          m = want;
-          l *= scale;
-        }
-        if (__any_sync(0xffffffffu, scale != 1.0f) && j > 0) {
-          // bring the output along: the product of the tile before is in it
-          ok = __all_sync(0xffffffffu, product_done(j - 1));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t v[16];
-            __syncwarp();
-            tmem_ld_32x32b_x16(out_col(q) + lanes + 16 * c, v);
-            tmem_ld_wait();
-            uint32_t a0[8], a1[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              a0[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
-              a1[i] = __float_as_uint(__uint_as_float(v[8 + i]) * scale);
-            }
-            tmem_st_32x32b_x8(out_col(q) + lanes + 16 * c, a0);
-            tmem_st_32x32b_x8(out_col(q) + lanes + 16 * c + 8, a1);
-          }
-          tmem_st_wait();
-        }
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {  // (weights of tokens 16 c .. over scores read already)
-          uint32_t s[16], wb[8];
-          __syncwarp();
-          tmem_ld_32x32b_x16(col + 16 * c, s);
-          tmem_ld_wait();
-          const KvpStrip f = strip[c];
-          float part = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
+          for (int k = 0; k < 32; k += 2) {
+            const KvpStrip& g = f[k >> 4];
             float w[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float x = __uint_as_float(s[k + i]) * (EXACT ? sm.step[ring.stage][16 * c + k + i] : 1.0f);
-              w[i] = f.nan >> (k + i) & 1u ? __int_as_float(0x7fffffff) : exp2_fast(fmaf(x, unit * f.key, f.e - m));
-              if (hidden(16 * c + k + i)) w[i] = 0.0f;
-              part += w[i];
+              w[i] = g.nan >> ((k + i) & 15) & 1u ? __int_as_float(0x7fffffff) : exp2_fast(fmaf(score(k + i), unit * g.key, g.e - m));
+              if (hidden(k + i)) w[i] = 0.0f;
+              sum = fmaf(w[i], g.down, sum);
             }
-            wb[k >> 1] = pack2<true>(w[0], w[1]);
+            wbits[k >> 1] = pack2<true>(w[0], w[1]);
           }
-          sum = fmaf(part, f.down, sum);
           __syncwarp();
-          tmem_st_32x32b_x8(col + 8 * c, wb);
         }
+        l += sum;
+        tmem_st_32x32b_x16(col + 16 * c, wbits);
       }
+      if (!ok) break;
       tmem_st_wait();
-      l += sum;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.weight[q][st]));  // (a warp may be a tile ahead of its neighbours)
