@@ -54,6 +54,67 @@ __device__ __forceinline__ int kv4_value_byte(int p, int h, int r, int t) {
   return ((p * 32 + r * 4 + ((t & 7) >> 1)) << 3) + 4 * h + 2 * (t & 1) + (t >> 3);
 }
 
+// Tokens that fill a strip in order (slots 16 i .. 16 i + 15 one behind the
+// other), as those of a prompt do, are taken together by one warp a head, the
+// others alone: a strip's values lie four tokens to a word, and one token alone
+// touches every one of its sectors.
+//
+// A block has the tokens [first, first + span), span <= 16, and the strips that
+// begin there. All lanes of a warp call this: lane l < span gets its token's slot,
+// and the masks have the tokens that begin a whole strip (one at most) and those
+// that are written alone. Bit i of a warp's view is token first - 16 + i; a bit of
+// `breaks` is set where a token does not follow the one before.
+struct Kv4Tokens {
+  int slot;
+  uint32_t strips, alone;
+};
+__device__ __forceinline__ Kv4Tokens kv4_tokens(const int* __restrict__ slots, int T, int first, int span, int lane) {
+  const int i0 = first - 16 + lane, i1 = first + 16 + lane;
+  const int a = i0 >= 0 && i0 < T ? __ldg(slots + i0) : 0, b = lane < 16 && i1 < T ? __ldg(slots + i1) : 0;
+  const int a_up = __shfl_up_sync(0xffffffffu, a, 1), b_up = __shfl_up_sync(0xffffffffu, b, 1);
+  const int last = __shfl_sync(0xffffffffu, a, 31);
+  const uint64_t breaks = (uint64_t)__ballot_sync(0xffffffffu, i0 < 1 || i0 >= T || lane == 0 || (unsigned)a - (unsigned)a_up != 1u) |
+                          (uint64_t)__ballot_sync(0xffffffffu, i1 >= T || (unsigned)b - (unsigned)(lane ? b_up : last) != 1u) << 32;
+  const int at = lane - (a & 15);  // where this token's strip would begin: 1 or more for lanes 16 ..
+  const bool mine = lane >= 16 && lane < 16 + span && i0 < T;
+  const bool whole = mine && ((breaks >> (at + 1)) & 0x7FFFu) == 0;
+  Kv4Tokens r;
+  r.slot = __shfl_sync(0xffffffffu, a, (lane & 15) + 16);
+  r.strips = __ballot_sync(0xffffffffu, whole && (a & 15) == 0) >> 16;
+  r.alone = __ballot_sync(0xffffffffu, mine && !whole) >> 16;
+  return r;
+}
+// Few tokens take a block each; more of them share blocks by strips.
+constexpr int KV4_APPEND_WARPS = 8;
+inline int kv4_span(long long T) { return T <= 1024 ? 1 : 16; }
+
+// a[j]'s nibble r to a[r]'s nibble j: halves, bytes, nibbles
+__device__ __forceinline__ void kv4_transpose(uint32_t (&a)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t x = a[j], y = a[j + 4];
+    a[j] = __byte_perm(x, y, 0x5410);
+    a[j + 4] = __byte_perm(x, y, 0x7632);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int j = (k & 1) + 4 * (k >> 1);
+    const uint32_t x = a[j], y = a[j + 2];
+    a[j] = __byte_perm(x, y, 0x6240);
+    a[j + 2] = __byte_perm(x, y, 0x7351);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint32_t x = a[j], y = a[j + 1];
+    a[j] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+    a[j + 1] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+  }
+}
+// The chunk (8 channels of a token) that is row j of the transposition of lane
+// item (p, q, h): token and chunk. Its word r is then that of lane (r, q).
+__device__ __forceinline__ int kv4_row_token(int j, int q) { return 2 * q + ((j >> 2) & 1) + 8 * ((j >> 1) & 1); }
+__device__ __forceinline__ int kv4_row_chunk(int j, int p, int h) { return 4 * p + 2 * (j & 1) + h; }
+
 struct Kv4AppendArgs {
   const uint16_t *k, *v;
   long long k_tok, k_head, v_tok, v_head;  // strides in elements
@@ -62,130 +123,256 @@ struct Kv4AppendArgs {
   Kv4Cache c;
 };
 
-// A thread takes 8 consecutive channels of one (token, head) of the keys or
-// the values; the g / 8 lanes of a group share its extremes by shuffles.
+// 8 channels of a token: their codes as a word (channel i in nibble i) and the
+// group's step and zero as stored. The g / 8 lanes of a group (neighbours; all
+// lanes of a warp call this) share its extremes by shuffles: (-min, max) as a
+// pair of the inputs' own type, whose order and sign are exact.
 template <bool F16>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendArgs a) {
-  const int chunks = a.c.dim / 8;
-  const long long units = (long long)a.T * a.c.heads * chunks;
-  const long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const bool live = u < 2 * units;
-  const bool val = u >= units;
-  const long long w = live ? (val ? u - units : u) : 0;
-  const int ch = (int)(w % chunks);
-  const long long th = w / chunks;
-  const int head = (int)(th % a.c.heads), tok = (int)(th / a.c.heads);
-  const int slot = live ? __ldg(a.slots + tok) : -1;
-  const bool put = slot >= 0 && (slot >> a.c.page_shift) < a.c.n_pages;
-  float x[8];
-  const uint16_t* src = (val ? a.v + tok * a.v_tok + head * a.v_head : a.k + tok * a.k_tok + head * a.k_head) + 8 * ch;
-  const uint4 raw = put ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (F16)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t kv4_quantize(const uint4& raw, int group, uint32_t& par) {
   const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
-  float lo = 0.0f, hi = 0.0f;
-  bool bad = false;
+  uint32_t low = 0, high = 0;  // 0 is always in the range
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    low = max2_nan<F16>(low, rw[i] ^ 0x80008000u);
+    high = max2_nan<F16>(high, rw[i]);
+  }
+  uint32_t both = max2_nan<F16>(__byte_perm(low, high, 0x5410), __byte_perm(low, high, 0x7632));
+  for (int o = group / 16; o; o >>= 1) both = max2_nan<F16>(both, __shfl_xor_sync(0xffffffffu, both, o));
+  const float2 ends = widen2<F16>(both);  // (-min, max); infinite or NaN if one of the inputs is
+  if (!(fmaxf(ends.x, ends.y) <= 3.402823466e38f && ends.x + ends.y == ends.x + ends.y)) {  // step NaN, codes and zero 0
+    par = 0x00007FFFu;
+    return 0;
+  }
+  const __half step = __float2half_rn(__fdiv_rn(__fadd_rn(ends.y, ends.x), 15.0f));
+  const float sf = fminf(fmaxf(__half2float(step), 5.9604644775390625e-8f), 65504.0f);
+  const float inv = __frcp_rn(sf);
+  const float zf = fminf(rintf(__fmul_rn(ends.x, inv)), 15.0f);
+  par = (uint32_t)__half_as_ushort(__float2half_rn(sf)) | (uint32_t)__half_as_ushort(__float2half_rn(zf)) << 16;
+  // clamp(rint(v) + z, 0, 15) = rint(clamp(v, -z, 15 - z)) + z: z is whole. The
+  // sum with 1.5 * 2^23 has rint(v) in its low bits; eight of them, each four
+  // bits further up, add to the word and to a known constant.
+  const float most = 15.0f - zf;
+  uint32_t word = (uint32_t)(int)zf * 0x11111111u - 0x4B400000u * 0x11111111u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = widen2<F16>(rw[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    const float v0 = fminf(fmaxf(__fmul_rn(f.x, inv), -zf), most), v1 = fminf(fmaxf(__fmul_rn(f.y, inv), -zf), most);
+    word += __float_as_uint(__fadd_rn(v0, 12582912.0f)) << (8 * i);
+    word += __float_as_uint(__fadd_rn(v1, 12582912.0f)) << (8 * i + 4);
   }
+  return word;
+}
+
+// Bound by HBM and, nearly as much, by the quantiser's instructions for prompts.
+template <bool F16>
+__global__ void __launch_bounds__(32 * KV4_APPEND_WARPS) kv4_append_kernel(const Kv4AppendArgs a, const int span) {
+  __shared__ uint32_t codes[KV4_APPEND_WARPS][16][33];  // a strip's value codes, a word a chunk; padded rows
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, begin = blockIdx.x * span;
+  const Kv4Tokens own = kv4_tokens(a.slots, a.T, begin, span, lane);
+  const int D = a.c.dim, chunks = D / 8, ng = D / a.c.group, per = a.c.group / 8, per_bits = __ffs(per) - 1, in_mask = (1 << a.c.page_shift) - 1;
+
+  for (uint32_t m = own.alone; m; m &= m - 1) {
+    const int i = __ffs(m) - 1, tok = begin + i, slot = __shfl_sync(0xffffffffu, own.slot, i);
+    const long long page = slot >> a.c.page_shift;
+    if (slot < 0 || page >= a.c.n_pages) continue;
+    // units of 8 channels: keys of all heads, then values (whole warps run, for the shuffles)
+    const int t = slot & 15, half = a.c.heads * chunks;
+    for (int u0 = 0; u0 < 2 * half; u0 += blockDim.x) {
+      const int u = u0 + threadIdx.x;
+      const bool live = u < 2 * half, val = u >= half;
+      const int w = live ? (val ? u - half : u) : 0, head = w / chunks, ch = w - head * chunks;
+      const uint16_t* src = (val ? a.v + (long long)tok * a.v_tok + (long long)head * a.v_head
+                                 : a.k + (long long)tok * a.k_tok + (long long)head * a.k_head) + 8 * ch;
+      const uint4 raw = live ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+      uint32_t par;
+      const uint32_t word = kv4_quantize<F16>(raw, a.c.group, par);
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 2);  // the 8 channels 16 away
+      const long long base = a.c.strip(page, head, slot & in_mask);
+      if (!live || !AWQ_SPAN_OK(base, a.c.strip_bytes, a.c.bytes(), BS_KV4_CACHE)) continue;
+      uint8_t* s = a.c.base + base;
+      if (!val) {
+        *reinterpret_cast<uint32_t*>(s + t * (D / 2) + ((ch & 3) * (D / 32) + (ch >> 2)) * 4) = word;
+      } else {
+        // lanes n = 0 and 1 hold channels 32 p + 8 h + r and 16 more: each writes four of the eight bytes
+        const int p = ch >> 2, n = (ch >> 1) & 1, h = ch & 1;
+        const uint32_t low = n ? other : word, high = n ? word : other;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    bad |= !(fabsf(x[i]) <= 3.402823466e38f);
-  }
-  if (bad) hi = __int_as_float(0x7f800000);
-  for (int o = a.c.group / 16; o; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const bool finite = hi <= 3.402823466e38f;
-  __half step = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-  const float sf = fminf(fmaxf(__half2float(step), 5.9604644775390625e-8f), 65504.0f);
-  const float inv = __frcp_rn(sf);
-  const float zf = fminf(rintf(__fmul_rn(-lo, inv)), 15.0f);
-  uint32_t word = 0;
-  if (finite) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = fminf(fmaxf(__fadd_rn(rintf(__fmul_rn(x[i], inv)), zf), 0.0f), 15.0f);
-      word |= (uint32_t)c << (4 * i);
+        for (int k = 0; k < 4; ++k) {
+          const int r = 4 * n + k;
+          s[8 * D + kv4_value_byte(p, h, r, t)] = (uint8_t)(((low >> (4 * r)) & 15u) | (((high >> (4 * r)) & 15u) << 4));
+        }
+      }
+      if ((ch & (per - 1)) == 0) *reinterpret_cast<uint32_t*>(s + 16 * D + (val ? 64 * ng : 0) + (ch >> per_bits) * 64 + 4 * t) = par;
     }
   }
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 2);  // the 8 channels 16 away
-  if (!put) return;
-  const int t = slot & 15;
-  const long long base = a.c.strip(slot >> a.c.page_shift, head, slot & ((1 << a.c.page_shift) - 1));
-  if (!AWQ_SPAN_OK(base, a.c.strip_bytes, a.c.bytes(), BS_KV4_CACHE)) return;
-  uint8_t* s = a.c.base + base;
-  if (!val) {
-    *reinterpret_cast<uint32_t*>(s + t * (a.c.dim / 2) + ((ch & 3) * (a.c.dim / 32) + (ch >> 2)) * 4) = word;
-  } else {
-    // lanes n = 0 and 1 hold channels 32 p + 8 h + r and 16 more: each writes four of the eight bytes
-    const int p = ch >> 2, n = (ch >> 1) & 1, h = ch & 1;
-    const uint32_t low = n ? other : word, high = n ? word : other;
+
+  if (!own.strips) return;
+  const int i = __ffs(own.strips) - 1, tok = begin + i, slot = __shfl_sync(0xffffffffu, own.slot, i);
+  const long long page = slot >> a.c.page_shift;
+  if (slot < 0 || page >= a.c.n_pages) return;
+  uint32_t(&cw)[16][33] = codes[warp];
+  // the warp's lanes over (token, chunk), tokens outermost: chunks of a group stay neighbours
+  const int t0 = lane / chunks, ch0 = lane - t0 * chunks, dt = 32 / chunks, dch = 32 - dt * chunks;
+  for (int head = warp; head < a.c.heads; head += KV4_APPEND_WARPS) {
+    const long long base = a.c.strip(page, head, slot & in_mask);
+    if (!AWQ_SPAN_OK(base, a.c.strip_bytes, a.c.bytes(), BS_KV4_CACHE)) continue;
+    uint8_t* s = a.c.base + base;
+#pragma unroll 1
+    for (int val = 0; val < 2; ++val) {
+      const uint16_t* src = val ? a.v + (long long)tok * a.v_tok + (long long)head * a.v_head
+                                : a.k + (long long)tok * a.k_tok + (long long)head * a.k_head;
+      const long long ld = val ? a.v_tok : a.k_tok;
+      uint8_t* pars = s + 16 * D + (val ? 64 * ng : 0);
+      int t = t0, ch = ch0;
+#pragma unroll 1
+      for (int u0 = 0; u0 < 16 * chunks; u0 += 64) {  // two chunks a lane at a time (16 * chunks is a multiple of 64)
+        uint4 raw[2];
+        int at[2], ac[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * n + i;
-      const uint32_t byte = ((low >> (4 * r)) & 15u) | (((high >> (4 * r)) & 15u) << 4);
-      s[8 * a.c.dim + kv4_value_byte(p, h, r, t)] = (uint8_t)byte;
+        for (int k = 0; k < 2; ++k) {
+          at[k] = t;
+          ac[k] = ch;
+          raw[k] = __ldg(reinterpret_cast<const uint4*>(src + t * ld + 8 * ch));
+          t += dt;
+          ch += dch;
+          if (ch >= chunks) ch -= chunks, ++t;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t par;
+          const uint32_t word = kv4_quantize<F16>(raw[k], a.c.group, par);
+          if (val)
+            cw[at[k]][ac[k]] = word;
+          else
+            *reinterpret_cast<uint32_t*>(s + at[k] * (D / 2) + ((ac[k] & 3) * (D / 32) + (ac[k] >> 2)) * 4) = word;
+          if ((ac[k] & (per - 1)) == 0) *reinterpret_cast<uint32_t*>(pars + (ac[k] >> per_bits) * 64 + 4 * at[k]) = par;
+        }
+      }
     }
-  }
-  if (ch % (a.c.group / 8) == 0) {
-    const int gi = ch / (a.c.group / 8), ng = a.c.dim / a.c.group;
-    const uint32_t par = finite ? (uint32_t)__half_as_ushort(__float2half_rn(sf)) |
-                                      (uint32_t)__half_as_ushort(__float2half_rn(zf)) << 16
-                                : 0x00007FFFu;
-    *reinterpret_cast<uint32_t*>(s + 16 * a.c.dim + (val ? 64 * ng : 0) + gi * 64 + 4 * t) = par;
+    __syncwarp();
+    for (int it = lane; it < D / 4; it += 32) {  // items (p, q, h)
+      const int h = it & 1, q = (it >> 1) & 3, p = it >> 3;
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = cw[kv4_row_token(j, q)][kv4_row_chunk(j, p, h)];
+      kv4_transpose(w);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) *reinterpret_cast<uint32_t*>(s + 8 * D + (p * 32 + 4 * r + q) * 8 + 4 * h) = w[r];
+    }
+    __syncwarp();
   }
 }
 
-// (code - zero) * step of one token of the cache, dense: a thread takes 8
-// consecutive channels; slots outside the cache give zeros.
+// (code - zero) * step of tokens of the cache, dense; slots outside it give
+// zeros. Blocks, strips and warps as in the write.
 template <bool F16>
-__global__ void __launch_bounds__(256)
-    kv4_gather_kernel(const Kv4Cache c, const int* __restrict__ slots, int T, void* __restrict__ kv, void* __restrict__ vv) {
-  const int chunks = c.dim / 8;
-  const long long units = (long long)T * c.heads * chunks;
-  for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < 2 * units;
-       u += (long long)gridDim.x * blockDim.x) {
-    const bool val = u >= units;
-    const long long w = val ? u - units : u;
-    const int ch = (int)(w % chunks);
-    const long long th = w / chunks;
-    const int head = (int)(th % c.heads), tok = (int)(th / c.heads);
-    const int slot = __ldg(slots + tok);
-    uint4 out = make_uint4(0, 0, 0, 0);
-    if (slot >= 0 && (slot >> c.page_shift) < c.n_pages) {
-      const int t = slot & 15;
-      const long long base = c.strip(slot >> c.page_shift, head, slot & ((1 << c.page_shift) - 1));
-      if (AWQ_SPAN_OK(base, c.strip_bytes, c.bytes(), BS_KV4_CACHE)) {
+__device__ __forceinline__ uint4 kv4_values(uint32_t word, uint32_t par) {
+  const float2 f = widen2<true>(par);  // (step, zero)
+  const float off = 8388608.0f + f.y;  // zero <= 15: exact, as is the difference
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = pack2<F16>(__fmul_rn(__fsub_rn(__uint_as_float(((word >> (8 * i)) & 15u) | 0x4B000000u), off), f.x),
+                      __fmul_rn(__fsub_rn(__uint_as_float(((word >> (8 * i + 4)) & 15u) | 0x4B000000u), off), f.x));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(32 * KV4_APPEND_WARPS)
+    kv4_gather_kernel(const Kv4Cache c, const int* __restrict__ slots, int T, void* __restrict__ kv, void* __restrict__ vv,
+                      const int span) {
+  __shared__ uint32_t codes[KV4_APPEND_WARPS][16][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, begin = blockIdx.x * span;
+  const Kv4Tokens own = kv4_tokens(slots, T, begin, span, lane);
+  const int D = c.dim, chunks = D / 8, ng = D / c.group, per_bits = __ffs(c.group / 8) - 1, in_mask = (1 << c.page_shift) - 1;
+  const long long all = (long long)T * c.heads * D;
+  bool in = true;
+  if (own.strips) {  // a strip outside the cache: its tokens are zeros
+    const int slot = __shfl_sync(0xffffffffu, own.slot, __ffs(own.strips) - 1);
+    in = slot >= 0 && (slot >> c.page_shift) < c.n_pages;
+  }
+
+  for (uint32_t m = own.alone; m; m &= m - 1) {
+    const int i = __ffs(m) - 1, tok = begin + i, slot = __shfl_sync(0xffffffffu, own.slot, i);
+    const long long page = slot >> c.page_shift;
+    const bool here = slot >= 0 && page < c.n_pages;
+    const int t = slot & 15, half = c.heads * chunks;
+    for (int u = threadIdx.x; u < 2 * half; u += blockDim.x) {
+      const bool val = u >= half;
+      const int w = val ? u - half : u, head = w / chunks, ch = w - head * chunks;
+      uint4 out = make_uint4(0, 0, 0, 0);
+      const long long base = here ? c.strip(page, head, slot & in_mask) : 0;
+      if (here && AWQ_SPAN_OK(base, c.strip_bytes, c.bytes(), BS_KV4_CACHE)) {
         const uint8_t* s = c.base + base;
-        const int gi = ch / (c.group / 8), ng = c.dim / c.group;
-        const uint32_t par = *reinterpret_cast<const uint32_t*>(s + 16 * c.dim + (val ? 64 * ng : 0) + gi * 64 + 4 * t);
-        const float step = __half2float(__ushort_as_half((unsigned short)(par & 0xFFFF)));
-        const float zero = __half2float(__ushort_as_half((unsigned short)(par >> 16)));
-        uint32_t codes = 0;
+        uint32_t word = 0;
         if (!val) {
-          codes = *reinterpret_cast<const uint32_t*>(s + t * (c.dim / 2) + ((ch & 3) * (c.dim / 32) + (ch >> 2)) * 4);
+          word = *reinterpret_cast<const uint32_t*>(s + t * (D / 2) + ((ch & 3) * (D / 32) + (ch >> 2)) * 4);
         } else {
           const int p = ch >> 2, n = (ch >> 1) & 1, h = ch & 1;
 #pragma unroll
           for (int r = 0; r < 8; ++r)
-            codes |= ((uint32_t)(s[8 * c.dim + kv4_value_byte(p, h, r, t)] >> (4 * n)) & 15u) << (4 * r);
+            word |= ((uint32_t)(s[8 * D + kv4_value_byte(p, h, r, t)] >> (4 * n)) & 15u) << (4 * r);
         }
-        uint32_t o[4];
+        out = kv4_values<F16>(word, *reinterpret_cast<const uint32_t*>(s + 16 * D + (val ? 64 * ng : 0) + (ch >> per_bits) * 64 + 4 * t));
+      }
+      uint16_t* dst = static_cast<uint16_t*>(val ? vv : kv);
+      const long long at = ((long long)tok * c.heads + head) * D + 8 * ch;
+      if (dst && AWQ_SPAN_OK(at, 8, all, BS_KV4_OUT)) *reinterpret_cast<uint4*>(dst + at) = out;
+    }
+  }
+
+  if (!own.strips) return;
+  const int i = __ffs(own.strips) - 1, tok = begin + i, slot = __shfl_sync(0xffffffffu, own.slot, i);
+  const long long page = slot >> c.page_shift;
+  uint32_t(&cw)[16][33] = codes[warp];
+  const int t0 = lane / chunks, ch0 = lane - t0 * chunks, dt = 32 / chunks, dch = 32 - dt * chunks;
+  for (int head = warp; head < c.heads; head += KV4_APPEND_WARPS) {
+    const long long base = in ? c.strip(page, head, slot & in_mask) : 0;
+    const bool ok = in && AWQ_SPAN_OK(base, c.strip_bytes, c.bytes(), BS_KV4_CACHE);
+    const uint8_t* s = c.base + base;
+    if (vv && ok) {
+      for (int it = lane; it < D / 4; it += 32) {
+        const int h = it & 1, q = (it >> 1) & 3, p = it >> 3;
+        uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = (float)((codes >> (8 * i)) & 15u), y = (float)((codes >> (8 * i + 4)) & 15u);
-          o[i] = pack2<F16>(__fmul_rn(x - zero, step), __fmul_rn(y - zero, step));
+        for (int r = 0; r < 8; ++r) w[r] = *reinterpret_cast<const uint32_t*>(s + 8 * D + (p * 32 + 4 * r + q) * 8 + 4 * h);
+        kv4_transpose(w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cw[kv4_row_token(j, q)][kv4_row_chunk(j, p, h)] = w[j];
+      }
+      __syncwarp();
+    }
+#pragma unroll 1
+    for (int val = 0; val < 2; ++val) {
+      uint16_t* dst = static_cast<uint16_t*>(val ? vv : kv);
+      if (!dst) continue;
+      const uint8_t* pars = s + 16 * D + (val ? 64 * ng : 0);
+      int t = t0, ch = ch0;
+#pragma unroll 2
+      for (int u0 = 0; u0 < 16 * chunks; u0 += 32) {
+        uint4 out = make_uint4(0, 0, 0, 0);
+        if (ok) {
+          const uint32_t word =
+              val ? cw[t][ch] : *reinterpret_cast<const uint32_t*>(s + t * (D / 2) + ((ch & 3) * (D / 32) + (ch >> 2)) * 4);
+          out = kv4_values<F16>(word, *reinterpret_cast<const uint32_t*>(pars + (ch >> per_bits) * 64 + 4 * t));
         }
-        out = make_uint4(o[0], o[1], o[2], o[3]);
+        const long long at = ((long long)(tok + t) * c.heads + head) * D + 8 * ch;
+        if (AWQ_SPAN_OK(at, 8, all, BS_KV4_OUT)) *reinterpret_cast<uint4*>(dst + at) = out;
+        t += dt;
+        ch += dch;
+        if (ch >= chunks) ch -= chunks, ++t;
       }
     }
-    void* dst = val ? vv : kv;
-    if (dst && AWQ_SPAN_OK(8 * w, 8, 8 * units, BS_KV4_OUT)) reinterpret_cast<uint4*>(dst)[w] = out;
+    __syncwarp();
   }
 }
 

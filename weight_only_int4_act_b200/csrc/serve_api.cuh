@@ -356,13 +356,12 @@ extern "C" awq_status awq_kv4_append(const void* k, const void* v, awq_dtype dty
   a.slots = slots;
   a.T = (int)T;
   a.c = kv4_cache(cfg, cache, n_pages);
-  const long long threads = 2 * T * cfg->n_kv_heads * (cfg->head_dim / 8);
-  if (cdiv(threads, 256) > INT32_MAX) return AWQ_ERR_SHAPE;
-  const unsigned grid = (unsigned)cdiv(threads, 256);
+  const int span = kv4_span(T);
+  const unsigned blocks = (unsigned)((T + span - 1) / span);
   if (dtype == AWQ_DTYPE_F16)
-    kv4_append_kernel<true><<<grid, 256, 0, as_stream(stream)>>>(a);
+    kv4_append_kernel<true><<<blocks, 32 * KV4_APPEND_WARPS, 0, as_stream(stream)>>>(a, span);
   else
-    kv4_append_kernel<false><<<grid, 256, 0, as_stream(stream)>>>(a);
+    kv4_append_kernel<false><<<blocks, 32 * KV4_APPEND_WARPS, 0, as_stream(stream)>>>(a, span);
   return launch_status();
 }
 
@@ -375,15 +374,14 @@ extern "C" awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const i
   if (!dtype_ok(dtype)) return AWQ_ERR_INVALID_ARG;
   if (T == 0 || (!k && !v)) return AWQ_OK;
   if (!slots || !aligned(slots, 4) || !aligned(k, 16) || !aligned(v, 16)) return AWQ_ERR_INVALID_ARG;
-  int sms = 0;
-  if ((st = check_device(&sms)) != AWQ_OK) return st;
+  if ((st = check_device(nullptr)) != AWQ_OK) return st;
   const Kv4Cache c = kv4_cache(cfg, cache, n_pages);
-  const long long blocks = cdiv(2 * T * cfg->n_kv_heads * (cfg->head_dim / 8), 256);
-  const unsigned grid = (unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms);
+  const int span = kv4_span(T);
+  const unsigned blocks = (unsigned)((T + span - 1) / span);
   if (dtype == AWQ_DTYPE_F16)
-    kv4_gather_kernel<true><<<grid, 256, 0, as_stream(stream)>>>(c, slots, (int)T, k, v);
+    kv4_gather_kernel<true><<<blocks, 32 * KV4_APPEND_WARPS, 0, as_stream(stream)>>>(c, slots, (int)T, k, v, span);
   else
-    kv4_gather_kernel<false><<<grid, 256, 0, as_stream(stream)>>>(c, slots, (int)T, k, v);
+    kv4_gather_kernel<false><<<blocks, 32 * KV4_APPEND_WARPS, 0, as_stream(stream)>>>(c, slots, (int)T, k, v, span);
   return launch_status();
 }
 
