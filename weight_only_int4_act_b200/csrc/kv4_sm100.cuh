@@ -123,9 +123,9 @@ struct Kv4AppendArgs {
   Kv4Cache c;
 };
 
-// 8 channels of a token: their codes as a word (channel i in nibble i) and the
-// group's step and zero as stored. The g / 8 lanes of a group (neighbours; all
-// lanes of a warp call this) share its extremes by shuffles: (-min, max) as a
+// 8 NC channels of a token: their codes as words (channel i of 8 in nibble i) and
+// the group's step and zero as stored. A group's lanes (neighbours; all lanes of
+// a warp call this) share its extremes by shuffles: (-min, max) as a
 // pair of the inputs' own type, whose order and sign are exact.
 template <bool F16>
 __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
@@ -136,43 +136,58 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-template <bool F16>
-__device__ __forceinline__ uint32_t kv4_quantize(const uint4& raw, int group, uint32_t& par) {
-  const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+template <bool F16, int NC>
+__device__ __forceinline__ void kv4_quantize(const uint4 (&raw)[NC], int group, uint32_t (&word)[NC], uint32_t& par) {
   uint32_t low = 0, high = 0;  // 0 is always in the range
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    low = max2_nan<F16>(low, rw[i] ^ 0x80008000u);
-    high = max2_nan<F16>(high, rw[i]);
+  for (int k = 0; k < NC; ++k) {
+    const uint32_t rw[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      low = max2_nan<F16>(low, rw[i] ^ 0x80008000u);
+      high = max2_nan<F16>(high, rw[i]);
+    }
   }
   uint32_t both = max2_nan<F16>(__byte_perm(low, high, 0x5410), __byte_perm(low, high, 0x7632));
-  for (int o = group / 16; o; o >>= 1) both = max2_nan<F16>(both, __shfl_xor_sync(0xffffffffu, both, o));
+  for (int o = group / (16 * NC); o; o >>= 1) both = max2_nan<F16>(both, __shfl_xor_sync(0xffffffffu, both, o));
   const float2 ends = widen2<F16>(both);  // (-min, max); infinite or NaN if one of the inputs is
-  if (!(fmaxf(ends.x, ends.y) <= 3.402823466e38f && ends.x + ends.y == ends.x + ends.y)) {  // step NaN, codes and zero 0
+  if (!(fabsf(ends.x) <= 3.402823466e38f && fabsf(ends.y) <= 3.402823466e38f)) {  // step NaN, codes and zero 0
     par = 0x00007FFFu;
-    return 0;
+#pragma unroll
+    for (int k = 0; k < NC; ++k) word[k] = 0;
+    return;
   }
   const __half step = __float2half_rn(__fdiv_rn(__fadd_rn(ends.y, ends.x), 15.0f));
   const float sf = fminf(fmaxf(__half2float(step), 5.9604644775390625e-8f), 65504.0f);
   const float inv = __frcp_rn(sf);
-  const float zf = fminf(rintf(__fmul_rn(ends.x, inv)), 15.0f);
+  // rint by a sum with 1.5 * 2^23, which has it in its low bits too. clamp(rint(v)
+  // + z, 0, 15) = rint(clamp(v, -z, 15 - z)) + z, as z is whole; and eight such
+  // sums, each four bits further up, add to the word and a known constant.
+  const float zero = __fadd_rn(fminf(__fmul_rn(ends.x, inv), 15.0f), 12582912.0f);
+  const float zf = __fsub_rn(zero, 12582912.0f), most = 15.0f - zf;
   par = (uint32_t)__half_as_ushort(__float2half_rn(sf)) | (uint32_t)__half_as_ushort(__float2half_rn(zf)) << 16;
-  // clamp(rint(v) + z, 0, 15) = rint(clamp(v, -z, 15 - z)) + z: z is whole. The
-  // sum with 1.5 * 2^23 has rint(v) in its low bits; eight of them, each four
-  // bits further up, add to the word and to a known constant.
-  const float most = 15.0f - zf;
-  uint32_t word = (uint32_t)(int)zf * 0x11111111u - 0x4B400000u * 0x11111111u;
+  const uint32_t start = (__float_as_uint(zero) - 2u * 0x4B400000u) * 0x11111111u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = widen2<F16>(rw[i]);
-    const float v0 = fminf(fmaxf(__fmul_rn(f.x, inv), -zf), most), v1 = fminf(fmaxf(__fmul_rn(f.y, inv), -zf), most);
-    word += __float_as_uint(__fadd_rn(v0, 12582912.0f)) << (8 * i);
-    word += __float_as_uint(__fadd_rn(v1, 12582912.0f)) << (8 * i + 4);
+  for (int k = 0; k < NC; ++k) {
+    const uint32_t rw[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+    uint32_t w = start;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = widen2<F16>(rw[i]);
+      const float v0 = fminf(fmaxf(__fmul_rn(f.x, inv), -zf), most), v1 = fminf(fmaxf(__fmul_rn(f.y, inv), -zf), most);
+      w += __float_as_uint(__fadd_rn(v0, 12582912.0f)) << (8 * i);
+      w += __float_as_uint(__fadd_rn(v1, 12582912.0f)) << (8 * i + 4);
+    }
+    word[k] = w;
   }
-  return word;
 }
 
-// Bound by HBM and, nearly as much, by the quantiser's instructions for prompts.
+// 16411 tokens of 8 heads of 128 in groups of 32, fp16: 29 us for 67 MB read and
+// 21 written (13.5 at a copy's rate); 64 single tokens 2.5 us, a launch. A token at
+// a time took 74 us: bytes of the value words written one by one, a rint, a
+// conversion and two divisions' worth of slow instructions for every 8 channels
+// (16 now), a block a token. Issue slots and the loads of eight warps a block, each
+// one pass behind the other, share the rest about equally.
 template <bool F16>
 __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS) kv4_append_kernel(const Kv4AppendArgs a, const int span) {
   __shared__ uint32_t codes[KV4_APPEND_WARPS][16][33];  // a strip's value codes, a word a chunk; padded rows
@@ -192,9 +207,10 @@ __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS) kv4_append_kernel(const
       const int w = live ? (val ? u - half : u) : 0, head = w / chunks, ch = w - head * chunks;
       const uint16_t* src = (val ? a.v + (long long)tok * a.v_tok + (long long)head * a.v_head
                                  : a.k + (long long)tok * a.k_tok + (long long)head * a.k_head) + 8 * ch;
-      const uint4 raw = live ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
-      uint32_t par;
-      const uint32_t word = kv4_quantize<F16>(raw, a.c.group, par);
+      const uint4 raw[1] = {live ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0)};
+      uint32_t words[1], par;
+      kv4_quantize<F16>(raw, a.c.group, words, par);
+      const uint32_t word = words[0];
       const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 2);  // the 8 channels 16 away
       const long long base = a.c.strip(page, head, slot & in_mask);
       if (!live || !AWQ_SPAN_OK(base, a.c.strip_bytes, a.c.bytes(), BS_KV4_CACHE)) continue;
@@ -220,8 +236,8 @@ __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS) kv4_append_kernel(const
   const long long page = slot >> a.c.page_shift;
   if (slot < 0 || page >= a.c.n_pages) return;
   uint32_t(&cw)[16][33] = codes[warp];
-  // the warp's lanes over (token, chunk), tokens outermost: chunks of a group stay neighbours
-  const int t0 = lane / chunks, ch0 = lane - t0 * chunks, dt = 32 / chunks, dch = 32 - dt * chunks;
+  // the warp's lanes over (token, two chunks), tokens outermost: chunks of a group stay neighbours
+  const int pairs = D / 16, t0 = lane / pairs, ch0 = lane - t0 * pairs, dt = 32 / pairs, dch = 32 - dt * pairs;
   for (int head = warp; head < a.c.heads; head += KV4_APPEND_WARPS) {
     const long long base = a.c.strip(page, head, slot & in_mask);
     if (!AWQ_SPAN_OK(base, a.c.strip_bytes, a.c.bytes(), BS_KV4_CACHE)) continue;
@@ -232,30 +248,25 @@ __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS) kv4_append_kernel(const
                                 : a.k + (long long)tok * a.k_tok + (long long)head * a.k_head;
       const long long ld = val ? a.v_tok : a.k_tok;
       uint8_t* pars = s + 16 * D + (val ? 64 * ng : 0);
-      int t = t0, ch = ch0;
+      int t = t0, pair = ch0;
 #pragma unroll 1
-      for (int u0 = 0; u0 < 16 * chunks; u0 += 64) {  // two chunks a lane at a time (16 * chunks is a multiple of 64)
-        uint4 raw[2];
-        int at[2], ac[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          at[k] = t;
-          ac[k] = ch;
-          raw[k] = __ldg(reinterpret_cast<const uint4*>(src + t * ld + 8 * ch));
-          t += dt;
-          ch += dch;
-          if (ch >= chunks) ch -= chunks, ++t;
+      for (int u0 = 0; u0 < 16 * pairs; u0 += 32) {  // D / 32 turns
+        const uint4* from = reinterpret_cast<const uint4*>(src + t * ld + 16 * pair);
+        const uint4 raw[2] = {__ldg(from), __ldg(from + 1)};
+        uint32_t word[2], par;
+        kv4_quantize<F16>(raw, a.c.group, word, par);
+        if (val) {
+          cw[t][2 * pair] = word[0];
+          cw[t][2 * pair + 1] = word[1];
+        } else {
+          uint8_t* to = s + t * (D / 2) + ((2 * pair & 3) * (D / 32) + (pair >> 1)) * 4;
+          *reinterpret_cast<uint32_t*>(to) = word[0];
+          *reinterpret_cast<uint32_t*>(to + D / 8) = word[1];
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t par;
-          const uint32_t word = kv4_quantize<F16>(raw[k], a.c.group, par);
-          if (val)
-            cw[at[k]][ac[k]] = word;
-          else
-            *reinterpret_cast<uint32_t*>(s + at[k] * (D / 2) + ((ac[k] & 3) * (D / 32) + (ac[k] >> 2)) * 4) = word;
-          if ((ac[k] & (per - 1)) == 0) *reinterpret_cast<uint32_t*>(pars + (ac[k] >> per_bits) * 64 + 4 * at[k]) = par;
-        }
+        if ((2 * pair & (per - 1)) == 0) *reinterpret_cast<uint32_t*>(pars + (2 * pair >> per_bits) * 64 + 4 * t) = par;
+        t += dt;
+        pair += dch;
+        if (pair >= pairs) pair -= pairs, ++t;
       }
     }
     __syncwarp();
@@ -273,7 +284,8 @@ __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS) kv4_append_kernel(const
 }
 
 // (code - zero) * step of tokens of the cache, dense; slots outside it give
-// zeros. Blocks, strips and warps as in the write.
+// zeros. Blocks, strips and warps as in the write. The same 16411 tokens: 25 us
+// (45 a token at a time; 13.5 at a copy's rate), waiting for the strips' words.
 template <bool F16>
 __device__ __forceinline__ uint4 kv4_values(uint32_t word, uint32_t par) {
   const float2 f = widen2<true>(par);  // (step, zero)
