@@ -50,7 +50,7 @@ def four_bit(x, g):
         hi = np.maximum(v.max(axis=-1), F32(0))
         step = np.clip(((hi - lo) / F32(15)).astype(np.float16).astype(F32), F32(2.0 ** -24), F32(65504))
         inv = (F32(1) / step).astype(F32)
-        zero = np.clip(np.rint(-lo * inv), 0, 15)
+        zero = np.clip(np.rint(-lo * inv), 0, 15) + F32(0)  # +0, not -0
         code = np.clip(np.rint(v * inv[..., None]) + zero[..., None], 0, 15)
     code[bad] = 0
     zero[bad] = 0

@@ -86,6 +86,65 @@ def test_append_byte_for_byte(dim, group, dtype):
         assert torch.equal(y.cpu(), ref)
 
 
+def _awkward(x, seed):
+    """Some groups' worth of x replaced by infinities, NaN, zeros, the least and the largest values."""
+    g = torch.Generator().manual_seed(seed)
+    flat, f = x.view(-1), torch.finfo(x.dtype)
+    for v in (float("inf"), -float("inf"), float("nan"), 0.0, -0.0, f.max, f.min, f.tiny, f.tiny * f.eps, -f.tiny):
+        at = torch.randint(0, flat.numel(), (3,), generator=g)
+        flat[at.cuda()] = v
+    x[0], x[-1, :, ::2] = 0, -0.0
+    return x
+
+
+def _runs(T, page, pages, seed):
+    """T slots: runs of following tokens that begin and end anywhere, some backwards, some outside the cache."""
+    r = np.random.default_rng(seed)
+    at, out = list(r.permutation(pages * page // 64) * 64), []
+    while len(out) < T:
+        base, skip, n = int(at.pop()), int(r.integers(0, 20)), int(r.integers(1, 45))
+        run = np.arange(base + skip, base + skip + n)
+        kind = r.integers(0, 8)
+        if kind == 0:
+            run = run[::-1]
+        elif kind == 1:
+            run = run + pages * page * 3
+        elif kind == 2:
+            run = run - 64 * (pages * page // 64 + 2)
+        elif kind == 3:
+            run = run[:1]
+        out += list(run)
+    return np.array(out[:T], dtype=np.int32)
+
+
+@pytest.mark.parametrize("T,dim,group,page,dtype", [(500, 64, 32, 16, "bf16"), (1024, 128, 128, 64, "f16"),
+                                                    (1025, 96, 32, 32, "bf16"), (1300, 128, 32, 16, "f16"),
+                                                    (1100, 256, 64, 256, "bf16"), (1040, 64, 64, 128, "f16")])
+def test_append_runs_of_tokens(T, dim, group, page, dtype):
+    """Runs of following slots (whole strips are taken together), broken, reversed and partly outside; awkward values."""
+    heads, pages = 3, 12800 // page
+    cfg = awq.make_kv4(heads, dim, page, group)
+    cache = awq.kv4_new_cache(pages, cfg)
+    cache.random_(-2 ** 31, 2 ** 31 - 1, generator=torch.Generator(device="cuda").manual_seed(2))
+    want = _bytes(cache).copy()
+    k, v = (_awkward(_rand((T, heads + 1, dim), dtype, T + i, 3.0), i)[:, 1:] for i in (0, 1))
+    slots = _runs(T, page, pages, T)
+    awq.kv4_append(k, v, torch.from_numpy(slots).cuda(), cache, cfg)
+    for kind, x in ((0, k), (1, v)):
+        code, step, zero = S.four_bit(_f64(x), group)
+        for t in range(T):
+            if 0 <= slots[t] < pages * page:
+                for h in range(heads):
+                    S.write_token(want, int(slots[t]), h, page, dim, group, kind, code[t, h], step[t, h], zero[t, h])
+    assert np.array_equal(_bytes(cache), want)
+    back = awq.kv4_gather(cache, torch.from_numpy(slots).cuda(), cfg, dtype=DT[dtype])
+    out = torch.from_numpy((slots < 0) | (slots >= pages * page))
+    for x, y in ((k, back[0]), (v, back[1])):
+        ref = torch.from_numpy(S.four_bit_values(*S.four_bit(_f64(x), group))).to(DT[dtype])
+        ref[out] = 0
+        assert torch.equal(torch.nan_to_num(y.cpu(), nan=-77.0), torch.nan_to_num(ref, nan=-77.0))
+
+
 def _fill(lens, heads, dim, group, page, dtype, seed, kscale=1.0, vscale=1.0, spare=2, scale_k=None):
     """A cache with shuffled pages: (cfg, cache, table, lens, k, v as written)."""
     g = torch.Generator().manual_seed(seed)
@@ -412,6 +471,58 @@ def test_python_refusals():
         awq.kv4_append(q[:, :2], q[:, 2:], torch.zeros(2, dtype=torch.int64, device="cuda"), cache, cfg)
     with pytest.raises(ValueError, match="one dtype"):
         awq.kv4_append(q[:, :2], q[:, 2:].half(), torch.zeros(2, dtype=torch.int32, device="cuda"), cache, cfg)
+
+
+@pytest.mark.parametrize("lens", [[(7 * i) % 41 for i in range(700)], [3000 if i in (100, 650) else 5 for i in range(1100)]])
+def test_more_sequences_than_a_launch(lens):
+    """Batches above one launch's plan; with and without row starts, and contexts of no tokens."""
+    _run(lens, [1 if n else 0 for n in lens], 2, 3, 64, 32, 16, "bf16", 120)
+    cfg, cache, table, lens_t, slots = _fill(lens, 2, 64, 32, 16, "bf16", 121)
+    q = _rand((len(lens), 6, 64), "bf16", 122, 2.0)
+    out, lse = awq.kv4_attention(q, cache, table, lens_t, cfg, lse=True)
+    _check(out, lse, q, cfg, _read(cache, cfg, slots), lens, range(len(lens) + 1), 3, 64 ** -0.5, "bf16")
+
+
+def test_cache_beyond_32_bits():
+    """The last pages of a cache of more than 2^32 bytes: written, read and attended as those of a small one."""
+    heads, dim, page, group, pages = 32, 256, 256, 128, 2000
+    cfg = awq.make_kv4(heads, dim, page, group)
+    big, small = awq.kv4_new_cache(pages, cfg), awq.kv4_new_cache(4, cfg)
+    assert big.numel() * 4 > 2 ** 32
+    where = [pages - 1, 3, pages - 3, 1000]
+    n = 4 * page - 37
+    k, v, q = _rand((n, heads, dim), "bf16", 1), _rand((n, heads, dim), "bf16", 2), _rand((1, heads, dim), "bf16", 3)
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    results = []
+    for cache, ids in ((big, where), (small, [2, 0, 3, 1])):
+        slots = torch.tensor([ids[i // page] * page + i % page for i in range(n)], dtype=torch.int32).cuda()
+        awq.kv4_append(k, v, slots, cache, cfg)
+        table = torch.tensor([ids], dtype=torch.int32).cuda()
+        results.append((*awq.kv4_gather(cache, slots, cfg), awq.kv4_attention(q, cache, table, lens, cfg)))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert results[0][0].any()
+    assert not big[[0, 1, 2, 4, 999, 1001, pages - 2]].any()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, over one cache; a prompt and single tokens."""
+    cfg, cache, table, lens, slots = _fill([900, 2300, 700], 4, 128, 128, 64, "bf16", 130)
+    one, many = _rand((3, 16, 128), "bf16", 131), _rand((600, 16, 128), "bf16", 132)
+    start = torch.tensor([0, 200, 400, 600], dtype=torch.int32).cuda()
+    want = (awq.kv4_attention(one, cache, table, lens, cfg),
+            awq.kv4_attention(many, cache, table, lens, cfg, q_start=start, max_q=200))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        with torch.cuda.stream(streams[0]):
+            got[0].append(awq.kv4_attention(one, cache, table, lens, cfg))
+        with torch.cuda.stream(streams[1]):
+            got[1].append(awq.kv4_attention(many, cache, table, lens, cfg, q_start=start, max_q=200))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
 
 
 def test_decode_step_captured_and_replayed():

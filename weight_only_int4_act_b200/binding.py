@@ -185,6 +185,7 @@ def _check(status: int, what: str):
         raise AwqError(status, what)
 
 
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -474,17 +475,19 @@ def _req_here(t, dtype, shape, dev, name):
 
 def _req_rows(t, dtype, shape, dev, name):
     """A tensor of device dev whose last axis is contiguous; the others may be strided."""
-    if not isinstance(t, _torch_names()[0]):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if not (isinstance(t, _torch_names()[0]) and t.dtype is dtype and t.get_device() == dev and t.shape == shape):
+        if not isinstance(t, _torch_names()[0]):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+            raise ValueError(
+                f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, got {tuple(t.shape)}")
+        _same_device(t, dev, name)
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    _same_device(t, dev, name)
 
 
 def _code(dtype, codes, name):
@@ -508,8 +511,8 @@ def quantize_int8(X, s=None, inverse=False, outputs=None):
     torch = _torch()
     dev, stream, codes = _here(X, "X")
     dt = _code(X.dtype, codes, "X")
-    _req_rows(X, X.dtype, (None, None), dev, "X")
-    rows, d_in = X.shape
+    rows, d_in = X.shape if X.dim() == 2 else (None, None)
+    _req_rows(X, X.dtype, (rows, d_in), dev, "X")
     mode = 0
     if s is not None:
         _req_here(s, torch.float32, (d_in,), dev, "s")
@@ -660,8 +663,8 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
     torch = _torch()
     dev, stream, codes = _here(q, "q")
     dt = _code(q.dtype, codes, "q")
-    _req_rows(q, q.dtype, (None, None, cfg.head_dim), dev, "q")
-    T, n_q_heads, D = q.shape
+    T, n_q_heads, D = q.shape if q.dim() == 3 else (None, None, None)
+    _req_rows(q, q.dtype, (T, n_q_heads, cfg.head_dim), dev, "q")
     _req_cache(cache, cfg, dev)
     _req_here(lens, torch.int32, None, dev, "lens")
     _req_here(table, torch.int32, None, dev, "table")

@@ -15,11 +15,9 @@
 // strip at a time. Keys the same, the strip's power of two going into the
 // factor of its scores; but for fp16 queries (EXACT; one group a head), whose
 // output resolves it, the codes less zeros (-15 .. 15) are the keys, exactly, and
-// each score is multiplied by its token's step in fp32. (Steps of both kinds
-// applied to scores and weights in fp32 cost a shared-memory load of 16 bytes
-// for every two tokens and thread, and shared memory, which also feeds the
-// MMAs, was what bound the kernel: 470 us at 2 x 2048 queries of 8000 tokens,
-// 32 over 8 heads of 128.)
+// each score is multiplied by its token's step in fp32 (2 x 2048 queries of 8000
+// tokens, 32 heads over 8 of 128, bf16: 474 us that way, 444 with folded keys; one
+// read of a step from shared memory a score, beside the MMAs' operands).
 // A token one of whose groups holds NaN turns the rows that see it to NaN.
 //
 // Warps (15): 0 loads packed strips (cp.async.bulk), 1 and 14 issue the MMAs of

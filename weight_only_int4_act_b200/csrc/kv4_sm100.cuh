@@ -152,7 +152,7 @@ __device__ __forceinline__ void kv4_quantize(const uint4 (&raw)[NC], int group, 
   for (int o = group / (16 * NC); o; o >>= 1) both = max2_nan<F16>(both, __shfl_xor_sync(0xffffffffu, both, o));
   const float2 ends = widen2<F16>(both);  // (-min, max); infinite or NaN if one of the inputs is
   if (!(fabsf(ends.x) <= 3.402823466e38f && fabsf(ends.y) <= 3.402823466e38f)) {  // step NaN, codes and zero 0
-    par = 0x00007FFFu;
+    par = 0x00007E00u;
 #pragma unroll
     for (int k = 0; k < NC; ++k) word[k] = 0;
     return;

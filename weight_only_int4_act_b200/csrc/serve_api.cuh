@@ -177,16 +177,11 @@ awq_status check_kv4_attention(int64_t batch, int64_t n_q_heads, int64_t max_q, 
 
 // Contexts of at most this many tokens (as the page tables bound them) are not
 // split between blocks, if the tables are small enough for one warp to check.
-#ifndef KV4_SOLO
-#define KV4_SOLO 2048
-#endif
-constexpr int64_t KV4_SOLO_TOKENS = KV4_SOLO, KV4_SOLO_PAGES = 4096;
+constexpr int64_t KV4_SOLO_TOKENS = 2048, KV4_SOLO_PAGES = 4096;
 
 // The prompt kernel takes the sequences of more than KVP_MIN_ROWS rows where it
 // has blocks for a good part of the SMs; else all go to the split kernel.
-#ifndef KVP_CTAS
-#define KVP_CTAS 40
-#endif
+constexpr int64_t KVP_CTAS = 40;
 bool kvp_used(int64_t batch, int64_t share, int64_t max_q, const awq_kv4cfg* c, bool f16) {
   // (fp16 with several groups a head would be rounded more than its output resolves)
   return c->head_dim <= 128 && (!f16 || c->head_dim == c->group) && max_q * share > KVP_MIN_ROWS &&
