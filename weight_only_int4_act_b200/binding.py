@@ -442,7 +442,7 @@ def _torch_names():
     """(Tensor, current_device, raw stream of a device, 16-bit types by code) of torch."""
     torch = _torch()
     torch.cuda.init()
-    return (torch.Tensor, torch.cuda.current_device, torch._C._cuda_getCurrentRawStream,
+    return (torch.Tensor, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
             {torch.bfloat16: AWQ_DTYPE_BF16, torch.float16: AWQ_DTYPE_F16})
 
 
@@ -501,6 +501,12 @@ def _scratch(like, nbytes):
     return like.new_empty(max(nbytes, 256), dtype=_torch().uint8)
 
 
+@functools.lru_cache(maxsize=None)
+def _unread(dev):
+    """An error word for calls that have no workspace of their own, where the workspace is nothing else: nobody reads it."""
+    return _torch().empty(1024, dtype=_torch().uint8, device=f"cuda:{dev}")
+
+
 # --------------------------------------------------------------------------- 8-bit integer linear layer
 def quantize_int8(X, s=None, inverse=False, outputs=None):
     """Codes int8 [rows, d_in] and steps float32 [rows] of the symmetric 8-bit
@@ -518,7 +524,7 @@ def quantize_int8(X, s=None, inverse=False, outputs=None):
         _req_here(s, torch.float32, (d_in,), dev, "s")
         mode = 2 if inverse else 1
     if outputs is None:
-        q = X.new_empty((rows, d_in), dtype=torch.int8)
+        q = torch.empty_strided((rows, d_in), (d_in, 1), dtype=torch.int8, device=X.device)
         step = X.new_empty(rows, dtype=torch.float32)
     else:
         q, step = outputs
@@ -554,12 +560,12 @@ def w8a8_gemm(xq, x_step, wq, w_step, dtype=None, bias=None, ws=None, out=None):
         _req_here(bias, torch.float32, (d_out,), dev, "bias")
     if out is None:
         dt = _code(dtype or torch.bfloat16, codes, "out")
-        out = xq.new_empty((N, d_out), dtype=dtype or torch.bfloat16)
+        out = torch.empty_strided((N, d_out), (d_out, 1), dtype=dtype or torch.bfloat16, device=xq.device)
     else:
         _req_here(out, dtype or out.dtype, (N, d_out), dev, "out")
         dt = _code(out.dtype, codes, "out")
     if ws is None:
-        ws = _scratch(xq, w8a8_workspace_size(N, d_out, d_in))
+        ws = _unread(dev)
     else:
         _same_device(ws, dev, "ws")
     st = lib().awq_w8a8_gemm(xq.data_ptr(), x_step.data_ptr(), wq.data_ptr(), w_step.data_ptr(),
@@ -629,7 +635,8 @@ def kv4_gather(cache, slots, cfg: Kv4Cfg, dtype=None, outputs=None):
     if outputs is None:
         dtype = dtype or _torch().bfloat16
         dt = _code(dtype, codes, "k")
-        k, v = cache.new_empty(shape, dtype=dtype), cache.new_empty(shape, dtype=dtype)
+        strides = (shape[1] * shape[2], shape[2], 1)
+        k, v = (_torch().empty_strided(shape, strides, dtype=dtype, device=cache.device) for _ in range(2))
     else:
         k, v = outputs
         dt = _code(dtype or k.dtype, codes, "k")
@@ -679,7 +686,7 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
         raise ValueError("without q_start, q must have one row a sequence")
     max_q = 1 if max_q is None else int(max_q)
     if out is None:
-        out = q.new_empty((T, n_q_heads, D))
+        out = torch.empty_strided((T, n_q_heads, D), (n_q_heads * D, D, 1), dtype=q.dtype, device=q.device)
     else:
         _req_here(out, q.dtype, (T, n_q_heads, D), dev, "out")
     lse_t = q.new_empty((T, n_q_heads), dtype=torch.float32) if lse else None
