@@ -946,18 +946,15 @@ struct Kv4Plan {
 __device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, longlong2* warp_sums) {
   const Kv4AttnArgs& a = s.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  if (threadIdx.x == 0) {
-    p.count[0] = p.real[0] = 0;
-    p.bad = 0;
-  }
-  __syncthreads();
+  if (threadIdx.x == 0) p.count[0] = p.real[0] = 0;
   long long count0 = 0, real0 = 0;
+  bool bad = false;
   for (int b0 = 0; b0 < a.batch; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
     long long count = 0, real = 0;
     if (b < a.batch) {
       const Kv4Seq q = kv4_seq(a, b);
-      if (q.bad) p.bad = 1;
+      bad |= q.bad;
       const int rows = q.n * a.share;
       // a sequence without context still has its rows to write: one unit, which reads nothing
       const int span = q.n > 0 && rows <= s.max_rows ? max(1, (int)(((long long)q.L + KV4_UNIT - 1) / KV4_UNIT)) : 0;
@@ -971,21 +968,23 @@ __device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, long
       real = all * span;
       count = real + all * (span ? KV4_EDGE : 0);
     }
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
+#pragma unroll 1
+    for (int d = 1; d < min(32, a.batch); d <<= 1) {  // (what lies behind the batch is 0)
       const long long x = __shfl_up_sync(0xffffffffu, count, d), y = __shfl_up_sync(0xffffffffu, real, d);
       if (lane >= d) {
         count += x;
         real += y;
       }
     }
-    if (lane == 31) warp_sums[warp] = make_longlong2(count, real);
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-      count += warp_sums[w].x;
-      real += warp_sums[w].y;
+    if (a.batch > 32) {
+      if (lane == 31) warp_sums[warp] = make_longlong2(count, real);
+      __syncthreads();
     }
     if (b < a.batch) {
+      for (int w = 0; w < warp; ++w) {
+        count += warp_sums[w].x;
+        real += warp_sums[w].y;
+      }
       p.count[b + 1] = count0 + count;
       p.real[b + 1] = real0 + real;
     }
@@ -997,7 +996,8 @@ __device__ __forceinline__ void kv4_plan(const Kv4SplitArgs& s, Kv4Plan& p, long
       __syncthreads();
     }
   }
-  __syncthreads();
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) p.bad = any;
 }
 
 // A place in the order of units.
@@ -1051,31 +1051,36 @@ struct Kv4Cursor {
   }
 };
 
-// The range of working warp w (of W) of this block: its first unit in cur, returns their number.
-__device__ __forceinline__ int kv4_range(const Kv4SplitArgs& s, const Kv4Plan& p, int w, int W, Kv4Cursor& cur) {
+// all * i / n, i <= n <= 256
+__device__ __forceinline__ long long kv4_share(long long all, int i, int n) {
+  // (a 64-bit quotient takes some 200 cycles)
+  return all < (1 << 24) ? (long long)((unsigned)all * (unsigned)i / (unsigned)n) : all * i / n;
+}
+
+// The ranges of the W working warps of this block, found by the producer warp:
+// lane w gets the first unit and the number of units of working warp w.
+__device__ __forceinline__ int kv4_ranges(const Kv4SplitArgs& s, const Kv4Plan& p, int W, int lane, Kv4Cursor& cur) {
   const int batch = s.a.batch;
   // Where there are fewer counted units than takers, the last takers get none,
   // so that the parts of a tile always are with neighbours.
-  const long long all = p.count[batch], blocks = min((long long)gridDim.x, all), c = blockIdx.x;
+  const long long all = p.count[batch];
+  const int blocks = (int)min((long long)gridDim.x, all), c = blockIdx.x;
   if (c >= blocks) return 0;
-  long long c0 = all * c / blocks, c1 = all * (c + 1) / blocks;
-  if (s.solo) {  // up to the begin of a tile
-    Kv4Cursor e;
-    if (c0 < all)
-      if (const int off = e.seek(p, batch, c0)) c0 += e.span + KV4_EDGE - off;
-    if (c1 < all)
-      if (const int off = e.seek(p, batch, c1)) c1 += e.span + KV4_EDGE - off;
+  long long mine = kv4_share(all, c + (lane & 1), blocks);  // even lanes: the block's begin, odd ones: its end
+  if (s.solo && mine < all)                                // up to the begin of a tile
+    if (const int off = cur.seek(p, batch, mine)) mine += cur.span + KV4_EDGE - off;
+  const long long c0 = __shfl_sync(0xffffffffu, mine, 0), c1 = __shfl_sync(0xffffffffu, mine, 1);
+  const int warps = (int)min((long long)W, c1 - c0);
+  long long at = p.real[batch];
+  if (lane <= warps) {
+    const long long u = c0 + (warps ? kv4_share(c1 - c0, lane, warps) : 0);
+    if (u < all) {
+      cur.seek(p, batch, u);
+      at = cur.index(p);
+    }
   }
-  const long long warps = min((long long)W, c1 - c0);
-  if (w >= warps) return 0;
-  const long long u0 = c0 + (c1 - c0) * w / warps, u1 = c0 + (c1 - c0) * (w + 1) / warps;
-  long long end = p.real[batch];
-  if (u1 < all) {
-    cur.seek(p, batch, u1);
-    end = cur.index(p);
-  }
-  cur.seek(p, batch, u0);
-  return (int)(end - cur.index(p));
+  const long long next = __shfl_down_sync(0xffffffffu, at, 1);
+  return lane < warps ? (int)(next - at) : 0;
 }
 
 // Query row r (in the sequence's n * share) of a kv head: its row in out and lse; -1 if there is none.
@@ -1174,6 +1179,8 @@ struct Kv4SplitSmem {
   uint64_t empty[W][STAGES];
   Kv4Plan plan;
   longlong2 sums[W + 1];
+  Kv4Cursor begin[W];    // a working warp's first unit
+  int units[W];          // and how many it has
   long long seg[W][2];   // tile of a warp's first and last part (-1: none)
   int flags[W][2];       // bit 0: the part begins its tile, bit 1: it ends it
   uint8_t lost[W][4];    // strips of a stage's unit that are not there to be read (by bit)
@@ -1188,8 +1195,12 @@ __device__ __forceinline__ void kv4_produce(const Kv4SplitArgs& s, Kv4SplitSmem<
   constexpr int W = Sm::W, STAGES = Sm::STAGES, STRIP = Sm::STRIP;
   const Kv4AttnArgs& a = s.a;
   Kv4Cursor cur{};
-  int left = lane < W ? kv4_range(s, sm.plan, lane, W, cur) : 0;
-  int stage = 0, sent = 0;
+  int left = kv4_ranges(s, sm.plan, W, lane, cur), stage = 0, sent = 0;
+  if (lane < W) {
+    sm.begin[lane] = cur;
+    sm.units[lane] = left;
+  }
+  __syncthreads();  // (the working warps are there for it at once)
   uint32_t phase = 1;  // a fresh ring is empty
   int page[2] = {-1, -1};
   // pages of 16 tokens hold one strip of the unit each, larger ones both, one behind the other
@@ -1299,8 +1310,9 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
       if (lane == 0 && (s.clear_err || bad)) *a.err = bad;
     }
   } else {
-    Kv4Cursor cur;
-    int left = kv4_range(s, sm.plan, warp, W, cur), stage = 0;
+    __syncthreads();
+    Kv4Cursor cur = sm.begin[warp];
+    int left = sm.units[warp], stage = 0;
     uint32_t phase = 0;
     bool fresh_tile = true, first = true, begins = cur.at == 0;
     St w;
