@@ -675,7 +675,8 @@ def run_ours(args, rank, world, local_rank):
 
 
 # ----------------------------------------------------------------------------- one entry point alone
-ONLY = ("stats", "pack", "fake_quant", "gram", "contract", "group_clip", "fold", "per_tensor", "segmented", "w4a16")
+ONLY = ("stats", "pack", "fake_quant", "gram", "contract", "group_clip", "fold", "per_tensor", "segmented", "w4a16",
+        "w8a8")
 
 
 def run_only(args):
@@ -706,7 +707,7 @@ def run_only(args):
     def bf16(bits):
         return torch.from_numpy(bits.view(np.int16)).view(torch.bfloat16).to(dev)
 
-    tokens = args.tokens if what == "w4a16" else N
+    tokens = args.tokens if what in ("w4a16", "w8a8") else N
     W = bf16(gen.make_weight(wl.seed, d_out, d_in, wl.w_std))
     X = bf16(gen.make_activations(wl.seed, tokens, d_in, wl.x_kind, wl.x_lognormal_sigma, wl.outlier_count,
                                   wl.outlier_factor))
@@ -802,6 +803,23 @@ def run_only(args):
         flops = 2.0 * tokens * d_out * d_in
         kernels = ["w4a16_gemm_tcgen05", "w4a16_streamk_reduce"]
         note = f"{tokens} tokens, {args.dtype} activations, W packed at s = 1"
+    elif what == "w8a8":
+        dt = torch.float16 if args.dtype == "f16" else torch.bfloat16
+        wq, w_step = awq.quantize_int8(W, s)
+        Xd = X.to(dt).contiguous()
+        xq, x_step = awq.quantize_int8(Xd, s, inverse=True)
+        ws8 = awq.workspace(awq.w8a8_workspace_size(tokens, d_out, d_in))
+        Y = torch.empty((tokens, d_out), dtype=dt, device=dev)
+        keep += [wq, w_step, Xd, xq, x_step, ws8, Y]
+        err_ws.append(ws8)
+
+        def fn():
+            awq.quantize_int8(Xd, s, inverse=True, outputs=(xq, x_step))
+            awq.w8a8_gemm(xq, x_step, wq, w_step, ws=ws8, out=Y)
+        byts = d_out * d_in + 4 * d_out + tokens * (2 * d_in + 2 * d_out) + 4 * d_in
+        flops = 2.0 * tokens * d_out * d_in
+        kernels = ["quantize_int8_rows", "w8a8_small_tcgen05 or w8a8_gemm(_pair)_tcgen05"]
+        note = f"{tokens} tokens, {args.dtype} activations quantised in the call, W S quantised once"
     else:
         raise SystemExit(f"unknown --only {what}")
 
@@ -831,7 +849,8 @@ def run_only(args):
         line["algorithmic_bytes"] = int(byts)
     if flops is not None:
         line["tflops"] = round(flops / (t * 1e-3) / 1e12, 2)
-        line["tensor_frac"] = round(flops / (t * 1e-3) / 1e12 / peaks.get("bf16_tflops", FALLBACK_PEAKS["bf16_tflops"]), 4)
+        peak = peaks.get("bf16_tflops", FALLBACK_PEAKS["bf16_tflops"]) * (2 if what == "w8a8" else 1)  # 8-bit: twice bf16
+        line["tensor_frac"] = round(flops / (t * 1e-3) / 1e12 / peak, 4)
         line["flops"] = flops
     if note:
         line["note"] = note
@@ -970,8 +989,8 @@ def main():
     ap.add_argument("--no-w4a16", action="store_true", help="skip the W4A16 inference-side timing")
     ap.add_argument("--no-graph", action="store_true", help="time the eager public calls only")
     ap.add_argument("--only", default=None, choices=ONLY, help="time one entry point alone (its own JSON line)")
-    ap.add_argument("--tokens", type=int, default=16, help="tokens for --only w4a16")
-    ap.add_argument("--dtype", default="f16", choices=["f16", "bf16"], help="activations for --only w4a16")
+    ap.add_argument("--tokens", type=int, default=16, help="tokens for --only w4a16 and w8a8")
+    ap.add_argument("--dtype", default="f16", choices=["f16", "bf16"], help="activations for --only w4a16 and w8a8")
     ap.add_argument("--json-out", default=None, help="also write the JSON line to this file")
     ap.add_argument("--seed", type=int, default=None,
                     help="seed of the synthetic inputs (default: the workload's own; parity then has no stored run)")

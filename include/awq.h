@@ -330,8 +330,8 @@ awq_status awq_quantize_int8(const void* x, awq_dtype dtype, int64_t ldx, const 
  * xq: DEVICE int8 [N, d_in], wq: DEVICE int8 [d_out, d_in], both 16-byte
  * aligned; x_step: float [N]; w_step: float [d_out]; bias: float [d_out] or
  * NULL; Y: DEVICE [N, d_out] bf16 or fp16, 16-byte aligned. d_in a multiple of
- * 16, at most 131072 (AWQ_ERR_SHAPE). ws: awq_w8a8_workspace_size bytes (error
- * word, and int32 partials where few tiles are split between CTAs).
+ * 16, at most 131072 (AWQ_ERR_SHAPE). ws: awq_w8a8_workspace_size bytes, the
+ * error word alone: calls whose errors are not told apart may share it.
  * Asynchronous; device-side errors land in the workspace. */
 size_t awq_w8a8_workspace_size(int64_t N, int64_t d_out, int64_t d_in);
 awq_status awq_w8a8_gemm(const int8_t* xq, const float* x_step, const int8_t* wq, const float* w_step,
@@ -365,7 +365,7 @@ size_t awq_kv4_page_bytes(const awq_kv4cfg* cfg);
  *   lo = min(0, min v), hi = max(0, max v), step = fp16((hi - lo) / 15) kept in [2^-24, 65504],
  *   inv = 1 / step, zero = rne(-lo * inv), code = clamp(rne(v * inv) + zero, 0, 15)
  * in fp32, one rounding an operation. A group that holds NaN or infinity gets
- * step NaN. k, v: DEVICE bf16 or fp16, element (t, h, d) at t * tok_stride +
+ * step NaN (0x7E00), zero and codes 0. k, v: DEVICE bf16 or fp16, element (t, h, d) at t * tok_stride +
  * h * head_stride + d (strides in elements, multiples of 8; k and v 16-byte
  * aligned), so slices of a fused projection are read in place. slots: DEVICE
  * int32 [T]: page * page_size + position; a slot outside the cache (for
@@ -399,7 +399,13 @@ awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const int32_t* slo
  * [T, n_q_heads] or NULL: the natural logarithm of the sum of exponentials.
  * max_q: at least every sequence's number of rows (host value; it chooses the
  * kernel). Scores, softmax statistics and output sums are fp32; the weights
- * (probability times value step) enter the tensor cores in fp16.
+ * (probability times value step) enter the tensor cores in fp16, and for bf16
+ * queries of more than 64 rows a sequence (tokens times query heads of a kv
+ * head) the keys and values (code - zero) * step do too, each rounded once
+ * relative to its strip's largest step; for fp16 ones the values alone. A row
+ * that sees a key with step NaN is NaN, one that sees a value with step NaN is
+ * NaN in that group's channels at least. The same call gives the same bits
+ * each time; another batch around a sequence may cut its context elsewhere.
  * Tokens in pages outside [0, n_pages) are left out, lengths are cut to
  * table_pages * page_size, and rows to max_q and T; any of these makes
  * awq_workspace_error report AWQ_ERR_DEVICE.

@@ -83,6 +83,8 @@ def test_kv4_cache_calls_refusals():
         st[i] = -128
         assert put(st=st) == ARG
     assert put(T=-1) == SHAPE and put(pages=0) == SHAPE and put(pages=(1 << 25)) == SHAPE
+    for pages in (1 << 58, 1 << 62):  # (times the page size: past 64 bits)
+        assert put(pages=pages) == SHAPE
     assert put(T=0, k=None, v=None, slots=None) == OK
 
     def get(cache=FAKE, pages=4, slots=FAKE, T=4, k=FAKE, v=FAKE, dt=1):
@@ -110,6 +112,7 @@ def test_kv4_attention_refusals():
     assert call(st=(1028, 128)) == ARG and call(st=(1024, 124)) == ARG
     assert call(heads=6) == SHAPE and call(heads=0) == SHAPE and call(batch=0) == SHAPE and call(batch=65536) == SHAPE
     assert call(max_q=0) == SHAPE and call(tp=0) == SHAPE and call(tp=1 << 26) == SHAPE and call(pages=0) == SHAPE
+    assert call(tp=1 << 58) == SHAPE and call(tp=1 << 62) == SHAPE and call(pages=1 << 62) == SHAPE
     assert call(T=2) == SHAPE and call(max_q=2) == SHAPE and call(T=-1, start=FAKE) == SHAPE
     need = awq.kv4_attention_workspace_size(3, 8, 1, cfg)
     assert need >= 1024 and call(n=need - 1) == WORKSPACE

@@ -53,7 +53,6 @@ enum BoundsSite : int {
   BS_Q8_CODES,      // quantize_int8_rows / _long: codes
   BS_Q8_STEP,       // quantize_int8_rows / _long: steps
   BS_W8_Y,          // the 8-bit integer product: Y stores
-  BS_KV4_IN,        // kv4_append_kernel: key / value rows
   BS_KV4_CACHE,     // kv4_append_kernel / kv4_gather_kernel: the cache
   BS_KV4_OUT,       // kv4_gather_kernel: dense keys / values
   BS_KV4_Q,         // 4-bit attention: query rows

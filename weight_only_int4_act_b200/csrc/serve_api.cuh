@@ -144,7 +144,7 @@ size_t kv4_head_bytes(const awq_kv4cfg* c) {
 
 awq_status check_kv4_cache(const awq_kv4cfg* c, const void* cache, int64_t n_pages) {
   if (!cache || !aligned(cache, 16)) return AWQ_ERR_INVALID_ARG;
-  if (n_pages < 1 || n_pages * c->page_size > (int64_t)INT32_MAX) return AWQ_ERR_SHAPE;
+  if (n_pages < 1 || n_pages > INT32_MAX / c->page_size) return AWQ_ERR_SHAPE;
   return AWQ_OK;
 }
 
@@ -394,7 +394,7 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   awq_status st = check_kv4_attention(batch, n_q_heads, max_q, cfg);
   if (st != AWQ_OK) return st;
   if ((st = check_kv4_cache(cfg, cache, n_pages)) != AWQ_OK) return st;
-  if (T < 0 || T > (1 << 28) || table_pages < 1 || table_pages * cfg->page_size > (int64_t)INT32_MAX)
+  if (T < 0 || T > (1 << 28) || table_pages < 1 || table_pages > INT32_MAX / cfg->page_size)
     return AWQ_ERR_SHAPE;
   if (!q_start && (T < batch || max_q != 1)) return AWQ_ERR_SHAPE;
   if (!dtype_ok(dtype) || !strides_ok(q_tok, q_head) || !std::isfinite(scale)) return AWQ_ERR_INVALID_ARG;
