@@ -20,6 +20,15 @@
 // read of a step from shared memory a score, beside the MMAs' operands).
 // A token one of whose groups holds NaN turns the rows that see it to NaN.
 //
+// Measured: 2 x 2048 queries of up to 8000 tokens, 32 heads over 8 of 128: 444 us,
+// 752 TFLOP/s (202 us at the bf16 rate). A context tile takes a block about 2200
+// cycles. Its MMAs are 1024 cycles' work and take 1560, as N = 64 costs what
+// N = 128 does (64 to 67 cycles); beside them go the exponentials of 16384 scores
+// on 8 warps and the handshakes between loader, unpacking, products and softmax,
+// about 300 cycles each. Blocks of unequal contexts on 148 SMs and their starts
+// are the rest. With context tiles of 128 tokens, whose scores have no second
+// buffer in tensor memory, 742 us.
+//
 // Warps (15): 0 loads packed strips (cp.async.bulk), 1 and 14 issue the MMAs of
 // the two row tiles (one thread for both spent as long on its handshakes as the
 // tensor cores on their work), 2..5 unpack strips into the operand tiles, 6..9
