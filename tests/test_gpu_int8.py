@@ -240,3 +240,26 @@ def test_side_stream_and_graph_replay():
         torch.cuda.synchronize()
         _check_rows(X, None, False, *outs)
         _check_product(Y, *outs, wq, ws)
+
+
+def test_short_and_long_calls_agree():
+    """Calls that leave outputs and workspace to the library (one compiled call) and calls that bring their own."""
+    X, W = _rand((37, 272), "bf16", 50), _rand((45, 272), "f16", 51)
+    s = torch.rand(272, device="cuda") + 0.5
+    work = awq.workspace(awq.w8a8_workspace_size(37, 45, 272))
+    for sc, inv in ((None, False), (s, False), (s, True)):
+        a = awq.quantize_int8(X[::2], sc, inverse=inv)
+        b = awq.quantize_int8(X[::2], sc, inverse=inv, outputs=tuple(torch.empty_like(t) for t in a))
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    x, w, bias = awq.quantize_int8(X, s, inverse=True), awq.quantize_int8(W, s), torch.randn(45, device="cuda")
+    for dt in (None, torch.bfloat16, torch.float16):
+        for bi in (None, bias):
+            a = awq.w8a8_gemm(*x, *w, dtype=dt, bias=bi)
+            out = torch.empty((37, 45), dtype=dt or torch.bfloat16, device="cuda")
+            assert a.dtype == out.dtype and torch.equal(a, awq.w8a8_gemm(*x, *w, bias=bi, ws=work, out=out))
+    with pytest.raises(ValueError):
+        awq.w8a8_gemm(*x, *w, dtype=torch.float32)
+    with pytest.raises(ValueError):
+        awq.w8a8_gemm(*x, w[0], w[1][:-1])
+    with pytest.raises(awq.AwqError, match="SHAPE"):
+        awq.quantize_int8(X[:, :200])

@@ -525,6 +525,37 @@ def test_two_streams_at_once():
         assert all(torch.equal(w, x) for x in g)
 
 
+def test_short_and_long_calls_agree():
+    """Calls that leave outputs and workspace to the library (one compiled call) and calls that bring their own."""
+    cfg, cache, table, lens, slots = _fill([300, 41, 77], 4, 128, 64, 32, "f16", 140)
+    q = _rand((3, 12, 136), "f16", 141)[:, 2:10, :128]  # strided
+    start = torch.tensor([0, 1, 1, 3], dtype=torch.int32).cuda()
+    work = awq.workspace(awq.kv4_attention_workspace_size(3, 8, 2, cfg))
+    out = torch.zeros((3, 8, 128), dtype=torch.float16, device="cuda")
+    for args in (dict(), dict(scale=0.3), dict(lse=True), dict(q_start=start, max_q=2), dict(max_q=1)):
+        a = awq.kv4_attention(q, cache, table, lens, cfg, **args)
+        b = awq.kv4_attention(q, cache, table, lens, cfg, ws=work, out=out, **args)
+        for x, y in zip(a if args.get("lse") else (a,), b if args.get("lse") else (b,)):
+            assert x.dtype == y.dtype and x.is_contiguous() and torch.equal(x, y)
+    s = torch.from_numpy(slots[:50]).int().cuda()
+    for dt in (None, torch.bfloat16, torch.float16):
+        a = awq.kv4_gather(cache, s, cfg, dtype=dt)
+        own = tuple(torch.empty((50, 4, 128), dtype=dt or torch.bfloat16, device="cuda") for _ in range(2))
+        b = awq.kv4_gather(cache, s, cfg, outputs=own)
+        assert a[0].dtype == (dt or torch.bfloat16) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    k = _rand((50, 4, 256), "bf16", 142)
+    one, two = cache.clone(), cache.clone()
+    assert awq.kv4_append(k[..., :128], k[..., 128:], s, one, cfg) is one
+    awq.kv4_append(k[..., :128].clone(), k[..., 128:].clone(), s, two, cfg)
+    assert torch.equal(one, two) and not torch.equal(one, cache)
+    with pytest.raises(awq.AwqError, match="SHAPE"):
+        awq.kv4_attention(q[:, :6], cache, table, lens, cfg)  # 6 query heads over 4
+    with pytest.raises(awq.AwqError, match="INVALID"):
+        awq.kv4_attention(q, cache, table, lens, cfg, scale=float("nan"))
+    with pytest.raises(ValueError, match="one row a sequence"):
+        awq.kv4_attention(q[:2], cache, table, lens, cfg)
+
+
 def test_decode_step_captured_and_replayed():
     """append + attend of one decode step in a graph, replayed as the contexts grow (lengths, slots and inputs change in
     place), beside a second graph with a workspace of its own."""

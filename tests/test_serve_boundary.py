@@ -131,6 +131,26 @@ def test_python_binding_refuses_cpu_tensors():
             call()
 
 
+def test_short_calls_leave_what_they_do_not_know():
+    """The compiled calls return None for arguments that the binding has to look at, and never reach the library."""
+    import torch
+    from weight_only_int4_act_b200 import binding as B
+    c = B._calls(B._active)
+    cfg = awq.make_kv4(2, 64)
+    at = ctypes.addressof(cfg)
+    x, i = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((4, 64), dtype=torch.int8)
+    for bad in (x, None, 3, "x", np.zeros(4)):
+        assert c.quantize_int8(bad, None, 1) is None and c.quantize_int8(x, bad, 1) is None
+        assert c.w8a8_gemm(i, x, i, x, bad, False, bad) is None
+        assert c.kv4_append(bad, x, i, i, at) is None and c.kv4_gather(bad, i, at, True) is None
+        assert c.kv4_attention(bad, i, i, i, at, None, None, None, False) is None
+    for f in vars(c).values():
+        with pytest.raises(TypeError):
+            f(1)
+    with pytest.raises((TypeError, ValueError)):
+        awq.quantize_int8([1.0])
+
+
 # ---------------------------------------------------------------- the oracle's own statements
 @pytest.mark.parametrize("D,g", [(64, 32), (96, 32), (128, 128), (256, 64)])
 def test_strip_layout_places_every_code_once(D, g):

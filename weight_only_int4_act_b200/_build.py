@@ -3,7 +3,9 @@
 Two builds of the same sources: "release" (lib/libawq_b200.so) and "check"
 (lib/libawq_b200_check.so, compiled with -DAWQ_BOUNDS_CHECK: every hand-
 addressed global access checks its index and records a failure in a device
-word instead of touching memory; see csrc/check.cuh).
+word instead of touching memory; see csrc/check.cuh). Beside them, by g++,
+lib/awq_calls.so: the Python module of csrc/torch_calls.cpp, which holds no
+kernels and calls whichever build is selected.
 """
 from __future__ import annotations
 
@@ -24,6 +26,9 @@ DEPS = SOURCES + [os.path.join(PKG, "csrc", f) for f in (
     "w4a16_sm100.cuh", "awq_api.cu", "serve_api.cuh", "w8a8_sm100.cuh", "kv4_sm100.cuh",
     "kv4_prompt_sm100.cuh")] + [os.path.join(ROOT, "include", "awq.h")]
 
+CALLS_PATH = os.path.join(LIB_DIR, "awq_calls.so")
+CALLS_DEPS = [os.path.join(PKG, "csrc", "torch_calls.cpp"), os.path.join(ROOT, "include", "awq.h")]
+
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -41,33 +46,54 @@ def lib_path(variant: str = "release") -> str:
 
 
 def stale(variant: str = "release") -> bool:
-    path = lib_path(variant)
+    return _older(lib_path(variant), DEPS)
+
+
+def _older(path, deps) -> bool:
     if not os.path.exists(path):
         return True
     t = os.path.getmtime(path)
-    return any(os.path.getmtime(p) > t for p in DEPS)
+    return any(os.path.getmtime(p) > t for p in deps)
+
+
+def calls_command(out: str) -> list:
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    include = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"), cuda]
+    return ["g++", "-O2", "-std=c++20", "-shared", "-fPIC",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + i for i in include), "-o", out,
+            CALLS_DEPS[0], "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+            "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False, variants=("release",)) -> str:
-    """Build the given variants if missing or older than their sources (nvcc
-    runs for all of them at once). Returns the path of the first."""
+    """Build the given variants and the calls' module if missing or older than
+    their sources (the compilers run for all of them at once). Returns the path of the first."""
     os.makedirs(LIB_DIR, exist_ok=True)
     jobs = []
+
+    def start(path, command):
+        cmd = command(path + ".tmp")
+        jobs.append((path, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+
     for v in variants:
-        if not force and not stale(v):
-            continue
-        tmp = lib_path(v) + ".tmp"
-        cmd = [nvcc(), *NVCC_FLAGS, *VARIANTS[v][1], "-o", tmp, *SOURCES]
-        jobs.append((v, tmp, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+        if force or stale(v):
+            start(lib_path(v), lambda out, v=v: [nvcc(), *NVCC_FLAGS, *VARIANTS[v][1], "-o", out, *SOURCES])
+    if force or _older(CALLS_PATH, CALLS_DEPS):
+        start(CALLS_PATH, calls_command)
     failed = []
-    for v, tmp, cmd, proc in jobs:
+    for path, cmd, proc in jobs:
         out, _ = proc.communicate()
         if proc.returncode != 0:
-            failed.append("nvcc failed:\n" + " ".join(cmd) + "\n" + out)
+            failed.append(os.path.basename(cmd[0]) + " failed:\n" + " ".join(cmd) + "\n" + out)
             continue
         if verbose:
             print(out)
-        os.replace(tmp, lib_path(v))
+        os.replace(path + ".tmp", path)
     if failed:
         raise RuntimeError("\n".join(failed))
     return lib_path(variants[0])

@@ -16,7 +16,7 @@ import functools
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
 
-from ._build import VARIANTS, lib_path
+from ._build import CALLS_PATH, VARIANTS, lib_path
 
 AWQ_OK = 0
 STATUS_NAMES = {
@@ -502,6 +502,29 @@ def _scratch(like, nbytes):
 
 
 @functools.lru_cache(maxsize=None)
+def _calls(variant):
+    """The serving calls of lib/awq_calls.so on a build of the library. Each
+    returns its results, a status, or None for arguments that the functions
+    below have to look at."""
+    import importlib.machinery
+    import importlib.util
+    import types
+    _torch()  # whose libraries the module needs
+    if not os.path.exists(CALLS_PATH):
+        raise RuntimeError(f"{CALLS_PATH} is missing; build it with __graft_entry__.build()")
+    loader = importlib.machinery.ExtensionFileLoader("awq_calls", CALLS_PATH)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader("awq_calls", loader))
+    loader.exec_module(m)
+    L = lib()
+    at = lambda name: ctypes.cast(getattr(L, name), c_void_p).value  # noqa: E731
+    p = functools.partial
+    return types.SimpleNamespace(
+        quantize_int8=p(m.quantize_int8, at("awq_quantize_int8")), w8a8_gemm=p(m.w8a8_gemm, at("awq_w8a8_gemm")),
+        kv4_append=p(m.kv4_append, at("awq_kv4_append")), kv4_gather=p(m.kv4_gather, at("awq_kv4_gather")),
+        kv4_attention=p(m.kv4_attention, at("awq_kv4_attention"), at("awq_kv4_attention_workspace_size")))
+
+
+@functools.lru_cache(maxsize=None)
 def _unread(dev):
     """An error word for calls that have no workspace of their own, where the workspace is nothing else: nobody reads it."""
     return _torch().empty(1024, dtype=_torch().uint8, device=f"cuda:{dev}")
@@ -514,6 +537,11 @@ def quantize_int8(X, s=None, inverse=False, outputs=None):
     strided). s (float32 [d_in]): the channels are multiplied by it first (a
     weight: W S) or, with inverse=True, by 1 / s (activations: X S^-1); without
     it X is taken as it is."""
+    if outputs is None:
+        r = _calls(_active).quantize_int8(X, s, 2 if inverse else 1)
+        if r.__class__ is tuple:
+            return r
+        _check(r or AWQ_OK, "awq_quantize_int8")
     torch = _torch()
     dev, stream, codes = _here(X, "X")
     dt = _code(X.dtype, codes, "X")
@@ -547,6 +575,12 @@ def w8a8_gemm(xq, x_step, wq, w_step, dtype=None, bias=None, ws=None, out=None):
     * w_step (+ bias, float32 [d_out]), the integer sum exact; xq int8 [N, d_in]
     and wq int8 [d_out, d_in] with their steps from quantize_int8."""
     torch = _torch()
+    if out is None and ws is None and dtype in (None, torch.bfloat16, torch.float16):
+        r = _calls(_active).w8a8_gemm(xq, x_step, wq, w_step, bias, dtype is torch.float16,
+                                      _unread(_torch_names()[1]()) if isinstance(xq, torch.Tensor) and xq.is_cuda else None)
+        if isinstance(r, torch.Tensor):
+            return r
+        _check(r or AWQ_OK, "awq_w8a8_gemm")
     dev, stream, codes = _here(xq, "xq")
     _req_here(xq, torch.int8, None, dev, "xq")
     _req_here(wq, torch.int8, None, dev, "wq")
@@ -605,6 +639,11 @@ def kv4_append(k, v, slots, cache, cfg: Kv4Cfg):
     """Write the keys and values k, v (bf16 or fp16 [T, n_kv_heads, head_dim],
     tokens and heads may be strided) of T tokens to their slots (int32 [T]: page
     * page_size + position; outside the cache: skipped) of the cache, in place."""
+    if cfg.__class__ is Kv4Cfg:
+        r = _calls(_active).kv4_append(k, v, slots, cache, ctypes.addressof(cfg))
+        if r is not None:
+            _check(r, "awq_kv4_append")
+            return cache
     dev, stream, codes = _here(k, "k")
     dt = _code(k.dtype, codes, "k")
     T = k.shape[0] if k.dim() else 0
@@ -626,6 +665,11 @@ def kv4_append(k, v, slots, cache, cfg: Kv4Cfg):
 def kv4_gather(cache, slots, cfg: Kv4Cfg, dtype=None, outputs=None):
     """Keys and values [T, n_kv_heads, head_dim] (bf16 by default, or fp16) that
     the cache holds for the T slots; a slot outside the cache reads as zeros."""
+    if outputs is None and cfg.__class__ is Kv4Cfg and dtype in (None, _torch().bfloat16, _torch().float16):
+        r = _calls(_active).kv4_gather(cache, slots, ctypes.addressof(cfg), dtype is _torch().float16)
+        if r.__class__ is tuple:
+            return r
+        _check(r or AWQ_OK, "awq_kv4_gather")
     dev, stream, codes = _here(cache, "cache")
     _req_cache(cache, cfg, dev)
     _req_here(slots, _torch().int32, None, dev, "slots")
@@ -668,6 +712,11 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
     head_dim], or (out, lse float32 [T, n_q_heads]) with lse=True. Rows of no
     sequence are left as they were (unset in a fresh output)."""
     torch = _torch()
+    if ws is None and out is None and cfg.__class__ is Kv4Cfg:
+        r = _calls(_active).kv4_attention(q, cache, table, lens, ctypes.addressof(cfg), q_start, max_q, scale, bool(lse))
+        if r.__class__ is tuple or isinstance(r, torch.Tensor):
+            return r
+        _check(r or AWQ_OK, "awq_kv4_attention")
     dev, stream, codes = _here(q, "q")
     dt = _code(q.dtype, codes, "q")
     T, n_q_heads, D = q.shape if q.dim() == 3 else (None, None, None)
