@@ -190,6 +190,7 @@ __device__ __forceinline__ void kv4_quantize(const uint4 (&raw)[NC], int group, 
 // one pass behind the other, share the rest about equally.
 template <bool F16>
 __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS) kv4_append_kernel(const Kv4AppendArgs a, const int span) {
+  let_next_kernel_start();
   __shared__ uint32_t codes[KV4_APPEND_WARPS][16][33];  // a strip's value codes, a word a chunk; padded rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, begin = blockIdx.x * span;
   const Kv4Tokens own = kv4_tokens(a.slots, a.T, begin, span, lane);
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS)
     kv4_gather_kernel(const Kv4Cache c, const int* __restrict__ slots, int T, void* __restrict__ kv, void* __restrict__ vv,
                       const int span) {
   __shared__ uint32_t codes[KV4_APPEND_WARPS][16][33];
+  wait_for_kernel_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, begin = blockIdx.x * span;
   const Kv4Tokens own = kv4_tokens(slots, T, begin, span, lane);
   const int D = c.dim, chunks = D / 8, ng = D / c.group, per_bits = __ffs(c.group / 8) - 1, in_mask = (1 << c.page_shift) - 1;
@@ -1302,6 +1304,7 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
     sm.bad = 0;
     sm.abort = 0;
   }
+  wait_for_kernel_before();
   kv4_plan(s, sm.plan, sm.sums);
   if (warp == W) {
     kv4_produce<D, G, NT>(s, sm, lane);
@@ -1398,7 +1401,7 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
       }
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_kernel_start();
   __syncthreads();
   // ---------------- join the warps' parts: chains of consecutive parts of one tile
   // lane e of every warp looks at part e (2 W <= 32): which parts begin a chain
@@ -1454,7 +1457,7 @@ __global__ void __launch_bounds__(32 * KV4_JOIN_WARPS) kv4_attention_join(const 
   constexpr int PART = 8 * NT * (D + 4);
   const Kv4AttnArgs& a = s.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_kernel_before();
   if (c == 0 && warp == 0) {
     int bad = 0;
     for (int i = lane; i < ctas; i += 32) bad = max(bad, s.cta_bad[i]);

@@ -26,21 +26,24 @@ bool kernel_smem(K kernel, int smem, std::atomic<unsigned long long>& once) {
   return true;
 }
 
-// Launch that may start while the kernel before it on the stream ends
-// (programmatic dependent launch): the kernel waits for it by
-// griddepcontrol.wait before it touches memory.
+// Launch that may start while the kernel before it on the stream still runs
+// (programmatic dependent launch): the kernel waits for that one's end before it
+// touches memory. cluster: CTAs of a cluster whose size the kernel leaves open.
 template <typename... P, typename... A>
-awq_status launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t cs, A... args) {
+awq_status launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t cs, unsigned cluster, A... args) {
   cudaLaunchConfig_t c{};
   c.gridDim = grid;
   c.blockDim = block;
   c.dynamicSmemBytes = smem;
   c.stream = cs;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &at;
-  c.numAttrs = 1;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = cluster ? 2 : 1;
   return cudaLaunchKernelEx(&c, kernel, P(args)...) == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
 }
 
@@ -302,25 +305,13 @@ extern "C" awq_status awq_w8a8_gemm(const int8_t* xq, const float* x_step, const
   if (p.small) {
     auto launch = [&](auto kernel) -> awq_status {
       if (!kernel_smem(kernel, W8_SMEM_LIMIT / 2, once[f16 ? 1 : 0])) return AWQ_ERR_CUDA;
-      cudaLaunchConfig_t c{};
-      c.gridDim = dim3((unsigned)p.ctas);
-      c.blockDim = dim3(W8_SMALL_THREADS);
-      c.dynamicSmemBytes = p.smem;
-      c.stream = cs;
-      cudaLaunchAttribute at{};
-      at.id = cudaLaunchAttributeClusterDimension;
-      at.val.clusterDim.x = (unsigned)a.split;
-      at.val.clusterDim.y = at.val.clusterDim.z = 1;
-      c.attrs = &at;
-      c.numAttrs = 1;
-      return cudaLaunchKernelEx(&c, kernel, tw, tx, a) == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+      return launch_behind(kernel, dim3((unsigned)p.ctas), dim3(W8_SMALL_THREADS), p.smem, cs, (unsigned)a.split, tw, tx, a);
     };
     return f16 ? launch(w8a8_small_tcgen05<true>) : launch(w8a8_small_tcgen05<false>);
   }
   auto launch = [&](auto kernel) -> awq_status {
     if (!kernel_smem(kernel, W8_SMEM_LIMIT, once[(p.pair ? 4 : 2) + (f16 ? 1 : 0)])) return AWQ_ERR_CUDA;
-    kernel<<<p.ctas, W8_THREADS, p.smem, cs>>>(tw, tx, a);
-    return launch_status();
+    return launch_behind(kernel, dim3((unsigned)p.ctas), dim3(W8_THREADS), p.smem, cs, 0, tw, tx, a);
   };
   return p.pair ? (f16 ? launch(w8a8_gemm_pair_tcgen05<true>) : launch(w8a8_gemm_pair_tcgen05<false>))
                 : (f16 ? launch(w8a8_gemm_tcgen05<true>) : launch(w8a8_gemm_tcgen05<false>));
@@ -373,11 +364,8 @@ extern "C" awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const i
   const Kv4Cache c = kv4_cache(cfg, cache, n_pages);
   const int span = kv4_span(T);
   const unsigned blocks = (unsigned)((T + span - 1) / span);
-  if (dtype == AWQ_DTYPE_F16)
-    kv4_gather_kernel<true><<<blocks, 32 * KV4_APPEND_WARPS, 0, as_stream(stream)>>>(c, slots, (int)T, k, v, span);
-  else
-    kv4_gather_kernel<false><<<blocks, 32 * KV4_APPEND_WARPS, 0, as_stream(stream)>>>(c, slots, (int)T, k, v, span);
-  return launch_status();
+  auto kernel = dtype == AWQ_DTYPE_F16 ? kv4_gather_kernel<true> : kv4_gather_kernel<false>;
+  return launch_behind(kernel, dim3(blocks), dim3(32 * KV4_APPEND_WARPS), 0, as_stream(stream), 0, c, slots, (int)T, k, v, span);
 }
 
 extern "C" size_t awq_kv4_attention_workspace_size(int64_t batch, int64_t n_q_heads, int64_t max_q,
@@ -451,9 +439,9 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
         auto j = kv4_attention_join<D, NT>;
         static std::atomic<unsigned long long> once_k{0}, once_j{0};
         if (!kernel_smem(k, smem, once_k) || !kernel_smem(j, 0, once_j)) return AWQ_ERR_CUDA;
-        k<<<KV4_CTAS, 32 * (kv4_warps(D, G, NT) + 1), smem, cs>>>(sa);
-        if ((st = launch_status()) != AWQ_OK || sa.solo) return st;
-        return launch_behind(j, dim3(KV4_CTAS), dim3(32 * KV4_JOIN_WARPS), 0, cs, sa, KV4_CTAS);
+        st = launch_behind(k, dim3(KV4_CTAS), dim3(32 * (kv4_warps(D, G, NT) + 1)), smem, cs, 0, sa);
+        if (st != AWQ_OK || sa.solo) return st;
+        return launch_behind(j, dim3(KV4_CTAS), dim3(32 * KV4_JOIN_WARPS), 0, cs, 0, sa, KV4_CTAS);
       };
       return L.nt == 2 ? launch(std::integral_constant<int, D <= 128 ? 2 : 1>{}) : launch(std::integral_constant<int, 1>{});
     });

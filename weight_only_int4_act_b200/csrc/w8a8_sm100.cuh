@@ -24,6 +24,14 @@
 
 namespace awq {
 
+// Kernels that come in chains (a quantiser and its product, a cache write and the
+// attention) overlap each other's launch: the first one lets the next start as
+// soon as all of its blocks have, and that one waits, its barriers and tensor
+// memory set up, until the first has ended and its writes are there. Nothing is
+// read or written before the wait.
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 enum : int { Q8_PLAIN = 0, Q8_MUL = 1, Q8_DIV = 2 };  // v = x, x s, x (1 / s)
 constexpr int W8_MAX_K = 131072;
 
@@ -92,6 +100,7 @@ __device__ __forceinline__ uint32_t q8_block_max(uint32_t top, uint32_t* red) {
 template <bool F16, int MODE, int CH>
 __global__ void quantize_int8_rows(const void* __restrict__ xv, long long ldx, const float* __restrict__ s, long long rows,
                                    int d_in, int8_t* __restrict__ q, float* __restrict__ step) {
+  let_next_kernel_start();
   const uint16_t* x = static_cast<const uint16_t*>(xv);
   __shared__ uint32_t red[2][32];
   const int n8 = d_in / 8, tid = threadIdx.x, T = blockDim.x;
@@ -143,6 +152,7 @@ template <bool F16, int MODE>
 __global__ void __launch_bounds__(1024)
     quantize_int8_long(const void* __restrict__ xv, long long ldx, const float* __restrict__ s, long long rows, int d_in,
                        int8_t* __restrict__ q, float* __restrict__ step) {
+  let_next_kernel_start();
   const uint16_t* x = static_cast<const uint16_t*>(xv);
   __shared__ uint32_t red[2][32];
   const int n8 = d_in / 8;
@@ -348,8 +358,6 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    // the error word of this call: only waits that give up after two seconds write it
-    if (blockIdx.x == 0) *args.err = 0;
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmW);
@@ -368,6 +376,9 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // barriers of both CTAs initialised before any remote use
   tc_fence_after();
+  wait_for_kernel_before();
+  // the error word of this call: only waits that give up after two seconds write it
+  if (blockIdx.x == 0 && threadIdx.x == 0) *args.err = 0;
   const uint32_t tmem_base = *tmem_slot;
   constexpr int acc_stride = 256;
 
@@ -557,7 +568,6 @@ __global__ void __launch_bounds__(W8_SMALL_THREADS)
     mbar_init(tfull, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    if (blockIdx.x == 0) *args.err = 0;
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmW);
@@ -570,6 +580,8 @@ __global__ void __launch_bounds__(W8_SMALL_THREADS)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  wait_for_kernel_before();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *args.err = 0;
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
