@@ -525,6 +525,56 @@ def test_two_streams_at_once():
         assert all(torch.equal(w, x) for x in g)
 
 
+def test_captured_between_other_work():
+    """Calls captured behind copies, fills and another stream's work, whose launches overlap the kernel before them: every
+    kernel sees what the ones before wrote."""
+    cfg, cache, table, lens, slots = _fill([300, 41, 2500], 4, 128, 128, 32, "bf16", 150)
+    X, W = _rand((9, 512), "bf16", 151), _rand((1024, 512), "bf16", 152, 0.1)
+    wq, w_step = awq.quantize_int8(W)
+    new = torch.from_numpy(slots[np.cumsum([300, 41, 2500]) - 1]).int().cuda()
+    x_in, q_in = torch.zeros_like(X[:3]), torch.zeros((3, 1024), dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            twice = x_in + x_in
+        xq, x_step = awq.quantize_int8(x_in)
+        here.wait_stream(side)
+        y = awq.w8a8_gemm(xq, x_step, wq, w_step)  # behind an event as well as a kernel
+        q_in.copy_(y)
+        kv = q_in.view(3, 8, 128)[:, :4].contiguous()
+        awq.kv4_append(kv, kv, new, cache, cfg)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            z = awq.quantize_int8(twice)[1]
+        out = awq.kv4_attention(q_in.view(3, 8, 128), cache, table, lens, cfg)
+        here.wait_stream(side)
+        k, _ = awq.kv4_gather(cache, new, cfg)
+        q_in.zero_()
+        many = awq.kv4_attention(out.repeat(40, 1, 1), cache, table[2:], lens[2:], cfg,
+                                 q_start=start, max_q=120)
+        return y, z, out, k, many
+    start = torch.tensor([0, 120], dtype=torch.int32, device="cuda")
+    x_in.copy_(X[:3])
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for i in range(3):
+        x_in.copy_(X[3 * i:3 * i + 3])
+        want = step()
+        torch.cuda.synchronize()
+        for t in got:
+            t.fill_(0)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b) and b.any()
+
+
 def test_short_and_long_calls_agree():
     """Calls that leave outputs and workspace to the library (one compiled call) and calls that bring their own."""
     cfg, cache, table, lens, slots = _fill([300, 41, 77], 4, 128, 64, 32, "f16", 140)

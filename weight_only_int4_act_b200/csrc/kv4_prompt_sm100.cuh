@@ -157,6 +157,8 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
   const Kv4AttnArgs& a = args.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.y, b = blockIdx.z;
+  let_next_kernel_start();
+  wait_for_kernel_before();
   const Kv4Seq seq = kv4_seq(a, b);
   const int rows = seq.n * a.share;
   if (threadIdx.x == 0 && seq.bad) atomicMax(a.err, ERR_KV4_PAGE);

@@ -191,6 +191,7 @@ __device__ __forceinline__ void kv4_quantize(const uint4 (&raw)[NC], int group, 
 template <bool F16>
 __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS) kv4_append_kernel(const Kv4AppendArgs a, const int span) {
   let_next_kernel_start();
+  wait_for_kernel_before();
   __shared__ uint32_t codes[KV4_APPEND_WARPS][16][33];  // a strip's value codes, a word a chunk; padded rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, begin = blockIdx.x * span;
   const Kv4Tokens own = kv4_tokens(a.slots, a.T, begin, span, lane);
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS)
     kv4_gather_kernel(const Kv4Cache c, const int* __restrict__ slots, int T, void* __restrict__ kv, void* __restrict__ vv,
                       const int span) {
   __shared__ uint32_t codes[KV4_APPEND_WARPS][16][33];
+  let_next_kernel_start();
   wait_for_kernel_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, begin = blockIdx.x * span;
   const Kv4Tokens own = kv4_tokens(slots, T, begin, span, lane);

@@ -256,15 +256,22 @@ extern "C" awq_status awq_quantize_int8(const void* x, awq_dtype dtype, int64_t 
   auto launch = [&](auto f16, auto m) {
     constexpr bool F = decltype(f16)::value;
     constexpr int M = decltype(m)::value;
+    const void* in = x;
+    // Blocks of a row each overlap the launch with the kernel before (333 rows of
+    // 4096 and their product: 28.8 -> 27.3 us). Blocks that stay for several rows
+    // would share the SMs with the waiting blocks of the kernels around them: 4096
+    // rows, 1000 more and the product took 102 us that way, 78 without.
+    auto behind = [&](auto kernel, unsigned blocks, unsigned block) {
+      if (blocks == rows)
+        return launch_behind(kernel, dim3(blocks), dim3(block), 0, cs, 0, in, ldx, s, rows, (int)d_in, q, step);
+      kernel<<<blocks, block, 0, cs>>>(in, ldx, s, rows, (int)d_in, q, step);
+      return launch_status();
+    };
     if (threads > (ch == 4 ? 512u : 1024u))
-      quantize_int8_long<F, M><<<(unsigned)(rows < 2 * sms ? rows : 2 * sms), 1024, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
-    else if (ch == 1)
-      quantize_int8_rows<F, M, 1><<<grid, threads, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
-    else if (ch == 2)
-      quantize_int8_rows<F, M, 2><<<grid, threads, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
-    else
-      quantize_int8_rows<F, M, 4><<<grid, threads, 0, cs>>>(x, ldx, s, rows, (int)d_in, q, step);
-    return launch_status();
+      return behind(quantize_int8_long<F, M>, (unsigned)(rows < 2 * sms ? rows : 2 * sms), 1024u);
+    if (ch == 1) return behind(quantize_int8_rows<F, M, 1>, grid, threads);
+    if (ch == 2) return behind(quantize_int8_rows<F, M, 2>, grid, threads);
+    return behind(quantize_int8_rows<F, M, 4>, grid, threads);
   };
   auto modes = [&](auto f16) {
     if (mode == AWQ_SCALE_MUL) return launch(f16, std::integral_constant<int, Q8_MUL>{});
@@ -344,11 +351,8 @@ extern "C" awq_status awq_kv4_append(const void* k, const void* v, awq_dtype dty
   a.c = kv4_cache(cfg, cache, n_pages);
   const int span = kv4_span(T);
   const unsigned blocks = (unsigned)((T + span - 1) / span);
-  if (dtype == AWQ_DTYPE_F16)
-    kv4_append_kernel<true><<<blocks, 32 * KV4_APPEND_WARPS, 0, as_stream(stream)>>>(a, span);
-  else
-    kv4_append_kernel<false><<<blocks, 32 * KV4_APPEND_WARPS, 0, as_stream(stream)>>>(a, span);
-  return launch_status();
+  auto kernel = dtype == AWQ_DTYPE_F16 ? kv4_append_kernel<true> : kv4_append_kernel<false>;
+  return launch_behind(kernel, dim3(blocks), dim3(32 * KV4_APPEND_WARPS), 0, as_stream(stream), 0, a, span);
 }
 
 extern "C" awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const int32_t* slots, int64_t T,
@@ -458,8 +462,7 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
       static_assert(smem <= 232448, "shared memory of the prompt attention");
       auto launch = [&](auto k, std::atomic<unsigned long long>& once) -> awq_status {
         if (!kernel_smem(k, smem, once)) return AWQ_ERR_CUDA;
-        k<<<grid, KVP_THREADS, smem, cs>>>(pa);
-        return launch_status();
+        return launch_behind(k, grid, dim3(KVP_THREADS), smem, cs, 0, pa);
       };
       static std::atomic<unsigned long long> once[2];
       if constexpr (D == G)

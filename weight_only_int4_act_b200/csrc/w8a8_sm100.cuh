@@ -101,6 +101,7 @@ template <bool F16, int MODE, int CH>
 __global__ void quantize_int8_rows(const void* __restrict__ xv, long long ldx, const float* __restrict__ s, long long rows,
                                    int d_in, int8_t* __restrict__ q, float* __restrict__ step) {
   let_next_kernel_start();
+  wait_for_kernel_before();
   const uint16_t* x = static_cast<const uint16_t*>(xv);
   __shared__ uint32_t red[2][32];
   const int n8 = d_in / 8, tid = threadIdx.x, T = blockDim.x;
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(1024)
     quantize_int8_long(const void* __restrict__ xv, long long ldx, const float* __restrict__ s, long long rows, int d_in,
                        int8_t* __restrict__ q, float* __restrict__ step) {
   let_next_kernel_start();
+  wait_for_kernel_before();
   const uint16_t* x = static_cast<const uint16_t*>(xv);
   __shared__ uint32_t red[2][32];
   const int n8 = d_in / 8;
@@ -376,6 +378,7 @@ __device__ __forceinline__ void w8a8_body(const CUtensorMap& tmW, const CUtensor
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // barriers of both CTAs initialised before any remote use
   tc_fence_after();
+  let_next_kernel_start();
   wait_for_kernel_before();
   // the error word of this call: only waits that give up after two seconds write it
   if (blockIdx.x == 0 && threadIdx.x == 0) *args.err = 0;
@@ -580,6 +583,7 @@ __global__ void __launch_bounds__(W8_SMALL_THREADS)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  let_next_kernel_start();
   wait_for_kernel_before();
   if (blockIdx.x == 0 && threadIdx.x == 0) *args.err = 0;
   const uint32_t tmem_base = *tmem_slot;
