@@ -413,7 +413,9 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
     const int q = (warp - 6) >> 2, quad = warp & 3, row = quad * 32 + lane, r = r0 + 128 * q + row;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const bool in = r < rows;
-    const int vis = in ? seq.L - seq.n + (int)((unsigned)r / (unsigned)a.share) + 1 : 0;
+    // (a row behind the last, whose query is 0 and which is not written, sees all:
+    // else its warp would take the long way at every tile)
+    const int vis = in ? seq.L - seq.n + (int)((unsigned)r / (unsigned)a.share) + 1 : 0x7fffffff;
     {
       // The warp's 32 rows, a row by LANES lanes of 8 channels each: scaled by a
       // power of two so that the largest entry lies in [2^10, 2^11) (a row of
