@@ -16,11 +16,11 @@
 // factor of its scores; but for fp16 queries (EXACT; one group a head), whose
 // output resolves it, the codes less zeros (-15 .. 15) are the keys, exactly, and
 // each score is multiplied by its token's step in fp32 (2 x 2048 queries of 8000
-// tokens, 32 heads over 8 of 128, bf16: 474 us that way, 444 with folded keys; one
+// tokens, 32 heads over 8 of 128, bf16: 474 us that way, 442 with folded keys; one
 // read of a step from shared memory a score, beside the MMAs' operands).
 // A token one of whose groups holds NaN turns the rows that see it to NaN.
 //
-// Measured: 2 x 2048 queries of up to 8000 tokens, 32 heads over 8 of 128: 444 us,
+// Measured: 2 x 2048 queries of up to 8000 tokens, 32 heads over 8 of 128: 442 us,
 // 752 TFLOP/s (202 us at the bf16 rate). A context tile takes a block about 2200
 // cycles. Its MMAs are 1024 cycles' work and take 1560, as N = 64 costs what
 // N = 128 does (64 to 67 cycles); beside them go the exponentials of 16384 scores

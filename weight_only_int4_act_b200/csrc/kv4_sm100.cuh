@@ -182,7 +182,7 @@ __device__ __forceinline__ void kv4_quantize(const uint4 (&raw)[NC], int group, 
   }
 }
 
-// 16411 tokens of 8 heads of 128 in groups of 32, fp16: 29 us for 67 MB read and
+// 16411 tokens of 8 heads of 128 in groups of 32, fp16: 30 us for 67 MB read and
 // 21 written (13.5 at a copy's rate); 64 single tokens 2.5 us, a launch. A token at
 // a time took 74 us: bytes of the value words written one by one, a rint, a
 // conversion and two divisions' worth of slow instructions for every 8 channels
@@ -238,55 +238,64 @@ __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS) kv4_append_kernel(const
   const long long page = slot >> a.c.page_shift;
   if (slot < 0 || page >= a.c.n_pages) return;
   uint32_t(&cw)[16][33] = codes[warp];
-  // the warp's lanes over (token, two chunks), tokens outermost: chunks of a group stay neighbours
-  const int pairs = D / 16, t0 = lane / pairs, ch0 = lane - t0 * pairs, dt = 32 / pairs, dch = 32 - dt * pairs;
-  for (int head = warp; head < a.c.heads; head += KV4_APPEND_WARPS) {
-    const long long base = a.c.strip(page, head, slot & in_mask);
-    if (!AWQ_SPAN_OK(base, a.c.strip_bytes, a.c.bytes(), BS_KV4_CACHE)) continue;
-    uint8_t* s = a.c.base + base;
+  // Items: a head, 128 channels of it at most, its keys and then its values; with few
+  // heads keys and values apart, for more warps. (3 x 4439 tokens of two heads of 256
+  // and their read-back take 30 us so, 50 with a whole head an item; 9000 tokens of 4
+  // heads of 128 21.3, 21.8 with keys and values apart.) The warp's lanes go over
+  // (token, two chunks), tokens outermost: chunks of a group stay neighbours.
+  const int apart = a.c.heads < 4, slices = D > 128 ? 2 : 1, width = D / slices, pairs = width / 16;
+  const int t0 = lane / pairs, pair0 = lane - t0 * pairs, dt = 32 / pairs, dp = 32 - dt * pairs;
+  for (int it = warp; it < slices * a.c.heads << apart; it += KV4_APPEND_WARPS) {
+    const int slice = slices == 2 ? it & 1 : 0, hv = slices == 2 ? it >> 1 : it, head = apart ? hv >> 1 : hv;
 #pragma unroll 1
-    for (int val = 0; val < 2; ++val) {
-      const uint16_t* src = val ? a.v + (long long)tok * a.v_tok + (long long)head * a.v_head
-                                : a.k + (long long)tok * a.k_tok + (long long)head * a.k_head;
+    for (int val = apart ? hv & 1 : 0, end = apart ? val + 1 : 2; val < end; ++val) {
+      const long long base = a.c.strip(page, head, slot & in_mask);
+      if (!AWQ_SPAN_OK(base, a.c.strip_bytes, a.c.bytes(), BS_KV4_CACHE)) continue;
+      uint8_t* s = a.c.base + base;
+      const uint16_t* src = (val ? a.v + (long long)tok * a.v_tok + (long long)head * a.v_head
+                                 : a.k + (long long)tok * a.k_tok + (long long)head * a.k_head) + slice * width;
       const long long ld = val ? a.v_tok : a.k_tok;
       uint8_t* pars = s + 16 * D + (val ? 64 * ng : 0);
-      int t = t0, pair = ch0;
+      int t = t0, pair = pair0;
 #pragma unroll 1
-      for (int u0 = 0; u0 < 16 * pairs; u0 += 32) {  // D / 32 turns
+      for (int u0 = 0; u0 < 16 * pairs; u0 += 32) {  // width / 32 turns
         const uint4* from = reinterpret_cast<const uint4*>(src + t * ld + 16 * pair);
         const uint4 raw[2] = {__ldg(from), __ldg(from + 1)};
+        const int ch = slice * (width / 8) + 2 * pair;
         uint32_t word[2], par;
         kv4_quantize<F16>(raw, a.c.group, word, par);
         if (val) {
           cw[t][2 * pair] = word[0];
           cw[t][2 * pair + 1] = word[1];
         } else {
-          uint8_t* to = s + t * (D / 2) + ((2 * pair & 3) * (D / 32) + (pair >> 1)) * 4;
+          uint8_t* to = s + t * (D / 2) + ((ch & 3) * (D / 32) + (ch >> 2)) * 4;
           *reinterpret_cast<uint32_t*>(to) = word[0];
           *reinterpret_cast<uint32_t*>(to + D / 8) = word[1];
         }
-        if ((2 * pair & (per - 1)) == 0) *reinterpret_cast<uint32_t*>(pars + (2 * pair >> per_bits) * 64 + 4 * t) = par;
+        if ((ch & (per - 1)) == 0) *reinterpret_cast<uint32_t*>(pars + (ch >> per_bits) * 64 + 4 * t) = par;
         t += dt;
-        pair += dch;
+        pair += dp;
         if (pair >= pairs) pair -= pairs, ++t;
       }
-    }
-    __syncwarp();
-    for (int it = lane; it < D / 4; it += 32) {  // items (p, q, h)
-      const int h = it & 1, q = (it >> 1) & 3, p = it >> 3;
-      uint32_t w[8];
+      if (!val) continue;
+      __syncwarp();
+      if (lane < width / 4) {  // items (p, q, h) of the transposition
+        const int h = lane & 1, q = (lane >> 1) & 3, p = lane >> 3;
+        uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = cw[kv4_row_token(j, q)][kv4_row_chunk(j, p, h)];
-      kv4_transpose(w);
+        for (int j = 0; j < 8; ++j) w[j] = cw[kv4_row_token(j, q)][kv4_row_chunk(j, p, h)];
+        kv4_transpose(w);
+        uint8_t* to = s + 8 * D + ((slice * (width / 32) + p) * 32 + q) * 8 + 4 * h;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) *reinterpret_cast<uint32_t*>(s + 8 * D + (p * 32 + 4 * r + q) * 8 + 4 * h) = w[r];
+        for (int r = 0; r < 8; ++r) *reinterpret_cast<uint32_t*>(to + 32 * r) = w[r];
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
 // (code - zero) * step of tokens of the cache, dense; slots outside it give
-// zeros. Blocks, strips and warps as in the write. The same 16411 tokens: 25 us
+// zeros. Blocks, strips and warps as in the write. The same 16411 tokens: 26 us
 // (45 a token at a time; 13.5 at a copy's rate), waiting for the strips' words.
 template <bool F16>
 __device__ __forceinline__ uint4 kv4_values(uint32_t word, uint32_t par) {
@@ -350,45 +359,49 @@ __global__ void __launch_bounds__(32 * KV4_APPEND_WARPS)
   const int i = __ffs(own.strips) - 1, tok = begin + i, slot = __shfl_sync(0xffffffffu, own.slot, i);
   const long long page = slot >> c.page_shift;
   uint32_t(&cw)[16][33] = codes[warp];
-  const int t0 = lane / chunks, ch0 = lane - t0 * chunks, dt = 32 / chunks, dch = 32 - dt * chunks;
-  for (int head = warp; head < c.heads; head += KV4_APPEND_WARPS) {
-    const long long base = in ? c.strip(page, head, slot & in_mask) : 0;
-    const bool ok = in && AWQ_SPAN_OK(base, c.strip_bytes, c.bytes(), BS_KV4_CACHE);
-    const uint8_t* s = c.base + base;
-    if (vv && ok) {
-      for (int it = lane; it < D / 4; it += 32) {
-        const int h = it & 1, q = (it >> 1) & 3, p = it >> 3;
-        uint32_t w[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) w[r] = *reinterpret_cast<const uint32_t*>(s + 8 * D + (p * 32 + 4 * r + q) * 8 + 4 * h);
-        kv4_transpose(w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) cw[kv4_row_token(j, q)][kv4_row_chunk(j, p, h)] = w[j];
-      }
-      __syncwarp();
-    }
+  const int apart = c.heads < 4, slices = D > 128 ? 2 : 1, width = D / slices, row = width / 8;  // items as in the write
+  const int t0 = lane / row, ch0 = lane - t0 * row, dt = 32 / row, dch = 32 - dt * row;
+  for (int it = warp; it < slices * c.heads << apart; it += KV4_APPEND_WARPS) {
+    const int slice = slices == 2 ? it & 1 : 0, hv = slices == 2 ? it >> 1 : it, head = apart ? hv >> 1 : hv;
 #pragma unroll 1
-    for (int val = 0; val < 2; ++val) {
+    for (int val = apart ? hv & 1 : 0, end = apart ? val + 1 : 2; val < end; ++val) {
       uint16_t* dst = static_cast<uint16_t*>(val ? vv : kv);
       if (!dst) continue;
+      const long long base = in ? c.strip(page, head, slot & in_mask) : 0;
+      const bool ok = in && AWQ_SPAN_OK(base, c.strip_bytes, c.bytes(), BS_KV4_CACHE);
+      const uint8_t* s = c.base + base;
+      if (val && ok) {
+        if (lane < width / 4) {
+          const int h = lane & 1, q = (lane >> 1) & 3, p = lane >> 3;
+          const uint8_t* from = s + 8 * D + ((slice * (width / 32) + p) * 32 + q) * 8 + 4 * h;
+          uint32_t w[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) w[r] = *reinterpret_cast<const uint32_t*>(from + 32 * r);
+          kv4_transpose(w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) cw[kv4_row_token(j, q)][kv4_row_chunk(j, p, h)] = w[j];
+        }
+        __syncwarp();
+      }
       const uint8_t* pars = s + 16 * D + (val ? 64 * ng : 0);
-      int t = t0, ch = ch0;
+      int t = t0, c0 = ch0;
 #pragma unroll 2
-      for (int u0 = 0; u0 < 16 * chunks; u0 += 32) {
+      for (int u0 = 0; u0 < 16 * row; u0 += 32) {
+        const int ch = slice * row + c0;
         uint4 out = make_uint4(0, 0, 0, 0);
         if (ok) {
           const uint32_t word =
-              val ? cw[t][ch] : *reinterpret_cast<const uint32_t*>(s + t * (D / 2) + ((ch & 3) * (D / 32) + (ch >> 2)) * 4);
+              val ? cw[t][c0] : *reinterpret_cast<const uint32_t*>(s + t * (D / 2) + ((ch & 3) * (D / 32) + (ch >> 2)) * 4);
           out = kv4_values<F16>(word, *reinterpret_cast<const uint32_t*>(pars + (ch >> per_bits) * 64 + 4 * t));
         }
         const long long at = ((long long)(tok + t) * c.heads + head) * D + 8 * ch;
         if (AWQ_SPAN_OK(at, 8, all, BS_KV4_OUT)) *reinterpret_cast<uint4*>(dst + at) = out;
         t += dt;
-        ch += dch;
-        if (ch >= chunks) ch -= chunks, ++t;
+        c0 += dch;
+        if (c0 >= row) c0 -= row, ++t;
       }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
@@ -897,7 +910,7 @@ struct Kv4Warp {
 // 131072 (604 MB) 119 us (92). The strips arrive at 6.9 TB/s; the rest is the
 // launch and the plan (4 us until the first copies are asked for), the slowest
 // warp of a block (2 to 3 us behind the mean) and the two joins (2 and 4 us). A
-// sequence of 777 tokens with 32 kv heads takes 8.9 us; 16 sequences with 5
+// sequence of 777 tokens with 32 kv heads takes 8.7 us; 16 sequences with 5
 // queries each, 16 rows a tile, 24 us, of which the same ends are half.
 constexpr int KV4_EDGE = 2;
 constexpr int KV4_MAX_BATCH = 512;  // sequences of a launch: what the block needs of them sits in shared memory

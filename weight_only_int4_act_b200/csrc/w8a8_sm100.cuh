@@ -222,15 +222,15 @@ __device__ __forceinline__ bool mbar_wait_lean(uint32_t bar, uint32_t parity, vo
 // the plan takes the tile shape with the fewest bytes an SM. Measured, with the
 // time at twice the bf16 rate: 16384 tokens of 28672 x 8192 2.44 to 2.57 ms
 // under the power cap (2.32), 1000 of 4096 x 11008 32 us (27), 333 of
-// 11008 x 4096 23 us (9: 129 tiles for 74 pairs are two waves, and the pipeline's
+// 11008 x 4096 22 us (9: 129 tiles for 74 pairs are two waves, and the pipeline's
 // fill and the last epilogue are 4 us of them).
 //
 // w8a8_small_tcgen05 (few tokens): the weights' bytes are the bound, and 128 of
 // its channels a CTA are too few CTAs. So a cluster of S CTAs shares a tile,
 // each over its S-th of K, several CTAs to an SM; at the end they add their
 // int32 accumulators through distributed shared memory (exact in any order).
-// Measured: 16 tokens of 28672 x 8192 42.5 us, 5.5 TB/s (36 us at a copy's rate);
-// one of 4096 x 4096 6.5 us (2.6), of which 4 are launch, fill and the join.
+// Measured: 16 tokens of 28672 x 8192 41.5 us, 5.7 TB/s (36 us at a copy's rate);
+// one of 4096 x 4096 5.3 us (2.6) behind other kernels, 6.5 alone.
 constexpr int W8_BM = 128;
 constexpr int W8_BK = 128;
 constexpr int W8_A_STAGE = W8_BM * W8_BK;
