@@ -157,7 +157,6 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
   const Kv4AttnArgs& a = args.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.y, b = blockIdx.z;
-  let_next_kernel_start();
   wait_for_kernel_before();
   const Kv4Seq seq = kv4_seq(a, b);
   const int rows = seq.n * a.share;
@@ -207,6 +206,10 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Only now may the next kernel start: the 8-bit product takes its tensor memory
+  // before it waits for this kernel's end, and a block of it on this SM would
+  // otherwise hold columns that this block still has to wait for.
+  let_next_kernel_start();
   const uint32_t tmem = sm.tmem;
   volatile int* abort_flag = &sm.abort;
   auto score_col = [&](int q, int buf) { return tmem + (uint32_t)(128 * q + 64 * buf); };

@@ -28,7 +28,9 @@ namespace awq {
 // attention) overlap each other's launch: the first one lets the next start as
 // soon as all of its blocks have, and that one waits, its barriers and tensor
 // memory set up, until the first has ended and its writes are there. Nothing is
-// read or written before the wait.
+// read or written before the wait. A kernel that allocates tensor memory lets the
+// next one start only once it has it: all that a waiting kernel holds, it holds
+// until the kernels before it have ended, and those must not need it.
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
