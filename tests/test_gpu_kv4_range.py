@@ -18,6 +18,16 @@ import weight_only_int4_act_b200 as awq  # noqa: E402
 from test_gpu_kv4 import DT, _check, _f64, _fill, _rand, _read  # noqa: E402
 
 
+def _write(cache, cfg, slots, k, v):
+    awq.kv4_append(k, v, torch.from_numpy(np.asarray(slots)).int().cuda(), cache, cfg)
+
+
+def _attend(q, cache, table, lens, cfg, new, **kw):
+    """(out, lse) of `new` rows a sequence."""
+    start = torch.arange(lens.numel() + 1, dtype=torch.int32, device="cuda") * new
+    return awq.kv4_attention(q, cache, table, lens, cfg, q_start=start, max_q=new, lse=True, **kw)
+
+
 # ---------------------------------------------------------------- kernels behind one another
 @pytest.mark.parametrize("dim", [64, 128])
 def test_prompt_then_the_8_bit_layer(dim):
@@ -40,3 +50,22 @@ def test_prompt_then_the_8_bit_layer(dim):
         torch.cuda.synchronize()
         got = [step(q, lambda: None) for _ in range(5)]
         assert all(torch.equal(want, g) for g in got) and want.any()
+
+
+# ---------------------------------------------------------------- references outgrown
+@pytest.mark.parametrize("dtype,dim,group", [("bf16", 64, 64), ("bf16", 128, 32), ("f16", 128, 128)])
+def test_prompt_reference_outgrown_in_the_second_half_of_a_tile(dtype, dim, group):
+    """In the second 32 tokens of a tile of 64 stands a key that outweighs all before it by more than 2^14: weights of the
+    tile's first half and the output so far are brought along. In the first tile, and again in later ones."""
+    heads, share, n = 10, 4, 200
+    lens_l = [330, 260]
+    cfg, cache, table, lens, slots = _fill(lens_l, heads, dim, group, 32, dtype, 220, kscale=0.2)
+    c = 8.0 / np.sqrt(dim)  # a step of 1 in a key's height is a score of about 12
+    for base in (0, lens_l[0]):
+        for i, at in enumerate((33 + 5, 64 + 60, 128 + 32, 192 + 47)):
+            v = _rand((1, heads, dim), dtype, 230 + i)
+            k = torch.full((1, heads, dim), float((i + 1) * 1.5), dtype=DT[dtype], device="cuda")
+            _write(cache, cfg, slots[base + at:base + at + 1], k, v)
+    q = (1.5 * c + _rand((2 * n, heads * share, dim), dtype, 240, 0.05).float()).to(DT[dtype])
+    out, lse = _attend(q, cache, table, lens, cfg, n)
+    _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, n, 2 * n], share, dim ** -0.5, dtype, True)

@@ -567,6 +567,7 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
             }
             if (c > 0) {
               uint32_t v[16];
+              tmem_st_wait();  // the first half's weights are there to be read
               __syncwarp();
               tmem_ld_32x32b_x16(col, v);
               tmem_ld_wait();
