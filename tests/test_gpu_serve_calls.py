@@ -1,0 +1,31 @@
+"""The serving calls from Python where arguments are not what a kernel can take: errors, never a crash."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import weight_only_int4_act_b200 as awq  # noqa: E402
+
+
+def test_tensors_without_storage_are_refused():
+    """Inside torch.func's transforms a tensor is a plain torch.Tensor of the right device and type whose data_ptr() throws:
+    a RuntimeError for every call, and the interpreter and the library go on."""
+    cfg = awq.make_kv4(2, 64, 16)
+    cache = awq.kv4_new_cache(4, cfg)
+    x = torch.zeros((3, 2, 4, 64), dtype=torch.bfloat16, device="cuda")
+    codes = torch.zeros((3, 4, 64), dtype=torch.int8, device="cuda")
+    step = torch.ones(4, device="cuda")
+    table, lens = torch.zeros((2, 1), dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(2, dtype=torch.int32, device="cuda")
+    calls = [(lambda t: awq.quantize_int8(t[0]), x),
+             (lambda t: awq.w8a8_gemm(t, step, codes[0], step), codes),
+             (lambda t: awq.kv4_append(t[:, :2], t[:, 2:], slots, cache, cfg), x),
+             (lambda t: awq.kv4_gather(cache, t[:, 0, 0].int(), cfg), x),
+             (lambda t: awq.kv4_attention(t, cache, table, lens, cfg), x)]
+    for f, arg in calls:
+        with pytest.raises(RuntimeError):
+            torch.func.vmap(f)(arg)
+        assert awq.quantize_int8(x[0, 0])[0].shape == (4, 64)  # as before

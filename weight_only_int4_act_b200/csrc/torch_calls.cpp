@@ -60,13 +60,18 @@ template <typename F>
 F* entry(PyObject* o) {
   return reinterpret_cast<F*>(PyLong_AsVoidPtr(o));
 }
-template <typename F>
-awq_status run(F f) {
-  awq_status st;
-  Py_BEGIN_ALLOW_THREADS;
-  st = f();
-  Py_END_ALLOW_THREADS;
-  return st;
+// The C call without the interpreter's lock, which comes back whatever happens.
+// What may throw (a tensor's data_ptr() does where it has no storage, inside
+// torch.func's transforms for one) is evaluated before: arguments are values here.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F, typename... A>
+awq_status run(PyObject* address, A... arg) {
+  F* f = entry<F>(address);
+  Unlocked unlocked;
+  return f(arg...);
 }
 
 PyObject* none() {
@@ -93,11 +98,9 @@ PyObject* quantize_int8(PyObject* const* arg) {
   const auto mode = s ? (awq_scale_mode)PyLong_AsLong(arg[3]) : AWQ_SCALE_NONE;
   at::Tensor q = fresh({n, d}, *X, at::kChar), step = fresh({n}, *X, at::kFloat);
   const int64_t ld = n > 1 ? X->stride(0) : d > 8 ? d : 8;
-  const awq_status st = run([&] {
-    return entry<decltype(awq_quantize_int8)>(arg[0])(X->data_ptr(), code, ld, s ? (const float*)s->data_ptr() : nullptr,
-                                                      mode, n, d, (int8_t*)q.data_ptr(), (float*)step.data_ptr(),
-                                                      here.stream());
-  });
+  const awq_status st = run<decltype(awq_quantize_int8)>(
+      arg[0], X->data_ptr(), code, ld, s ? (const float*)s->data_ptr() : nullptr, mode, n, d, (int8_t*)q.data_ptr(),
+      (float*)step.data_ptr(), here.stream());
   return pair(st, std::move(q), std::move(step));
 }
 
@@ -113,13 +116,11 @@ PyObject* w8a8_gemm(PyObject* const* arg) {
   if (arg[5] != Py_None && !(is(bias, at::kFloat, 1) && bias->size(0) == d_out)) return none();
   const bool f16 = arg[6] == Py_True;
   at::Tensor y = fresh({n, d_out}, *x, f16 ? at::kHalf : at::kBFloat16);
-  const awq_status st = run([&] {
-    return entry<decltype(awq_w8a8_gemm)>(arg[0])(
-        (const int8_t*)x->data_ptr(), (const float*)dx->data_ptr(), (const int8_t*)w->data_ptr(),
-        (const float*)dw->data_ptr(), bias ? (const float*)bias->data_ptr() : nullptr,
-        f16 ? AWQ_DTYPE_F16 : AWQ_DTYPE_BF16, n, d_out, d_in, y.data_ptr(), ws->data_ptr(), (size_t)ws->numel(),
-        here.stream());
-  });
+  const awq_status st = run<decltype(awq_w8a8_gemm)>(
+      arg[0], (const int8_t*)x->data_ptr(), (const float*)dx->data_ptr(), (const int8_t*)w->data_ptr(),
+      (const float*)dw->data_ptr(), bias ? (const float*)bias->data_ptr() : nullptr,
+      f16 ? AWQ_DTYPE_F16 : AWQ_DTYPE_BF16, n, d_out, d_in, y.data_ptr(), ws->data_ptr(), (size_t)ws->numel(),
+      here.stream());
   return st != AWQ_OK ? PyLong_FromLong(st) : THPVariable_Wrap(std::move(y));
 }
 
@@ -134,11 +135,9 @@ PyObject* kv4_append(PyObject* const* arg) {
   if (k->size(1) != cfg.n_kv_heads || k->size(2) != cfg.head_dim || !is(slots, at::kInt, 1) || slots->size(0) != T ||
       !cache_of(cache, cfg))
     return none();
-  return PyLong_FromLong(run([&] {
-    return entry<decltype(awq_kv4_append)>(arg[0])(k->data_ptr(), v->data_ptr(), code, T, k->stride(0), k->stride(1),
-                                                   v->stride(0), v->stride(1), (const int32_t*)slots->data_ptr(),
-                                                   cache->data_ptr(), cache->size(0), &cfg, here.stream());
-  }));
+  return PyLong_FromLong(run<decltype(awq_kv4_append)>(
+      arg[0], k->data_ptr(), v->data_ptr(), code, T, k->stride(0), k->stride(1), v->stride(0), v->stride(1),
+      (const int32_t*)slots->data_ptr(), cache->data_ptr(), cache->size(0), &cfg, here.stream()));
 }
 
 // (entry, cache, slots, address of the cfg, fp16 outputs)
@@ -151,11 +150,9 @@ PyObject* kv4_gather(PyObject* const* arg) {
   const int64_t T = slots->size(0);
   const at::ScalarType type = f16 ? at::kHalf : at::kBFloat16;
   at::Tensor k = fresh({T, cfg.n_kv_heads, cfg.head_dim}, *cache, type), v = fresh({T, cfg.n_kv_heads, cfg.head_dim}, *cache, type);
-  const awq_status st = run([&] {
-    return entry<decltype(awq_kv4_gather)>(arg[0])(cache->data_ptr(), cache->size(0), (const int32_t*)slots->data_ptr(), T,
-                                                   &cfg, k.data_ptr(), v.data_ptr(),
-                                                   f16 ? AWQ_DTYPE_F16 : AWQ_DTYPE_BF16, here.stream());
-  });
+  const awq_status st = run<decltype(awq_kv4_gather)>(
+      arg[0], cache->data_ptr(), cache->size(0), (const int32_t*)slots->data_ptr(), T, &cfg, k.data_ptr(), v.data_ptr(),
+      f16 ? AWQ_DTYPE_F16 : AWQ_DTYPE_BF16, here.stream());
   return pair(st, std::move(k), std::move(v));
 }
 
@@ -181,13 +178,11 @@ PyObject* kv4_attention(PyObject* const* arg) {
   const size_t need = entry<decltype(awq_kv4_attention_workspace_size)>(arg[1])(batch, heads, max_q, &cfg);
   at::Tensor out = fresh({T, heads, D}, *q, q->scalar_type()), ws = fresh({need > 256 ? (int64_t)need : 256}, *q, at::kByte), lse;
   if (with_lse) lse = fresh({T, heads}, *q, at::kFloat);
-  const awq_status st = run([&] {
-    return entry<decltype(awq_kv4_attention)>(arg[0])(
-        q->data_ptr(), code, q->stride(0), q->stride(1), T, heads, start ? (const int32_t*)start->data_ptr() : nullptr, max_q,
-        cache->data_ptr(), cache->size(0), (const int32_t*)table->data_ptr(), table->size(1),
-        (const int32_t*)lens->data_ptr(), batch, (float)scale, &cfg, out.data_ptr(),
-        with_lse ? (float*)lse.data_ptr() : nullptr, ws.data_ptr(), (size_t)ws.numel(), here.stream());
-  });
+  const awq_status st = run<decltype(awq_kv4_attention)>(
+      arg[0], q->data_ptr(), code, q->stride(0), q->stride(1), T, heads, start ? (const int32_t*)start->data_ptr() : nullptr,
+      max_q, cache->data_ptr(), cache->size(0), (const int32_t*)table->data_ptr(), table->size(1),
+      (const int32_t*)lens->data_ptr(), batch, (float)scale, &cfg, out.data_ptr(),
+      with_lse ? (float*)lse.data_ptr() : nullptr, ws.data_ptr(), (size_t)ws.numel(), here.stream());
   if (with_lse) return pair(st, std::move(out), std::move(lse));
   return st != AWQ_OK ? PyLong_FromLong(st) : THPVariable_Wrap(std::move(out));
 }
