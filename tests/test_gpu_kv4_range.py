@@ -69,3 +69,51 @@ def test_prompt_reference_outgrown_in_the_second_half_of_a_tile(dtype, dim, grou
     q = (1.5 * c + _rand((2 * n, heads * share, dim), dtype, 240, 0.05).float()).to(DT[dtype])
     out, lse = _attend(q, cache, table, lens, cfg, n)
     _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, n, 2 * n], share, dim ** -0.5, dtype, True)
+
+
+def _low(lens_l, heads, dim, group, page, dtype, seed, nats, where, qual=1.5):
+    """A cache whose tokens `where` (a slice of each sequence) have keys that score about -nats with q of about qual."""
+    cfg, cache, table, lens, slots = _fill(lens_l, heads, dim, group, page, dtype, seed, kscale=0.05)
+    at = 0
+    for n in lens_l:
+        mine = slots[at:at + n][where]
+        at += n
+        if len(mine):
+            k = (-nats / (qual * dim ** 0.5) * (1 + 0.01 * _rand((len(mine), heads, dim), "bf16", seed + 1).float()))
+            _write(cache, cfg, mine, k.to(DT[dtype]), _rand((len(mine), heads, dim), dtype, seed + 2))
+    return cfg, cache, table, lens, slots
+
+
+@pytest.mark.parametrize("nats", [60, 100, 200, 1000])
+@pytest.mark.parametrize("dim,group,share", [(64, 32, 1), (64, 64, 12), (96, 32, 2), (128, 128, 4), (128, 32, 16), (256, 128, 3)])
+def test_all_scores_far_below_zero(dim, group, share, nats):
+    """The softmax does not care: one token, a few, contexts cut between warps and blocks (16-row tiles where share > 8)."""
+    dtype = "bf16" if share % 2 else "f16"
+    lens_l = [1, 5, 33, 700, 2600]
+    cfg, cache, table, lens, slots = _low(lens_l, 2, dim, group, 16, dtype, 250, nats, slice(None))
+    q = (1.5 + _rand((5, 2 * share, dim), dtype, 251, 0.01).float()).to(DT[dtype])
+    out, lse = awq.kv4_attention(q, cache, table, lens, cfg, lse=True)
+    _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, range(6), share, dim ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("nats", [100, 1000])
+@pytest.mark.parametrize("where", [slice(0, 32), slice(0, 64), slice(64, 640), slice(32, None), slice(1000, 1064)])
+@pytest.mark.parametrize("dim,share", [(64, 4), (128, 12), (256, 2)])
+def test_some_scores_far_below_zero(dim, share, where, nats):
+    """The first tokens, whole ranges of a warp, or all but the first, beside ordinary ones."""
+    lens_l = [40, 1100, 5000]
+    cfg, cache, table, lens, slots = _low(lens_l, 2, dim, dim // 2, 32, "f16", 260, nats, where)
+    q = (1.5 + _rand((3, 2 * share, dim), "f16", 261, 0.01).float()).half()
+    out, lse = awq.kv4_attention(q, cache, table, lens, cfg, lse=True)
+    _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, range(4), share, dim ** -0.5, "f16")
+
+
+@pytest.mark.parametrize("nats", [100, 1000])
+@pytest.mark.parametrize("where", [slice(None), slice(0, 32), slice(0, 64), slice(70, 300)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_prompt_scores_far_below_zero(dtype, where, nats):
+    lens_l, n = [300, 170], 150
+    cfg, cache, table, lens, slots = _low(lens_l, 10, 128, 128, 32, dtype, 270, nats, where)
+    q = (1.5 + _rand((2 * n, 40, 128), dtype, 271, 0.01).float()).to(DT[dtype])
+    out, lse = _attend(q, cache, table, lens, cfg, n)
+    _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, n, 2 * n], 4, 128 ** -0.5, dtype, True)

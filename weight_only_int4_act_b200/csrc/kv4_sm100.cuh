@@ -641,8 +641,9 @@ struct Kv4Warp {
         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
         if (up == -INFINITY) up = 0.0f;
-        // (d moves by what m really moved)
-        const float mn = m[u][c] + up, by = mn - m[u][c], f = exp2_fast(-by);
+        // (d moves by what m really moved; a fresh state holds zeros, and its
+        // reference may fall by any amount)
+        const float mn = m[u][c] + up, by = mn - m[u][c], f = fresh ? 1.0f : exp2_fast(-by);
         m[u][c] = mn;
         l[u][c] *= f;
 #pragma unroll
