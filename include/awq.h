@@ -401,8 +401,9 @@ awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const int32_t* slo
  * kernel). Scores, softmax statistics and output sums are fp32; the weights
  * (probability times value step) enter the tensor cores in fp16, and for bf16
  * queries of more than 64 rows a sequence (tokens times query heads of a kv
- * head) the keys and values (code - zero) * step do too, each rounded once
- * relative to its strip's largest step; for fp16 ones the values alone. A row
+ * head) the keys and values (code - zero) * step do too, each rounded once (by
+ * half an fp16 step of itself, or 2^-35 of the largest step among 16 tokens
+ * where that is more); for fp16 ones the values alone. A row
  * that sees a key with step NaN is NaN, one that sees a value with step NaN is
  * NaN in that group's channels at least. The same call gives the same bits
  * each time; another batch around a sequence may cut its context elsewhere.

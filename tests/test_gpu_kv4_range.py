@@ -117,3 +117,37 @@ def test_prompt_scores_far_below_zero(dtype, where, nats):
     q = (1.5 + _rand((2 * n, 40, 128), dtype, 271, 0.01).float()).to(DT[dtype])
     out, lse = _attend(q, cache, table, lens, cfg, n)
     _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, n, 2 * n], 4, 128 ** -0.5, dtype, True)
+
+
+# ---------------------------------------------------------------- value steps of very different sizes
+@pytest.mark.parametrize("ratio", [10, 14, 17, 20])
+@pytest.mark.parametrize("seen", [True, False])
+@pytest.mark.parametrize("dtype,group", [("bf16", 128), ("bf16", 32), ("f16", 128)])
+def test_prompt_one_value_huge_and_unlikely(dtype, group, seen, ratio):
+    """A token whose value step is 2^ratio times the others', whose probability is about nothing, or which most rows do not
+    see: the others' part keeps its digits."""
+    heads, n, L = 20, 150, 200
+    for where in ((3, 40, 100) if seen else (L - 2, L - 40)):
+        cfg, cache, table, lens, slots = _fill([L, L], heads, 128, group, 16, dtype, 280, vscale=2.0 ** -8)
+        k = torch.full((1, heads, 128), -4.0 if seen else 0.1, dtype=DT[dtype], device="cuda")
+        v = _rand((1, heads, 128), dtype, 281, 2.0 ** (ratio - 8))
+        for b in (0, 1):
+            _write(cache, cfg, slots[b * L + where:b * L + where + 1], k, v)
+        q = (1.5 + _rand((2 * n, 2 * heads, 128), dtype, 282, 0.2).float()).to(DT[dtype])
+        out, lse = _attend(q, cache, table, lens, cfg, n)
+        parts = _read(cache, cfg, slots)
+        _check(out, lse, q, cfg, parts, [L, L], [0, n, 2 * n], 2, 128 ** -0.5, dtype, True)
+
+
+@pytest.mark.parametrize("dtype,dim,group", [("bf16", 128, 128), ("bf16", 64, 32), ("f16", 64, 64)])
+def test_prompt_value_steps_of_all_sizes(dtype, dim, group):
+    """Every token's values have a size of their own, over 2^22; scores spread as well."""
+    heads, n, lens_l = 10, 130, [420, 333]
+    cfg, cache, table, lens, slots = _fill(lens_l, heads, dim, group, 64, dtype, 290)
+    g = torch.Generator(device="cuda").manual_seed(291)
+    size = torch.exp2(22 * torch.rand((len(slots), heads, 1), generator=g, device="cuda") - 10)
+    k, v = _rand((len(slots), heads, dim), dtype, 292), _rand((len(slots), heads, dim), dtype, 293)
+    _write(cache, cfg, slots, k, (v.float() * size).clamp(-30000, 30000).to(DT[dtype]))
+    q = _rand((2 * n, 4 * heads, dim), dtype, 294, 2.0)
+    out, lse = _attend(q, cache, table, lens, cfg, n)
+    _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, n, 2 * n], 4, dim ** -0.5, dtype, True)

@@ -8,20 +8,26 @@
 // the next tile's scores are there when a softmax ends; W_q takes the place of
 // its S_q).
 //
-// Values are unpacked as (code - zero) step 2^(10 - e), e the exponent of the
-// largest step in the strip of 16 tokens: one rounding to fp16 (2^-11) of each
-// value, without overflow or underflow whatever the steps are; e joins the
-// weight's exponent, w = 2^(score + e - m), and leaves the sum of the p again, a
-// strip at a time. Keys the same, the strip's power of two going into the
+// Values are unpacked as (code - zero) step 2^(10 - e): one rounding to fp16 of
+// each value, off by 2^-11 of it or, where it is far below, 2^-35 of 2^e; e joins
+// the weight's exponent, w = 2^(score + e - m), and leaves the sum of the p again.
+// e is the exponent of the largest step in the strip of 16 tokens where those of
+// its tokens lie within KVP_SPREAD of each other, so that the softmax has one
+// number a strip; in other strips each token has its own, and the softmax takes
+// the way that looks at every token. A row's reference m thus follows what its
+// tokens weigh, p times step, to KVP_SPREAD: a token of a huge step and no
+// probability does not push the others out of fp16's range. Keys have their
+// strip's largest step always (what the small ones lose there is at most 2^-20
+// |q| a channel of a score): that power of two goes into the
 // factor of its scores; but for fp16 queries (EXACT; one group a head), whose
 // output resolves it, the codes less zeros (-15 .. 15) are the keys, exactly, and
 // each score is multiplied by its token's step in fp32 (2 x 2048 queries of 8000
-// tokens, 32 heads over 8 of 128, bf16: 474 us that way, 442 with folded keys; one
+// tokens, 32 heads over 8 of 128, bf16: 474 us that way where folded keys took 442; one
 // read of a step from shared memory a score, beside the MMAs' operands).
 // A token one of whose groups holds NaN turns the rows that see it to NaN.
 //
-// Measured: 2 x 2048 queries of up to 8000 tokens, 32 heads over 8 of 128: 442 us,
-// 752 TFLOP/s (202 us at the bf16 rate). A context tile takes a block about 2200
+// Measured: 2 x 2048 queries of up to 8000 tokens, 32 heads over 8 of 128: 451 us,
+// 741 TFLOP/s (202 us at the bf16 rate). A context tile takes a block about 2200
 // cycles. Its MMAs are 1024 cycles' work and take 1560, as N = 64 costs what
 // N = 128 does (64 to 67 cycles); beside them go the exponentials of 16384 scores
 // on 8 warps and the handshakes between loader, unpacking, products and softmax,
@@ -40,11 +46,17 @@ namespace awq {
 
 constexpr int KVP_ROWS = 256, KVP_TOK = 64, KVP_THREADS = 480, KVP_STAGES = 3, KVP_RAW = 5;
 constexpr int KVP_MIN_ROWS = 64;  // sequences of at most so many rows are the split kernel's
-// The reference exponent may lag behind the largest score by this: weights then
-// reach 2^15, which fp16 holds, and are as exact as below 1; what falls below
-// 2^-24 of 1 does so beside a weight of at least 1. (With 8, one tile in eight
-// had a warp that stopped to rescale.)
-constexpr float KVP_LAG = 14.0f;
+// How far apart the exponents of the tokens' largest steps may lie in a strip that
+// has one for all of them.
+constexpr int KVP_SPREAD = 2;
+// The reference is whole, so that what is scaled when it moves keeps its digits,
+// and is set such that the row's largest weight then lies in (2^3, 2^4]: with
+// KVP_SPREAD and a step's mantissa taken off, its largest p step is 1 or more, and
+// what falls below fp16's 2^-24 does so beside that. It may lag behind by KVP_LAG:
+// weights then reach 2^15, which fp16 holds. (2 x 2048 queries of 8000 tokens: 451
+// us; with a spread of 3, and so 2^5, 458; with an exponent a token in every
+// strip 478; with one a strip and 2^0, whatever the steps, 442.)
+constexpr float KVP_HEAD = 4.0f, KVP_LAG = 15.0f;
 constexpr int ERR_KVP_RAW = 0x601, ERR_KVP_FREE = 0x602, ERR_KVP_SCORE = 0x603, ERR_KVP_WEIGHT = 0x604, ERR_KVP_OUT = 0x605,
               ERR_KVP_TILE = 0x606;
 
@@ -54,10 +66,11 @@ struct KvpArgs {
 };
 
 // What the softmax knows of a strip: its keys are (code - zero) step / key, its
-// values (code - zero) step 2^(10 - e), down = 2^-e; tokens (by bit) that hold NaN.
+// values (code - zero) step 2^(10 - e), down = 2^-e. odd: tokens (by bit) that hold
+// NaN, and bit 16 where each token has an e of its own (KvpSmem::e).
 struct KvpStrip {
   float key, e, down;
-  unsigned nan;
+  unsigned odd;
 };
 
 template <int D, int G>
@@ -70,6 +83,7 @@ struct KvpSmem {
   alignas(128) uint8_t raw[KVP_RAW][4 * STRIP];
   alignas(16) KvpStrip strip[KVP_STAGES][4];
   float step[KVP_STAGES][KVP_TOK];   // EXACT: key step of a token
+  float e[KVP_STAGES][KVP_TOK];      // exponent of a token's values
   float unit[2][128];                // score (log2) per unit of a row's product
   int lost_raw[KVP_RAW], lost[KVP_STAGES];  // strips (by bit) in pages outside the cache
   uint64_t raw_full[KVP_RAW], raw_empty[KVP_RAW], tile_full[KVP_STAGES], tile_empty[KVP_STAGES];
@@ -333,17 +347,25 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
         most = fmaxf(most, x);
       }
       const bool there = !lost && t0 + lt < seq.L;  // (else its bytes may hold anything)
-      int e = there && !nan ? (int)(__float_as_uint(most) >> 23) - 127 : -24;
+      const bool sized = there && !nan;
+      int e = sized ? (int)(__float_as_uint(most) >> 23) - 127 : -24;
+      // the largest e and the least (as 256 less it) over the half warp, two 16-bit numbers in a word
+      uint32_t ends = (uint32_t)(e + 128) << 16 | (sized ? (uint32_t)(128 - e) : 0u);
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, d));
+      for (int d = 1; d < 16; d <<= 1) ends = __vmaxu2(ends, __shfl_xor_sync(0xffffffffu, ends, d));
       const unsigned nans = __ballot_sync(0xffffffffu, there && nan);
-      const int ek = __shfl_sync(0xffffffffu, e, 0), ev = __shfl_sync(0xffffffffu, e, 16);
+      const uint32_t ends_v = __shfl_sync(0xffffffffu, ends, 16);
+      const int ek = (int)(__shfl_sync(0xffffffffu, ends, 0) >> 16) - 128, ev = (int)(ends_v >> 16) - 128;
+      const bool each = ev + (int)(ends_v & 0xffffu) > 128 + KVP_SPREAD;
+      if (!each) e = ev;  // (lanes 16 .. have the values' tokens)
       if (EXACT && lane < 16) sm.step[ring.stage][16 * u + lane] = there ? most : 0.0f;
+      if (lane >= 16) sm.e[ring.stage][16 * u + lt] = (float)e;
       if (lane == 0)
         sm.strip[ring.stage][u] = KvpStrip{EXACT ? 1.0f : __uint_as_float((uint32_t)(117 + ek) << 23), (float)ev,
-                                           __uint_as_float((uint32_t)(127 - ev) << 23), (nans | nans >> 16) & 0xffffu};
+                                           __uint_as_float((uint32_t)(127 - ev) << 23),
+                                           ((nans | nans >> 16) & 0xffffu) | (each ? 0x10000u : 0u)};
       if (u == 0 && lane == 0) sm.lost[ring.stage] = sm.lost_raw[raw.stage];
-      const float kup = __uint_as_float((uint32_t)(137 - ek) << 23), vup = __uint_as_float((uint32_t)(137 - ev) << 23);
+      const float kup = __uint_as_float((uint32_t)(137 - ek) << 23);
       // (step times its strip's power of two, zero) of a token's group; nothing where its bytes may hold anything or NaN
       const unsigned dead = (nans | nans >> 16) | (lost ? 0xffffu : t0 + 16 > seq.L ? 0xffffu << max(seq.L - t0, 0) : 0u);
       auto param = [&](const uint32_t* par, int gi, int t, float up) -> float2 {
@@ -375,14 +397,22 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       // values: rows are channels, 64 tokens of 2 bytes; a lane writes pairs of tokens
       const uint2* vw = reinterpret_cast<const uint2*>(s + 8 * D) + lane;
       const int ta = 2 * q4, tb = ta + 8;
+      float vup[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vup[i] = __uint_as_float((uint32_t)(137 - ev) << 23);
+      if (each) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vup[i] = __uint_as_float((uint32_t)(137 - __shfl_sync(0xffffffffu, e, 16 + (i & 1) + (i < 2 ? ta : tb))) << 23);
+      }
       uint2 w2[NJ];
       __half2 vz0[NG], vz1[NG], vm0[NG], vm1[NG];
 #pragma unroll
       for (int p = 0; p < NJ; ++p) w2[p] = vw[32 * p];
 #pragma unroll
       for (int gi = 0; gi < NG; ++gi) {
-        const float2 a0 = param(vpar, gi, ta, vup), a1 = param(vpar, gi, ta + 1, vup), b0 = param(vpar, gi, tb, vup),
-                     b1 = param(vpar, gi, tb + 1, vup);
+        const float2 a0 = param(vpar, gi, ta, vup[0]), a1 = param(vpar, gi, ta + 1, vup[1]), b0 = param(vpar, gi, tb, vup[2]),
+                     b1 = param(vpar, gi, tb + 1, vup[3]);
         vm0[gi] = __floats2half2_rn(a0.x, a1.x);
         vz0[gi] = __floats2half2_rn(a0.y, a1.y);
         vm1[gi] = __floats2half2_rn(b0.x, b1.x);
@@ -500,7 +530,7 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       for (int c = 0; c < 2; ++c) {
         const KvpStrip f[2] = {strip[2 * c], strip[2 * c + 1]};
         const unsigned off = lost >> (2 * c) & 3u;
-        const bool odd = __any_sync(0xffffffffu, t0 + 32 * c + 32 > vis) || off || f[0].nan || f[1].nan;
+        const bool odd = __any_sync(0xffffffffu, t0 + 32 * c + 32 > vis) || off || f[0].odd || f[1].odd;
         uint32_t s[32], wbits[16];
         tmem_ld_32x32b_x32(col + 32 * c, s);
         tmem_ld_wait();
@@ -529,23 +559,26 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
             sum = fmaf(part.x + part.y, f[h].down, sum);
           }
           const float2 top2 = __half22float2(big);
-          done = !__any_sync(0xffffffffu, fmaxf(top2.x, top2.y) > 32768.0f);
+          done = !__any_sync(0xffffffffu, fmaxf(top2.x, top2.y) > 65504.0f);
         }
         if (!done) {
-          // The first tokens, some that a row does not see, NaN, and scores that
-          // outgrow the reference: the row's largest exponent first.
+          // The first tokens, some that a row does not see, NaN, steps of very
+          // different sizes, and scores that outgrow the reference: the row's
+          // largest exponent first.
           auto score = [&](int k) {
             return __uint_as_float(s[k]) * (EXACT ? sm.step[ring.stage][32 * c + k] : 1.0f);
           };
+          const float* e = sm.e[ring.stage] + 32 * c;
           auto hidden = [&](int k) { return t0 + 32 * c + k >= vis || (off >> (k >> 4) & 1u); };
           float want = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (!hidden(k)) want = fmaxf(want, fmaf(score(k), unit * f[k >> 4].key, f[k >> 4].e));
+            if (!hidden(k)) want = fmaxf(want, fmaf(score(k), unit * f[k >> 4].key, e[k]));
           float scale = 1.0f;
           if (want > m + KVP_LAG) {
-            scale = exp2_fast(m - want);
-            m = want;
+            const float to = ceilf(want) - KVP_HEAD, by = to - m;  // (2^-by exactly; 0 from 127 on)
+            scale = __uint_as_float((uint32_t)(127 - (int)fminf(by, 127.0f)) << 23);
+            m = to;
             l *= scale;
           }
           if (__any_sync(0xffffffffu, scale != 1.0f)) {
@@ -587,9 +620,10 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
             float w[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              w[i] = g.nan >> ((k + i) & 15) & 1u ? __int_as_float(0x7fffffff) : exp2_fast(fmaf(score(k + i), unit * g.key, g.e - m));
+              const float et = e[k + i];
+              w[i] = g.odd >> ((k + i) & 15) & 1u ? __int_as_float(0x7fffffff) : exp2_fast(fmaf(score(k + i), unit * g.key, et - m));
               if (hidden(k + i)) w[i] = 0.0f;
-              sum = fmaf(w[i], g.down, sum);
+              sum = fmaf(w[i], __uint_as_float((uint32_t)(127 - (int)et) << 23), sum);
             }
             wbits[k >> 1] = pack2<true>(w[0], w[1]);
           }
