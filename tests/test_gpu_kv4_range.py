@@ -151,3 +151,26 @@ def test_prompt_value_steps_of_all_sizes(dtype, dim, group):
     q = _rand((2 * n, 4 * heads, dim), dtype, 294, 2.0)
     out, lse = _attend(q, cache, table, lens, cfg, n)
     _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, n, 2 * n], 4, dim ** -0.5, dtype, True)
+
+
+# ---------------------------------------------------------------- pages that are not there, contexts never written
+@pytest.mark.parametrize("dim,group,share", [(64, 32, 1), (64, 64, 12), (96, 32, 2), (128, 128, 4), (128, 32, 2), (128, 128, 12),
+                                             (256, 128, 3)])
+def test_lost_pages_of_16_tokens(dim, group, share):
+    """Every other page lost, the first among them, and scores of about -60: the tokens that are there keep their weights."""
+    lens_l = [300, 2000]
+    cfg, cache, table, lens, slots = _low(lens_l, 2, dim, group, 16, "f16", 310, 40, slice(None))
+    lost = table.clone()
+    lost[:, ::2] = -1
+    q = (1.5 + _rand((2, 2 * share, dim), "f16", 311, 0.01).float()).half()
+    work = awq.workspace(awq.kv4_attention_workspace_size(2, 2 * share, 1, cfg))
+    out, lse = awq.kv4_attention(q, cache, lost, lens, cfg, ws=work, lse=True)
+    with pytest.raises(awq.AwqError, match="DEVICE"):
+        awq.workspace_error(work)
+    keep, kept, at = [], [], 0
+    for n in lens_l:
+        mine = slots[at:at + n]
+        at += n
+        keep.append(mine[np.arange(n) // 16 % 2 == 1])
+        kept.append(len(keep[-1]))
+    _check(out, lse, q, cfg, _read(cache, cfg, np.concatenate(keep)), kept, range(3), share, dim ** -0.5, "f16")

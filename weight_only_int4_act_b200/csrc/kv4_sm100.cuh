@@ -818,8 +818,9 @@ struct Kv4Warp {
 #pragma unroll 1
       for (int s = 0; s < 2; ++s) {
         if (t0 + 16 * s >= vis_max) break;
-        if (t0 + 16 * s + 16 > vis_min || drop)
-          strips<true, 1>(base + s * STRIP, t0 + 16 * s, drop >> s, lane);
+        if (drop >> s & 1u) continue;  // (it would set the reference to nothing)
+        if (t0 + 16 * s + 16 > vis_min)
+          strips<true, 1>(base + s * STRIP, t0 + 16 * s, 0, lane);
         else
           strips<false, 1>(base + s * STRIP, t0 + 16 * s, 0, lane);
       }
