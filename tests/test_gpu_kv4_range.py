@@ -174,3 +174,25 @@ def test_lost_pages_of_16_tokens(dim, group, share):
         keep.append(mine[np.arange(n) // 16 % 2 == 1])
         kept.append(len(keep[-1]))
     _check(out, lse, q, cfg, _read(cache, cfg, np.concatenate(keep)), kept, range(3), share, dim ** -0.5, "f16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [1, 9, 130])
+def test_contexts_never_written(new, dim, dtype):
+    """A fresh cache holds zeros: keys and values of 0, of the same weight as any other token with a score of 0; alone,
+    before written tokens and behind them."""
+    heads, share = 10, 3
+    for written in (slice(0, 0), slice(64, None), slice(0, 40)):
+        lens_l = [140, 333]
+        cfg, cache, table, lens, slots = _fill(lens_l, heads, dim, dim, 16, dtype, 320)
+        cache.zero_()
+        at = 0
+        for n in lens_l:
+            mine = slots[at:at + n][written]
+            at += n
+            if len(mine):
+                _write(cache, cfg, mine, _rand((len(mine), heads, dim), dtype, 321), _rand((len(mine), heads, dim), dtype, 322))
+        q = _rand((2 * new, heads * share, dim), dtype, 323)
+        out, lse = _attend(q, cache, table, lens, cfg, new)
+        _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, new, 2 * new], share, dim ** -0.5, dtype, new > 20)

@@ -348,7 +348,8 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       }
       const bool there = !lost && t0 + lt < seq.L;  // (else its bytes may hold anything)
       const bool sized = there && !nan;
-      int e = sized ? (int)(__float_as_uint(most) >> 23) - 127 : -24;
+      // (the quantiser's steps are 2^-24 or more; 0 is a token never written)
+      int e = sized ? max((int)(__float_as_uint(most) >> 23) - 127, -24) : -24;
       // the largest e and the least (as 256 less it) over the half warp, two 16-bit numbers in a word
       uint32_t ends = (uint32_t)(e + 128) << 16 | (sized ? (uint32_t)(128 - e) : 0u);
 #pragma unroll

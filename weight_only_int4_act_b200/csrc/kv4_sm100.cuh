@@ -628,7 +628,8 @@ struct Kv4Warp {
         float x = dv[s][0][h];
 #pragma unroll
         for (int gi = 1; gi < NG; ++gi) x = fmaxf(x, dv[s][gi][h]);
-        e[s][h] = (float)((int)(__float_as_uint(x) >> 23) - 127);
+        // (the quantiser's steps are 2^-24 or more; 0 is a token never written)
+        e[s][h] = (float)max((int)(__float_as_uint(x) >> 23) - 127, -24);
       }
 #pragma unroll
     for (int u = 0; u < NT; ++u)
