@@ -153,6 +153,35 @@ def test_prompt_value_steps_of_all_sizes(dtype, dim, group):
     _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, n, 2 * n], 4, dim ** -0.5, dtype, True)
 
 
+@pytest.mark.parametrize("new", [1, 4])
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 32), (128, 64), (256, 64)])
+def test_quiet_group_beside_a_loud_one(dim, group, new):
+    """Values of one group 2^21 times the others': the quiet groups keep their own digits. A row's largest weight (probability
+    times its loudest step) is at least 2^6 in the kernel's units, so half of fp16's smallest subnormal is at most 2^-31 of
+    it: that bound in the place of 2^-25, everything else by the group's own values."""
+    L, heads, share = 7, 2, 2
+    cfg, cache, table, lens, slots = _fill([L], heads, dim, group, 16, "f16", 300)
+    k = _rand((L, heads, dim), "f16", 301, 0.2)
+    v = _rand((L, heads, dim), "f16", 302, 2.0 ** -8)
+    v[..., :group] *= 2.0 ** 21
+    _write(cache, cfg, slots, k, v)
+    q = _rand((new, heads * share, dim), "f16", 303)
+    out, _ = _attend(q, cache, table, lens, cfg, new)
+    (kc, ks, kz), (vc, vs, vz) = _read(cache, cfg, slots)
+    kk, vv = S.four_bit_values(kc, ks, kz), S.four_bit_values(vc, vs, vz)
+    ref, _, p = S.attention(_f64(q), kk, vv, share, dim ** -0.5, L - new + 1)
+    rep = lambda a: np.repeat(a, group, axis=-1)  # noqa: E731
+    size = (vc + rep(vz)) * rep(vs)
+    for e in range(heads * share):
+        h, pe = e // share, p[:, e]
+        top = (pe * vs[:, h].max(axis=-1)).max(axis=1, keepdims=True)
+        codes = (pe > 0).astype(float) @ (vc + rep(vz))[:, h]
+        # e_t below 2^-9 for these keys (the largest ds_t of test_gpu_kv4's bound: 272 2^-22 / 16 * 256 * 0.8 at D = 256, |k| + its
+        # zero of 1 at most); half steps of 2^-11 of the weights and of the result
+        tol = 1.1 * ((2.0 ** -11 + 2.0 ** -9) * (np.abs(ref[:, e]) + pe @ size[:, h]) + 2.0 ** -31 * top * codes) + 2.0 ** -25
+        assert (np.abs(_f64(out)[:, e] - ref[:, e]) <= tol).all()
+
+
 # ---------------------------------------------------------------- pages that are not there, contexts never written
 @pytest.mark.parametrize("dim,group,share", [(64, 32, 1), (64, 64, 12), (96, 32, 2), (128, 128, 4), (128, 32, 2), (128, 128, 12),
                                              (256, 128, 3)])

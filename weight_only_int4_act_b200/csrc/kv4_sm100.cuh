@@ -498,6 +498,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 constexpr int KV4_UNIT = 32;       // tokens a warp takes at a time: two strips
 constexpr int KV4_RECENTRE = 4;    // units between recentre()s
+constexpr float KV4_HEAD = 6.0f;   // the largest weight's exponent where a reference is taken
 constexpr float KV4_LOWEST = -1.7e38f;  // reference exponent of a part that saw no token
 
 // What a warp knows of a tile of 8 NT query rows of one (sequence, kv head).
@@ -614,10 +615,13 @@ struct Kv4Warp {
 
   // Reference exponents that admit these scores (d: score - m; dv: value
   // steps of the lane's two tokens a strip): the largest score plus the
-  // exponent of its token's value step, so that w = p step <= 2 whatever the
-  // steps are. Moves d along. Taken for a tile's first tokens and then only
-  // when a weight passes 2^8. (A column that sees none of a tile's first tokens
-  // sees none of the later ones either: rows see a prefix of the context.)
+  // exponent of its token's value step, less KV4_HEAD, so that the largest
+  // w = p step lies in [2^6, 2^7) whatever the steps are. Moves d along. Taken for
+  // a tile's first tokens and then only when a weight passes 2^15, so the largest
+  // weight of a row is never below 2^6: groups whose steps are 2^20 below the
+  // loudest one's have weights of fp16's full precision still. (A column that sees
+  // none of a tile's first tokens sees none of the later ones either: rows see a
+  // prefix of the context.)
   template <int N>
   __device__ __forceinline__ void raise(float (&d)[N][NT][4], const float (&dv)[N][NG][2]) {
     float e[N][2];
@@ -637,7 +641,7 @@ struct Kv4Warp {
       for (int c = 0; c < 2; ++c) {
         float up = fresh ? -INFINITY : 0.0f;
 #pragma unroll
-        for (int s = 0; s < N; ++s) up = fmaxf(up, fmaxf(d[s][u][c] + e[s][0], d[s][u][c + 2] + e[s][1]));
+        for (int s = 0; s < N; ++s) up = fmaxf(up, fmaxf(d[s][u][c] + e[s][0], d[s][u][c + 2] + e[s][1]) - KV4_HEAD);
         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
         up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
@@ -767,7 +771,7 @@ struct Kv4Warp {
             for (int gi = 0; gi < NG; ++gi) {
               const float x = p[s][u][i] * dv[s][gi][i >> 1];
               w[s][u][gi][i] = hidden[s][u][i] ? 0.0f : x;
-              big |= w[s][u][gi][i] > 256.0f;
+              big |= w[s][u][gi][i] > 32768.0f;
             }
           }
       return fresh || __any_sync(0xffffffffu, big);
