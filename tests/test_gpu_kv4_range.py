@@ -225,3 +225,19 @@ def test_contexts_never_written(new, dim, dtype):
         q = _rand((2 * new, heads * share, dim), dtype, 323)
         out, lse = _attend(q, cache, table, lens, cfg, new)
         _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, new, 2 * new], share, dim ** -0.5, dtype, new > 20)
+
+
+@pytest.mark.parametrize("new", [1, 130])
+@pytest.mark.parametrize("dim,share", [(64, 2), (128, 12), (256, 2)])
+def test_contexts_written_in_part_with_scores_far_below_zero(dim, share, new):
+    """Tokens never written (score 0) outweigh by far all that is written before them."""
+    lens_l = [140, 1500]
+    for first in (35, 100):
+        cfg, cache, table, lens, slots = _low(lens_l, 10, dim, dim // 2, 16, "f16", 330, 200, slice(None))
+        part = np.concatenate([slots[:first], slots[140:140 + first]])
+        k, v = awq.kv4_gather(cache, torch.from_numpy(part).int().cuda(), cfg, dtype=torch.float16)
+        cache.zero_()
+        _write(cache, cfg, part, k, v)
+        q = (1.5 + _rand((2 * new, 10 * share, dim), "f16", 331, 0.01).float()).half()
+        out, lse = _attend(q, cache, table, lens, cfg, new)
+        _check(out, lse, q, cfg, _read(cache, cfg, slots), lens_l, [0, new, 2 * new], share, dim ** -0.5, "f16", new > 20)

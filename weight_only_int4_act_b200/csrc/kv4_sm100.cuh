@@ -733,7 +733,9 @@ struct Kv4Warp {
       for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          dv[s][gi][h] = __low2float(*reinterpret_cast<const __half2*>(vpar + 16 * gi + 8 * h + g));
+          // (a token never written has step 0; the 2^-60, which is lost in any other
+          // step, lets it outgrow the reference too, as its probability counts)
+          dv[s][gi][h] = __low2float(*reinterpret_cast<const __half2*>(vpar + 16 * gi + 8 * h + g)) + 8.673617379884035e-19f;
           const uint2 pz = *reinterpret_cast<const uint2*>(vpar + 16 * gi + 8 * h + 2 * q);
           uint32_t z = __byte_perm(pz.x, pz.y, 0x7632);
           if (EDGE) {
