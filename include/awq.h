@@ -389,7 +389,8 @@ awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const int32_t* slo
  * Sequence b has q's rows q_start[b] .. q_start[b + 1] - 1 (q_start: DEVICE
  * int32 [batch + 1], not decreasing; NULL: one row a sequence) and a context
  * of lens[b] tokens (DEVICE int32 [batch]), its token i in page
- * table[b, i / page_size] (DEVICE int32 [batch, table_pages]). Its rows are
+ * table[b, i / page_size] (DEVICE int32 [batch, table_pages], table_pages *
+ * page_size < 2^31 - 128: AWQ_ERR_SHAPE). Its rows are
  * the last tokens of the context: row j of n sees the first lens[b] - n + 1 + j
  * tokens. A row that sees none gives zeros (lse -inf). Rows of q that belong
  * to no sequence are neither read nor written.

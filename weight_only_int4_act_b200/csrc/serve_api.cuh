@@ -386,7 +386,8 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
   awq_status st = check_kv4_attention(batch, n_q_heads, max_q, cfg);
   if (st != AWQ_OK) return st;
   if ((st = check_kv4_cache(cfg, cache, n_pages)) != AWQ_OK) return st;
-  if (T < 0 || T > (1 << 28) || table_pages < 1 || table_pages > INT32_MAX / cfg->page_size)
+  // (the kernels' token indices run on to the end of a tile of 64 and its neighbour in 32 bits)
+  if (T < 0 || T > (1 << 28) || table_pages < 1 || table_pages > (INT32_MAX - 128) / cfg->page_size)
     return AWQ_ERR_SHAPE;
   if (!q_start && (T < batch || max_q != 1)) return AWQ_ERR_SHAPE;
   if (!dtype_ok(dtype) || !strides_ok(q_tok, q_head) || !std::isfinite(scale)) return AWQ_ERR_INVALID_ARG;
