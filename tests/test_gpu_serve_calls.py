@@ -29,3 +29,23 @@ def test_tensors_without_storage_are_refused():
         with pytest.raises(RuntimeError):
             torch.func.vmap(f)(arg)
         assert awq.quantize_int8(x[0, 0])[0].shape == (4, 64)  # as before
+
+
+def test_strides_of_axes_of_one():
+    """The stride of an axis with one entry means nothing: a token's slice out of rows of an odd pitch, a lone head."""
+    cfg = awq.make_kv4(1, 64, 16)
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    slot = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v, q = (torch.randn((1, 1, 64), generator=g, device="cuda").bfloat16() for _ in range(3))
+    odd = [torch.empty_strided((1, 1, 64), (205, 77, 1), dtype=torch.bfloat16, device="cuda").copy_(t) for t in (k, v, q)]
+    assert odd[0].stride() == (205, 77, 1)
+    one, two = awq.kv4_new_cache(1, cfg), awq.kv4_new_cache(1, cfg)
+    awq.kv4_append(k, v, slot, one, cfg)
+    awq.kv4_append(odd[0], odd[1], slot, two, cfg)
+    assert torch.equal(one, two) and one.any()
+    out = torch.empty_like(q)
+    want = awq.kv4_attention(q, one, table, lens, cfg)
+    assert torch.equal(awq.kv4_attention(odd[2], one, table, lens, cfg), want) and want.any()
+    assert torch.equal(awq.kv4_attention(odd[2], one, table, lens, cfg, out=out), want)  # (the long way)
+    assert torch.equal(awq.quantize_int8(odd[0][0])[0], awq.quantize_int8(k[0])[0])

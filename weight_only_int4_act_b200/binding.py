@@ -490,6 +490,11 @@ def _req_rows(t, dtype, shape, dev, name):
         raise ValueError(f"{name} must be contiguous along its last axis")
 
 
+def _pitch(t, axis):
+    """Elements from one entry of an axis to the next (the stride of a single entry means nothing)."""
+    return t.stride(axis) if t.shape[axis] > 1 else 0
+
+
 def _code(dtype, codes, name):
     code = codes.get(dtype)
     if code is None:
@@ -654,10 +659,8 @@ def kv4_append(k, v, slots, cache, cfg: Kv4Cfg):
     _req_rows(v, k.dtype, shape, dev, "v")
     _req_here(slots, _torch().int32, (T,), dev, "slots")
     _req_cache(cache, cfg, dev)
-    k0, k1, _ = k.stride()
-    v0, v1, _ = v.stride()
-    st = lib().awq_kv4_append(k.data_ptr(), v.data_ptr(), dt, T, k0, k1, v0, v1, slots.data_ptr(), cache.data_ptr(),
-                              cache.shape[0], ctypes.byref(cfg), stream)
+    st = lib().awq_kv4_append(k.data_ptr(), v.data_ptr(), dt, T, _pitch(k, 0), _pitch(k, 1), _pitch(v, 0), _pitch(v, 1),
+                              slots.data_ptr(), cache.data_ptr(), cache.shape[0], ctypes.byref(cfg), stream)
     _check(st, "awq_kv4_append")
     return cache
 
@@ -743,9 +746,8 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
         ws = _scratch(q, kv4_attention_workspace_size(batch, n_q_heads, max_q, cfg))
     else:
         _same_device(ws, dev, "ws")
-    q0, q1, _ = q.stride()
-    st = lib().awq_kv4_attention(q.data_ptr(), dt, q0, q1, T, n_q_heads, None if q_start is None else q_start.data_ptr(),
-                                 max_q, cache.data_ptr(), cache.shape[0], table.data_ptr(), table.shape[1],
+    st = lib().awq_kv4_attention(q.data_ptr(), dt, _pitch(q, 0), _pitch(q, 1), T, n_q_heads,
+                                 None if q_start is None else q_start.data_ptr(), max_q, cache.data_ptr(), cache.shape[0], table.data_ptr(), table.shape[1],
                                  lens.data_ptr(), batch, D ** -0.5 if scale is None else float(scale),
                                  ctypes.byref(cfg), out.data_ptr(), lse_t.data_ptr() if lse else None, ws.data_ptr(),
                                  ws.numel() * ws.element_size(), stream)

@@ -46,6 +46,8 @@ bool rows(const at::Tensor* t, int64_t dim, awq_dtype& code) {
   code = t->scalar_type() == at::kHalf ? AWQ_DTYPE_F16 : AWQ_DTYPE_BF16;
   return true;
 }
+// elements from one entry of an axis to the next (the stride of a single entry means nothing)
+int64_t pitch(const at::Tensor* t, int64_t axis) { return t->size(axis) > 1 ? t->stride(axis) : 0; }
 bool cache_of(const at::Tensor* t, const awq_kv4cfg& c) {
   if (c.group < 1 || c.head_dim < 1 || c.page_size < 1 || !is(t, at::kInt, 3)) return false;
   return t->size(1) == c.n_kv_heads &&
@@ -136,7 +138,7 @@ PyObject* kv4_append(PyObject* const* arg) {
       !cache_of(cache, cfg))
     return none();
   return PyLong_FromLong(run<decltype(awq_kv4_append)>(
-      arg[0], k->data_ptr(), v->data_ptr(), code, T, k->stride(0), k->stride(1), v->stride(0), v->stride(1),
+      arg[0], k->data_ptr(), v->data_ptr(), code, T, pitch(k, 0), pitch(k, 1), pitch(v, 0), pitch(v, 1),
       (const int32_t*)slots->data_ptr(), cache->data_ptr(), cache->size(0), &cfg, here.stream()));
 }
 
@@ -179,7 +181,7 @@ PyObject* kv4_attention(PyObject* const* arg) {
   at::Tensor out = fresh({T, heads, D}, *q, q->scalar_type()), ws = fresh({need > 256 ? (int64_t)need : 256}, *q, at::kByte), lse;
   if (with_lse) lse = fresh({T, heads}, *q, at::kFloat);
   const awq_status st = run<decltype(awq_kv4_attention)>(
-      arg[0], q->data_ptr(), code, q->stride(0), q->stride(1), T, heads, start ? (const int32_t*)start->data_ptr() : nullptr,
+      arg[0], q->data_ptr(), code, pitch(q, 0), pitch(q, 1), T, heads, start ? (const int32_t*)start->data_ptr() : nullptr,
       max_q, cache->data_ptr(), cache->size(0), (const int32_t*)table->data_ptr(), table->size(1),
       (const int32_t*)lens->data_ptr(), batch, (float)scale, &cfg, out.data_ptr(),
       with_lse ? (float*)lse.data_ptr() : nullptr, ws.data_ptr(), (size_t)ws.numel(), here.stream());
