@@ -16,7 +16,8 @@
  *   - Groups are g consecutive input channels within one row of W.
  *   - Every pointer argument is DEVICE memory owned by the caller, unless the
  *     comment says "host". The library allocates no device memory and keeps
- *     no state of its own beyond what awq_act_stats_noalloc documents;
+ *     no state of its own beyond what awq_act_stats_noalloc and
+ *     awq_device_error document;
  *     scratch memory is the caller's workspace.
  *   - Calls are asynchronous and ordered on `stream` (a cudaStream_t; NULL is
  *     the legacy default stream). A returned AWQ_OK means the work was
@@ -411,13 +412,23 @@ awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const int32_t* slo
  * Tokens in pages outside [0, n_pages) are left out, lengths are cut to
  * table_pages * page_size, and rows to max_q and T; any of these makes
  * awq_workspace_error report AWQ_ERR_DEVICE.
- * ws: awq_kv4_attention_workspace_size bytes. Asynchronous. */
+ * ws: awq_kv4_attention_workspace_size bytes, for one call at a time; a call
+ * captured into a graph keeps it for as long as the graph is replayed.
+ * Asynchronous. */
 size_t awq_kv4_attention_workspace_size(int64_t batch, int64_t n_q_heads, int64_t max_q, const awq_kv4cfg* cfg);
 awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t q_tok_stride, int64_t q_head_stride, int64_t T,
                              int64_t n_q_heads, const int32_t* q_start, int64_t max_q, const void* cache,
                              int64_t n_pages, const int32_t* table, int64_t table_pages, const int32_t* lens,
                              int64_t batch, float scale, const awq_kv4cfg* cfg, void* out, float* lse, void* ws,
                              size_t ws_bytes, awq_stream_t stream);
+
+/* Errors that the device found in awq_w8a8_gemm and awq_kv4_attention, whatever
+ * workspaces the calls had: each records the first one in a word of the device
+ * besides its own workspace, where the next call with that workspace clears it.
+ * Reads and clears that word of the current device, synchronising `stream`
+ * (calls on other streams count once they have ended): AWQ_OK or
+ * AWQ_ERR_DEVICE. */
+awq_status awq_device_error(awq_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * The search, one step at a time (awq_search_scales is exactly these calls

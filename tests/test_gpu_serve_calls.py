@@ -10,6 +10,14 @@ if not torch.cuda.is_available():  # pragma: no cover
 import weight_only_int4_act_b200 as awq  # noqa: E402
 
 
+@pytest.fixture(autouse=True)
+def _no_error_from_before():
+    try:
+        awq.device_error()
+    except awq.AwqError:
+        pass
+
+
 def test_tensors_without_storage_are_refused():
     """Inside torch.func's transforms a tensor is a plain torch.Tensor of the right device and type whose data_ptr() throws:
     a RuntimeError for every call, and the interpreter and the library go on."""
@@ -49,3 +57,58 @@ def test_strides_of_axes_of_one():
     assert torch.equal(awq.kv4_attention(odd[2], one, table, lens, cfg), want) and want.any()
     assert torch.equal(awq.kv4_attention(odd[2], one, table, lens, cfg, out=out), want)  # (the long way)
     assert torch.equal(awq.quantize_int8(odd[0][0])[0], awq.quantize_int8(k[0])[0])
+
+
+def _attention(new, context=40):
+    """Arguments of an attention call of `new` rows in each of 5 sequences, whose tables are good."""
+    cfg = awq.make_kv4(8, 64, 16)
+    cache = awq.kv4_new_cache(5 * context // 16 + 5, cfg)
+    pages = -(-context // 16)
+    table = torch.arange(5 * pages, dtype=torch.int32, device="cuda").view(5, pages)
+    lens = torch.full((5,), context, dtype=torch.int32, device="cuda")
+    q = torch.ones((5 * new, 16, 64), dtype=torch.bfloat16, device="cuda")
+    start = torch.arange(6, dtype=torch.int32, device="cuda") * new
+    return q, cache, table, lens, cfg, dict(q_start=start, max_q=new)
+
+
+@pytest.mark.parametrize("new,context", [(1, 40), (1, 4000), (90, 200)])
+def test_device_errors_are_kept(new, context):
+    """Calls without a workspace of their own: what the device finds is told by device_error(), once; short contexts, split
+    ones, prompts; a page outside the cache, a length past the table, rows past max_q, and a replayed graph."""
+    q, cache, table, lens, cfg, args = _attention(new, context)
+    good = awq.kv4_attention(q, cache, table, lens, cfg, **args)
+    awq.device_error()
+    bad_page, bad_len = table.clone(), lens.clone()
+    bad_page[3, 1] = cache.shape[0]
+    bad_len[4] = table.shape[1] * 16 + 1
+    short = dict(args, max_q=new - 1) if new > 1 else dict(args, q_start=args["q_start"] + 1)
+    for a in ((bad_page, lens, args), (table, bad_len, args), (table, lens, short)):
+        awq.kv4_attention(q, cache, a[0], a[1], cfg, **a[2])
+        assert torch.equal(awq.kv4_attention(q, cache, table, lens, cfg, **args), good)  # (does not clear it)
+        with pytest.raises(awq.AwqError, match="DEVICE"):
+            awq.device_error()
+        awq.device_error()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = awq.kv4_attention(q, cache, table, lens, cfg, **args)
+    g.replay()
+    awq.device_error()
+    table.copy_(bad_page)
+    g.replay()
+    with pytest.raises(awq.AwqError, match="DEVICE"):
+        awq.device_error()
+    assert torch.isfinite(out).all()
+
+
+def test_workspaces_still_tell_of_their_own_call():
+    q, cache, table, lens, cfg, args = _attention(1)
+    works = [awq.workspace(awq.kv4_attention_workspace_size(5, 16, 1, cfg)) for _ in range(2)]
+    bad = table.clone()
+    bad[0, 0] = -1
+    awq.kv4_attention(q, cache, bad, lens, cfg, ws=works[0], **args)
+    awq.kv4_attention(q, cache, table, lens, cfg, ws=works[1], **args)
+    awq.workspace_error(works[1])
+    for check in (lambda: awq.workspace_error(works[0]), awq.device_error):
+        with pytest.raises(awq.AwqError, match="DEVICE"):
+            check()
+        check()

@@ -6,6 +6,6 @@ from .binding import (  # noqa: F401
     fold_inv_scales, w4a16_workspace_size, w4a16_gemm, pack_workspace_size, selftest_bounded_wait,
     select_library, bounds_checks_enabled, bounds_error, selftest_bounds, AWQ_ERR_BOUNDS,
     quantize_int8, w8a8_workspace_size, w8a8_gemm, Kv4Cfg, make_kv4, kv4_page_bytes, kv4_new_cache, kv4_append,
-    kv4_gather, kv4_attention_workspace_size, kv4_attention,
+    kv4_gather, kv4_attention_workspace_size, kv4_attention, device_error,
     stats_workspace_size, search_workspace_size, search_form, workspace, debug_dw, step, status_str,
 )

@@ -40,7 +40,7 @@ EXPORTED = (
     "awq_pack_workspace_size", "awq_quantize_pack_ws", "awq_selftest_bounded_wait",
     "awq_bounds_checks_enabled", "awq_bounds_error", "awq_selftest_bounds",
     "awq_quantize_int8", "awq_w8a8_workspace_size", "awq_w8a8_gemm", "awq_kv4_page_bytes", "awq_kv4_append",
-    "awq_kv4_gather", "awq_kv4_attention_workspace_size", "awq_kv4_attention",
+    "awq_kv4_gather", "awq_kv4_attention_workspace_size", "awq_kv4_attention", "awq_device_error",
 )
 
 
@@ -155,6 +155,7 @@ def lib() -> ctypes.CDLL:
         sig |= {
             "awq_quantize_int8": (c_int32, [c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int64, c_int64, c_void_p,
                                             c_void_p, c_void_p]),
+            "awq_device_error": (c_int32, [c_void_p]),
             "awq_w8a8_workspace_size": (c_size_t, [c_int64, c_int64, c_int64]),
             "awq_w8a8_gemm": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64,
                                         c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
@@ -531,7 +532,8 @@ def _calls(variant):
 
 @functools.lru_cache(maxsize=None)
 def _unread(dev):
-    """An error word for calls that have no workspace of their own, where the workspace is nothing else: nobody reads it."""
+    """An error word for calls that have no workspace of their own, where the workspace is nothing else: device_error()
+    tells what goes wrong in them."""
     return _torch().empty(1024, dtype=_torch().uint8, device=f"cuda:{dev}")
 
 
@@ -578,7 +580,9 @@ def w8a8_workspace_size(N, d_out, d_in) -> int:
 def w8a8_gemm(xq, x_step, wq, w_step, dtype=None, bias=None, ws=None, out=None):
     """Y [N, d_out] (dtype bf16 by default, or fp16) = (xq wq^T) * x_step[:, None]
     * w_step (+ bias, float32 [d_out]), the integer sum exact; xq int8 [N, d_in]
-    and wq int8 [d_out, d_in] with their steps from quantize_int8."""
+    and wq int8 [d_out, d_in] with their steps from quantize_int8. What the device
+    finds wrong is in device_error(), and in workspace_error(ws) for a call with
+    a workspace of its own."""
     torch = _torch()
     if out is None and ws is None and dtype in (None, torch.bfloat16, torch.float16):
         r = _calls(_active).w8a8_gemm(xq, x_step, wq, w_step, bias, dtype is torch.float16,
@@ -713,7 +717,11 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
     max_q at least the longest; default: one row a sequence), the last tokens of
     that context. scale: default 1 / sqrt(head_dim). Returns out [T, n_q_heads,
     head_dim], or (out, lse float32 [T, n_q_heads]) with lse=True. Rows of no
-    sequence are left as they were (unset in a fresh output)."""
+    sequence are left as they were (unset in a fresh output). Pages outside the
+    cache, lengths past the table and rows past max_q are left out without an
+    exception: device_error() tells of them, and workspace_error(ws) for a call
+    with a workspace of its own. A workspace given serves one call at a time, and
+    one given to a captured call must live as long as its graph."""
     torch = _torch()
     if ws is None and out is None and cfg.__class__ is Kv4Cfg:
         r = _calls(_active).kv4_attention(q, cache, table, lens, ctypes.addressof(cfg), q_start, max_q, scale, bool(lse))
@@ -747,10 +755,10 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
     else:
         _same_device(ws, dev, "ws")
     st = lib().awq_kv4_attention(q.data_ptr(), dt, _pitch(q, 0), _pitch(q, 1), T, n_q_heads,
-                                 None if q_start is None else q_start.data_ptr(), max_q, cache.data_ptr(), cache.shape[0], table.data_ptr(), table.shape[1],
-                                 lens.data_ptr(), batch, D ** -0.5 if scale is None else float(scale),
-                                 ctypes.byref(cfg), out.data_ptr(), lse_t.data_ptr() if lse else None, ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), stream)
+                                 None if q_start is None else q_start.data_ptr(), max_q, cache.data_ptr(),
+                                 cache.shape[0], table.data_ptr(), table.shape[1], lens.data_ptr(), batch,
+                                 D ** -0.5 if scale is None else float(scale), ctypes.byref(cfg), out.data_ptr(),
+                                 lse_t.data_ptr() if lse else None, ws.data_ptr(), ws.numel() * ws.element_size(), stream)
     _check(st, "awq_kv4_attention")
     return (out, lse_t) if lse else out
 
@@ -778,6 +786,13 @@ def bounds_error():
 def selftest_bounds(ws):
     """Launch the index checks' failure path (see include/awq.h)."""
     _check(lib().awq_selftest_bounds(_ptr(ws), ws.numel() * ws.element_size(), _stream()), "awq_selftest_bounds")
+
+
+def device_error():
+    """Raise AwqError if the device found something wrong in w8a8_gemm or kv4_attention (a page outside the cache, a length
+    past the table, rows past max_q, a wait that gave up) since the last time this was called for the current device;
+    waits for the current stream. One error is kept, whichever call it came from."""
+    _check(lib().awq_device_error(_stream()), "device")
 
 
 def workspace_error(ws):

@@ -174,7 +174,11 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
   wait_for_kernel_before();
   const Kv4Seq seq = kv4_seq(a, b);
   const int rows = seq.n * a.share;
-  if (threadIdx.x == 0 && seq.bad) atomicMax(a.err, ERR_KV4_PAGE);
+  auto bad_page = [&]() {
+    atomicMax(a.err, ERR_KV4_PAGE);
+    keep_device_error(ERR_KV4_PAGE);
+  };
+  if (threadIdx.x == 0 && seq.bad) bad_page();
   // the longest tiles first
   const int n_tiles = (rows + KVP_ROWS - 1) / KVP_ROWS, tile = n_tiles - 1 - (int)blockIdx.x;
   if (rows <= KVP_MIN_ROWS || tile < 0) return;
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __g
       const bool in = lane < 4 && t0 < seq.L;
       const int page = in && p < a.table_pages ? __ldg(a.table + (long long)b * a.table_pages + p) : -1;
       bool good = in && page >= 0 && page < a.c.n_pages;
-      if (in && !good) atomicMax(a.err, ERR_KV4_PAGE);
+      if (in && !good) bad_page();
       if (good && lane % per == 0) {
         // (a run's later strips lie in the same page: inside the cache too)
         const long long off = a.c.strip(page, head, t0 & ((1 << a.c.page_shift) - 1));

@@ -1343,6 +1343,7 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
       }
       bad = __reduce_max_sync(0xffffffffu, bad);
       if (lane == 0 && (s.clear_err || bad)) *a.err = bad;
+      if (lane == 0 && bad) keep_device_error(bad);
     }
   } else {
     __syncthreads();
@@ -1363,6 +1364,7 @@ __global__ void __launch_bounds__(32 * (kv4_warps(D, G, NT) + 1), 1)
         // a copy that never came (the wait took two seconds): report, write nothing
         if (lane == 0) {
           sm.bad = ERR_KV4_COPY;
+          keep_device_error(ERR_KV4_COPY);
           if (s.solo) *a.err = ERR_KV4_COPY;
         }
         break;
@@ -1487,6 +1489,7 @@ __global__ void __launch_bounds__(32 * KV4_JOIN_WARPS) kv4_attention_join(const 
     for (int i = lane; i < ctas; i += 32) bad = max(bad, s.cta_bad[i]);
     bad = __reduce_max_sync(0xffffffffu, bad);
     if (lane == 0 && (s.clear_err || bad)) *a.err = bad;
+    if (lane == 0 && bad) keep_device_error(bad);
   }
   const long long seg = s.cta_seg[2 * c + 1];
   int n = 1;

@@ -281,6 +281,20 @@ extern "C" awq_status awq_quantize_int8(const void* x, awq_dtype dtype, int64_t 
   return dtype == AWQ_DTYPE_F16 ? modes(std::true_type{}) : modes(std::false_type{});
 }
 
+extern "C" awq_status awq_device_error(awq_stream_t stream) {
+  cudaStream_t cs = as_stream(stream);
+  int word = 0;
+  if (cudaMemcpyFromSymbolAsync(&word, g_device_err, sizeof(int), 0, cudaMemcpyDeviceToHost, cs) != cudaSuccess ||
+      cudaStreamSynchronize(cs) != cudaSuccess)
+    return AWQ_ERR_CUDA;
+  if (word == 0) return AWQ_OK;
+  const int zero = 0;
+  if (cudaMemcpyToSymbolAsync(g_device_err, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, cs) != cudaSuccess ||
+      cudaStreamSynchronize(cs) != cudaSuccess)
+    return AWQ_ERR_CUDA;
+  return AWQ_ERR_DEVICE;
+}
+
 extern "C" size_t awq_w8a8_workspace_size(int64_t N, int64_t d_out, int64_t d_in) {
   if (check_w8(N, d_out, d_in) != AWQ_OK) return 0;
   return kAlign;

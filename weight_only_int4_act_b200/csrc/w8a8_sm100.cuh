@@ -185,6 +185,12 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+// What a serving kernel finds wrong goes to its call's workspace and, as many
+// calls leave theirs to be forgotten, to one word of the device as well: the
+// first code since awq_device_error() last read it.
+__device__ int g_device_err;
+__device__ __forceinline__ void keep_device_error(int code) { atomicCAS(&g_device_err, 0, code); }
+
 // mbar_wait for handshakes on the critical path: try_wait itself sleeps in
 // hardware for a while, and the clock, whose read costs about a microsecond, is
 // looked at only after many tries. Same bound and same effects when it gives up.
@@ -201,7 +207,10 @@ __device__ __forceinline__ bool mbar_wait_lean(uint32_t bar, uint32_t parity, vo
       if (t0 == 0) t0 = t;
       if (t - t0 > AWQ_WAIT_LIMIT_NS) {
         *abort_flag = 1;
-        if (err) atomicCAS(err, 0, code);
+        if (err) {
+          atomicCAS(err, 0, code);
+          keep_device_error(code);
+        }
         return false;
       }
     }
