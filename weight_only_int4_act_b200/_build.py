@@ -3,14 +3,17 @@
 Two builds of the same sources: "release" (lib/libawq_b200.so) and "check"
 (lib/libawq_b200_check.so, compiled with -DAWQ_BOUNDS_CHECK: every hand-
 addressed global access checks its index and records a failure in a device
-word instead of touching memory; see csrc/check.cuh). Beside them, by g++,
-lib/awq_calls.so: the Python module of csrc/torch_calls.cpp, which holds no
-kernels and calls whichever build is selected.
+word instead of touching memory; see csrc/check.cuh). They need nvcc alone.
+Beside them, by g++ against the headers of the installed torch, whose version
+is in the name: lib/awq_calls.<python>.torch-<version>.so, the Python module of
+csrc/torch_calls.cpp, which holds no kernels and calls whichever build is selected.
 """
 from __future__ import annotations
 
 import os
 import subprocess
+import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,7 +29,6 @@ DEPS = SOURCES + [os.path.join(PKG, "csrc", f) for f in (
     "w4a16_sm100.cuh", "awq_api.cu", "serve_api.cuh", "w8a8_sm100.cuh", "kv4_sm100.cuh",
     "kv4_prompt_sm100.cuh")] + [os.path.join(ROOT, "include", "awq.h")]
 
-CALLS_PATH = os.path.join(LIB_DIR, "awq_calls.so")
 CALLS_DEPS = [os.path.join(PKG, "csrc", "torch_calls.cpp"), os.path.join(ROOT, "include", "awq.h")]
 
 NVCC_FLAGS = [
@@ -45,6 +47,18 @@ def lib_path(variant: str = "release") -> str:
     return os.path.join(LIB_DIR, VARIANTS[variant][0])
 
 
+def torch_version() -> str:
+    import importlib.metadata
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return "none"
+
+
+def calls_path() -> str:
+    return os.path.join(LIB_DIR, f"awq_calls.{sys.implementation.cache_tag}.torch-{torch_version()}.so")
+
+
 def stale(variant: str = "release") -> bool:
     return _older(lib_path(variant), DEPS)
 
@@ -61,6 +75,8 @@ def calls_command(out: str) -> list:
 
     import torch
     base = os.path.dirname(torch.__file__)
+    if torch.version.cuda is None:
+        raise ImportError("torch was built without CUDA")
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     include = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
                os.path.join(base, "include", "torch", "csrc", "api", "include"), cuda]
@@ -72,7 +88,8 @@ def calls_command(out: str) -> list:
 
 def build(force: bool = False, verbose: bool = False, variants=("release",)) -> str:
     """Build the given variants and the calls' module if missing or older than
-    their sources (the compilers run for all of them at once). Returns the path of the first."""
+    their sources (the compilers run for all of them at once). Returns the path
+    of the first. Without a CUDA build of torch there is no calls' module."""
     os.makedirs(LIB_DIR, exist_ok=True)
     jobs = []
 
@@ -83,8 +100,11 @@ def build(force: bool = False, verbose: bool = False, variants=("release",)) -> 
     for v in variants:
         if force or stale(v):
             start(lib_path(v), lambda out, v=v: [nvcc(), *NVCC_FLAGS, *VARIANTS[v][1], "-o", out, *SOURCES])
-    if force or _older(CALLS_PATH, CALLS_DEPS):
-        start(CALLS_PATH, calls_command)
+    if force or _older(calls_path(), CALLS_DEPS):
+        try:
+            start(calls_path(), calls_command)
+        except ImportError as e:
+            warnings.warn(f"the Python calls' module is not built: {e}")
     failed = []
     for path, cmd, proc in jobs:
         out, _ = proc.communicate()

@@ -16,7 +16,7 @@ import functools
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
 
-from ._build import CALLS_PATH, VARIANTS, lib_path
+from ._build import VARIANTS, calls_path, lib_path
 
 AWQ_OK = 0
 STATUS_NAMES = {
@@ -509,16 +509,17 @@ def _scratch(like, nbytes):
 
 @functools.lru_cache(maxsize=None)
 def _calls(variant):
-    """The serving calls of lib/awq_calls.so on a build of the library. Each
+    """The serving calls of csrc/torch_calls.cpp on a build of the library. Each
     returns its results, a status, or None for arguments that the functions
     below have to look at."""
     import importlib.machinery
     import importlib.util
     import types
     _torch()  # whose libraries the module needs
-    if not os.path.exists(CALLS_PATH):
-        raise RuntimeError(f"{CALLS_PATH} is missing; build it with __graft_entry__.build()")
-    loader = importlib.machinery.ExtensionFileLoader("awq_calls", CALLS_PATH)
+    path = calls_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing; build it with __graft_entry__.build()")
+    loader = importlib.machinery.ExtensionFileLoader("awq_calls", path)
     m = importlib.util.module_from_spec(importlib.util.spec_from_loader("awq_calls", loader))
     loader.exec_module(m)
     L = lib()
