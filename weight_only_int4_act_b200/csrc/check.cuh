@@ -49,7 +49,7 @@ enum BoundsSite : int {
   BS_GRAM_FIX,      // gram_tail_fixup: partial pieces and G'
   BS_FOLD_S,        // fold_inv_scales_kernel: s
   BS_FOLD_P,        // fold_inv_scales_kernel: the folded tensor
-  BS_Q8_IN,         // quantize_int8_rows: input rows
+  BS_Q8_IN,         // quantize_int8_rows / _long: input rows
   BS_Q8_CODES,      // quantize_int8_rows / _long: codes
   BS_Q8_STEP,       // quantize_int8_rows / _long: steps
   BS_W8_Y,          // the 8-bit integer product: Y stores

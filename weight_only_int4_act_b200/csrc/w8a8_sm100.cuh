@@ -162,12 +162,16 @@ __global__ void __launch_bounds__(1024)
   const int n8 = d_in / 8;
   int turn = 0;
   for (long long r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
-    const uint4* row = reinterpret_cast<const uint4*>(x + r * ldx);
+    auto load = [&](int c) {
+      return AWQ_SPAN_OK(r * ldx + 8 * c, 8, (rows - 1) * ldx + d_in, BS_Q8_IN)
+                 ? __ldg(reinterpret_cast<const uint4*>(x + r * ldx) + c)
+                 : make_uint4(0, 0, 0, 0);
+    };
     uint32_t top = 0;
     for (int c = threadIdx.x; c < n8; c += blockDim.x) {
       float f[8], v[8];
       q8_factors<MODE>(s, c, f);
-      q8_values<F16, MODE>(__ldg(row + c), f, v);
+      q8_values<F16, MODE>(load(c), f, v);
       top = q8_top(v, top);
     }
     top = q8_block_max(top, red[turn]);
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(1024)
     for (int c = threadIdx.x; c < n8; c += blockDim.x) {
       float f[8], v[8];
       q8_factors<MODE>(s, c, f);
-      q8_values<F16, MODE>(__ldg(row + c), f, v);
+      q8_values<F16, MODE>(load(c), f, v);
       if (AWQ_SPAN_OK(r * d_in + 8 * c, 8, rows * d_in, BS_Q8_CODES))
         *reinterpret_cast<uint2*>(q + r * d_in + 8 * c) = q8_codes(v, inv, finite);
     }
