@@ -60,11 +60,6 @@ constexpr float KVP_HEAD = 4.0f, KVP_LAG = 15.0f;
 constexpr int ERR_KVP_RAW = 0x601, ERR_KVP_FREE = 0x602, ERR_KVP_SCORE = 0x603, ERR_KVP_WEIGHT = 0x604, ERR_KVP_OUT = 0x605,
               ERR_KVP_TILE = 0x606;
 
-struct KvpArgs {
-  Kv4AttnArgs a;
-  int tiles;  // row tiles of the longest sequence: gridDim.x
-};
-
 // What the softmax knows of a strip: its keys are (code - zero) step / key, its
 // values (code - zero) step 2^(10 - e), down = 2^-e. odd: tokens (by bit) that hold
 // NaN, and bit 16 where each token has an e of its own (KvpSmem::e).
@@ -162,13 +157,12 @@ __device__ __forceinline__ KvpPairs kvp_unpack(uint32_t w, __half2 z0, __half2 z
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 template <int D, int G, bool EXACT>
-__global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __grid_constant__ KvpArgs args) {
+__global__ void __launch_bounds__(KVP_THREADS, 1) kv4_attention_prompt(const __grid_constant__ Kv4AttnArgs a) {
   using Sm = KvpSmem<D, G>;
   constexpr int NJ = D / 32, NG = D / G, STRIP = Sm::STRIP;
   static_assert(!EXACT || NG == 1, "one step a token");
   extern __shared__ uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-  const Kv4AttnArgs& a = args.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.y, b = blockIdx.z;
   wait_for_kernel_before();

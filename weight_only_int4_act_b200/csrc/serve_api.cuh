@@ -467,8 +467,6 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
     if (st != AWQ_OK) return st;
   }
   if (!prompt) return AWQ_OK;
-  KvpArgs pa{};
-  pa.a = a;
   const dim3 grid((unsigned)cdiv(max_q * a.share, KVP_ROWS), (unsigned)cfg->n_kv_heads, (unsigned)batch);
   return kv4_shapes(cfg->head_dim, cfg->group, [&](auto d, auto g) -> awq_status {
     constexpr int D = decltype(d)::value, G = decltype(g)::value;
@@ -477,7 +475,7 @@ extern "C" awq_status awq_kv4_attention(const void* q, awq_dtype dtype, int64_t 
       static_assert(smem <= 232448, "shared memory of the prompt attention");
       auto launch = [&](auto k, std::atomic<unsigned long long>& once) -> awq_status {
         if (!kernel_smem(k, smem, once)) return AWQ_ERR_CUDA;
-        return launch_behind(k, grid, dim3(KVP_THREADS), smem, cs, 0, pa);
+        return launch_behind(k, grid, dim3(KVP_THREADS), smem, cs, 0, a);
       };
       static std::atomic<unsigned long long> once[2];
       if constexpr (D == G)
