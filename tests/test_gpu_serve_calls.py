@@ -112,3 +112,30 @@ def test_workspaces_still_tell_of_their_own_call():
         with pytest.raises(awq.AwqError, match="DEVICE"):
             check()
         check()
+
+
+def test_no_rows_is_no_work():
+    """A step without tokens: empty results from every call, with and without outputs of the caller's; shapes that the
+    library does not take are refused all the same."""
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    s = torch.ones(64, device="cuda")
+    for args in (dict(), dict(s=s), dict(s=s, inverse=True)):
+        q, step = awq.quantize_int8(x, **args)
+        assert q.shape == (0, 64) and q.dtype == torch.int8 and step.shape == (0,)
+    assert awq.quantize_int8(x, outputs=(q, step))[0] is q
+    w = awq.quantize_int8(torch.ones((48, 64), dtype=torch.bfloat16, device="cuda"))
+    y = awq.w8a8_gemm(q, step, *w, dtype=torch.float16)
+    assert y.shape == (0, 48) and y.dtype == torch.float16 and awq.w8a8_gemm(q, step, *w, out=y) is y
+    with pytest.raises(awq.AwqError):
+        awq.quantize_int8(torch.empty((0, 24), dtype=torch.bfloat16, device="cuda"))
+    cfg = awq.make_kv4(2, 64, 16)
+    cache = awq.kv4_new_cache(2, cfg)
+    none = torch.empty((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for batch, args in ((0, dict()), (0, dict(q_start=torch.zeros(1, **i32), max_q=1)), (3, dict(q_start=torch.zeros(4, **i32), max_q=5))):
+        table, lens = torch.zeros((batch, 2), **i32), torch.zeros(batch, **i32)
+        out, lse = awq.kv4_attention(none, cache, table, lens, cfg, lse=True, **args)
+        assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+        assert awq.kv4_attention(none, cache, table, lens, cfg, out=out, **args) is out
+    with pytest.raises(awq.AwqError):
+        awq.kv4_attention(none[:, :3], cache, table, lens, cfg, **args)  # 3 heads over 2

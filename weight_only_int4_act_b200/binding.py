@@ -542,9 +542,9 @@ def _unread(dev):
 def quantize_int8(X, s=None, inverse=False, outputs=None):
     """Codes int8 [rows, d_in] and steps float32 [rows] of the symmetric 8-bit
     quantiser, one step per row, of X (bf16 or fp16 [rows, d_in]; rows may be
-    strided). s (float32 [d_in]): the channels are multiplied by it first (a
-    weight: W S) or, with inverse=True, by 1 / s (activations: X S^-1); without
-    it X is taken as it is."""
+    strided, and none is no work). s (float32 [d_in]): the channels are
+    multiplied by it first (a weight: W S) or, with inverse=True, by 1 / s
+    (activations: X S^-1); without it X is taken as it is."""
     if outputs is None:
         r = _calls(_active).quantize_int8(X, s, 2 if inverse else 1)
         if r.__class__ is tuple:
@@ -566,6 +566,8 @@ def quantize_int8(X, s=None, inverse=False, outputs=None):
         q, step = outputs
         _req_here(q, torch.int8, (rows, d_in), dev, "q")
         _req_here(step, torch.float32, (rows,), dev, "step")
+    if rows == 0 and w8a8_workspace_size(1, 1, d_in):  # (a d_in that the library takes)
+        return q, step
     st = lib().awq_quantize_int8(X.data_ptr(), dt, X.stride(0) if rows > 1 else max(d_in, 8),
                                  None if s is None else s.data_ptr(), mode, rows, d_in, q.data_ptr(), step.data_ptr(),
                                  stream)
@@ -581,7 +583,7 @@ def w8a8_workspace_size(N, d_out, d_in) -> int:
 def w8a8_gemm(xq, x_step, wq, w_step, dtype=None, bias=None, ws=None, out=None):
     """Y [N, d_out] (dtype bf16 by default, or fp16) = (xq wq^T) * x_step[:, None]
     * w_step (+ bias, float32 [d_out]), the integer sum exact; xq int8 [N, d_in]
-    and wq int8 [d_out, d_in] with their steps from quantize_int8. What the device
+    (no tokens: no work) and wq int8 [d_out, d_in] with their steps from quantize_int8. What the device
     finds wrong is in device_error(), and in workspace_error(ws) for a call with
     a workspace of its own."""
     torch = _torch()
@@ -612,6 +614,8 @@ def w8a8_gemm(xq, x_step, wq, w_step, dtype=None, bias=None, ws=None, out=None):
         ws = _unread(dev)
     else:
         _same_device(ws, dev, "ws")
+    if N == 0 and w8a8_workspace_size(1, d_out, d_in):
+        return out
     st = lib().awq_w8a8_gemm(xq.data_ptr(), x_step.data_ptr(), wq.data_ptr(), w_step.data_ptr(),
                              None if bias is None else bias.data_ptr(), dt, N, d_out, d_in, out.data_ptr(),
                              ws.data_ptr(), ws.numel() * ws.element_size(), stream)
@@ -717,7 +721,8 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
     queries the rows q_start[b] .. q_start[b+1] - 1 (int32 [batch + 1], with
     max_q at least the longest; default: one row a sequence), the last tokens of
     that context. scale: default 1 / sqrt(head_dim). Returns out [T, n_q_heads,
-    head_dim], or (out, lse float32 [T, n_q_heads]) with lse=True. Rows of no
+    head_dim], or (out, lse float32 [T, n_q_heads]) with lse=True (no rows: no
+    work). Rows of no
     sequence are left as they were (unset in a fresh output). Pages outside the
     cache, lengths past the table and rows past max_q are left out without an
     exception: device_error() tells of them, and workspace_error(ws) for a call
@@ -751,6 +756,8 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
     else:
         _req_here(out, q.dtype, (T, n_q_heads, D), dev, "out")
     lse_t = q.new_empty((T, n_q_heads), dtype=torch.float32) if lse else None
+    if T == 0 and kv4_attention_workspace_size(max(batch, 1), n_q_heads, max_q, cfg):
+        return (out, lse_t) if lse else out
     if ws is None:
         ws = _scratch(q, kv4_attention_workspace_size(batch, n_q_heads, max_q, cfg))
     else:

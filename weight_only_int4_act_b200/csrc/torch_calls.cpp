@@ -96,6 +96,7 @@ PyObject* quantize_int8(PyObject* const* arg) {
   awq_dtype code;
   if (!rows(X, 2, code)) return none();
   const int64_t n = X->size(0), d = X->size(1);
+  if (n == 0) return none();
   if (arg[2] != Py_None && !(is(s, at::kFloat, 1) && s->size(0) == d)) return none();
   const auto mode = s ? (awq_scale_mode)PyLong_AsLong(arg[3]) : AWQ_SCALE_NONE;
   at::Tensor q = fresh({n, d}, *X, at::kChar), step = fresh({n}, *X, at::kFloat);
@@ -114,7 +115,7 @@ PyObject* w8a8_gemm(PyObject* const* arg) {
   if (!is(x, at::kChar, 2) || !is(w, at::kChar, 2) || !is(dx, at::kFloat, 1) || !is(dw, at::kFloat, 1) || !is(ws, at::kByte, 1))
     return none();
   const int64_t n = x->size(0), d_in = x->size(1), d_out = w->size(0);
-  if (w->size(1) != d_in || dx->size(0) != n || dw->size(0) != d_out) return none();
+  if (n == 0 || w->size(1) != d_in || dx->size(0) != n || dw->size(0) != d_out) return none();
   if (arg[5] != Py_None && !(is(bias, at::kFloat, 1) && bias->size(0) == d_out)) return none();
   const bool f16 = arg[6] == Py_True;
   at::Tensor y = fresh({n, d_out}, *x, f16 ? at::kHalf : at::kBFloat16);
@@ -169,7 +170,7 @@ PyObject* kv4_attention(PyObject* const* arg) {
   if (!rows(q, 3, code) || q->size(2) != cfg.head_dim || !cache_of(cache, cfg) || !is(lens, at::kInt, 1) || !is(table, at::kInt, 2))
     return none();
   const int64_t T = q->size(0), heads = q->size(1), D = q->size(2), batch = lens->size(0);
-  if (table->size(0) != batch) return none();
+  if (T == 0 || table->size(0) != batch) return none();
   if (arg[7] == Py_None ? T != batch : !(is(start, at::kInt, 1) && start->size(0) == batch + 1 && arg[8] != Py_None))
     return none();
   if ((arg[8] != Py_None && !PyLong_CheckExact(arg[8])) || (arg[9] != Py_None && !PyFloat_CheckExact(arg[9]))) return none();
