@@ -400,18 +400,25 @@ awq_status awq_kv4_gather(const void* cache, int64_t n_pages, const int32_t* slo
  * head_dim] contiguous in q's type, 16-byte aligned; lse: DEVICE float
  * [T, n_q_heads] or NULL: the natural logarithm of the sum of exponentials.
  * max_q: at least every sequence's number of rows (host value; it chooses the
- * kernel). Scores, softmax statistics and output sums are fp32; the weights
- * (probability times value step) enter the tensor cores in fp16, and for bf16
- * queries of more than 64 rows a sequence (tokens times query heads of a kv
- * head) the keys and values (code - zero) * step do too, each rounded once (by
- * half an fp16 step of itself, or 2^-35 of the largest step among 16 tokens
- * where that is more); for fp16 ones the values alone. A row
+ * kernel). Sequences of more than 64 rows (tokens times query heads of a kv
+ * head) go to a kernel that reads the context once for 256 of them, where
+ * head_dim <= 128, q is bf16 or group = head_dim, and batch * n_kv_heads *
+ * ceil(max_q * n_q_heads / n_kv_heads / 256) >= 40; all others to one that reads
+ * it once for 8 or 16, which suits few rows (2 x 2048 queries of up to 8000
+ * tokens, 32 heads over 8 of 128: 0.45 ms with the one, and in fp16 with several
+ * groups a head 2.4 to 2.9 ms with the other).
+ * Scores, softmax statistics and output sums are fp32. The weights (probability
+ * times value step) enter the tensor cores in fp16, off by 2^-11 of themselves
+ * or by 2^-25 where a row's largest is 1 or more; for bf16 queries in the kernel
+ * for 256 rows the keys and values (code - zero) * step do too, each rounded
+ * once (by 2^-11 of itself, or 2^-35 of the largest step among 16 tokens where
+ * that is more); for fp16 ones the values alone. A row
  * that sees a key with step NaN is NaN, one that sees a value with step NaN is
  * NaN in that group's channels at least. The same call gives the same bits
  * each time; another batch around a sequence may cut its context elsewhere.
  * Tokens in pages outside [0, n_pages) are left out, lengths are cut to
  * table_pages * page_size, and rows to max_q and T; any of these makes
- * awq_workspace_error report AWQ_ERR_DEVICE.
+ * awq_workspace_error and awq_device_error report AWQ_ERR_DEVICE.
  * ws: awq_kv4_attention_workspace_size bytes, for one call at a time; a call
  * captured into a graph keeps it for as long as the graph is replayed.
  * Asynchronous. */

@@ -722,7 +722,9 @@ def kv4_attention(q, cache, table, lens, cfg: Kv4Cfg, q_start=None, max_q=None, 
     max_q at least the longest; default: one row a sequence), the last tokens of
     that context. scale: default 1 / sqrt(head_dim). Returns out [T, n_q_heads,
     head_dim], or (out, lse float32 [T, n_q_heads]) with lse=True (no rows: no
-    work). Rows of no
+    work). Many rows a sequence (more than 64 tokens times query heads of a kv
+    head) are fast for head_dim up to 128, in fp16 with group = head_dim, and in
+    batches that fill the GPU (include/awq.h has the rule). Rows of no
     sequence are left as they were (unset in a fresh output). Pages outside the
     cache, lengths past the table and rows past max_q are left out without an
     exception: device_error() tells of them, and workspace_error(ws) for a call

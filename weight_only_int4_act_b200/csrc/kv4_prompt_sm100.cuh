@@ -22,8 +22,8 @@
 // factor of its scores; but for fp16 queries (EXACT; one group a head), whose
 // output resolves it, the codes less zeros (-15 .. 15) are the keys, exactly, and
 // each score is multiplied by its token's step in fp32 (2 x 2048 queries of 8000
-// tokens, 32 heads over 8 of 128, bf16: 474 us that way where folded keys took 442; one
-// read of a step from shared memory a score, beside the MMAs' operands).
+// tokens, 32 heads over 8 of 128: 475 us that way in fp16, 454 with folded keys in
+// bf16 of the same run; one read of a step from shared memory a score, beside the MMAs' operands).
 // A token one of whose groups holds NaN turns the rows that see it to NaN.
 //
 // Measured: 2 x 2048 queries of up to 8000 tokens, 32 heads over 8 of 128: 451 us,
@@ -32,8 +32,7 @@
 // N = 128 does (64 to 67 cycles); beside them go the exponentials of 16384 scores
 // on 8 warps and the handshakes between loader, unpacking, products and softmax,
 // about 300 cycles each. Blocks of unequal contexts on 148 SMs and their starts
-// are the rest. With context tiles of 128 tokens, whose scores have no second
-// buffer in tensor memory, 742 us.
+// are the rest.
 //
 // Warps (15): 0 loads packed strips (cp.async.bulk), 1 and 14 issue the MMAs of
 // the two row tiles (one thread for both spent as long on its handshakes as the
